@@ -16,12 +16,14 @@ from . import _build
 
 Q8_0, Q4_0, Q4_K, IQ1_M, W8A8, Q6_K = 0, 1, 2, 3, 4, 5
 DEVERR_TIMEOUT, DEVERR_EXPERT_ID, DEVERR_DUP_EXPERT = 1, 2, 4
+DEVERR_PAGE, DEVERR_POSITION, DEVERR_LENGTH = 8, 16, 32
 
 #: every symbol include/mmq.h declares
 EXPORTS = ("mmq_status_string", "mmq_last_cuda_error", "mmq_q8_1_bytes", "mmq_weight_bytes", "mmq_w8a8_act_bytes", "mmq_quantize_q8_1",
            "mmq_gemm", "mmq_gemm_id_workspace_bytes", "mmq_gemm_id", "mmq_gemm_debug_partials",
            "mmq_gemm_debug_block_sums", "mmq_selftest_bounded_wait",
-           "mmq_read_device_errors", "mmq_gemm_id_noalloc", "mmq_q8_1_prepare")
+           "mmq_read_device_errors", "mmq_gemm_id_noalloc", "mmq_q8_1_prepare",
+           "mmq_qk_norm_rope", "mmq_kv_append", "mmq_kv_read", "mmq_attention_workspace_bytes", "mmq_attention")
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
 _lib = None
@@ -29,6 +31,27 @@ _lib = None
 
 class MMQError(RuntimeError):
     pass
+
+
+class _Heads(ctypes.Structure):                  # mmq_heads
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Rotary(ctypes.Structure):                 # mmq_rotary
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class _Cache(ctypes.Structure):                  # mmq_kv_cache
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class _Seqs(ctypes.Structure):                   # mmq_kv_seqs
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("cu_tokens", ctypes.c_void_p), ("seqs", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -75,6 +98,15 @@ def load():
     lib.mmq_gemm_id_noalloc.restype = I
     lib.mmq_read_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), P]
     lib.mmq_read_device_errors.restype = I
+    F = ctypes.c_float                           # structures are passed by address (ctypes.byref), as P
+    lib.mmq_qk_norm_rope.argtypes = [P, I, P, P, P, I, P, P, I64, I, P, P, F, P]
+    lib.mmq_kv_append.argtypes = [P, P, I64, P, P, P, P, I, P, P, P, F, P]
+    lib.mmq_kv_read.argtypes = [P, P, I64, P, P, P]
+    lib.mmq_attention_workspace_bytes.argtypes = [I64, I, I, I, I, I64, I64]
+    lib.mmq_attention_workspace_bytes.restype = SZ
+    lib.mmq_attention.argtypes = [P, I, P, P, I64, I64, I64, F, I, I64, P, P, P, SZ, P]
+    for f in (lib.mmq_qk_norm_rope, lib.mmq_kv_append, lib.mmq_kv_read, lib.mmq_attention):
+        f.restype = I
     _lib = lib
     return lib
 
@@ -238,3 +270,191 @@ def selftest_bounded_wait(device="cuda", stream=None) -> list[int]:
     res = torch.full((4,), -1, dtype=torch.int32, device=device)
     _check(load().mmq_selftest_bounded_wait(_ptr(res), _stream(stream)), "mmq_selftest_bounded_wait")
     return res.cpu().tolist()
+
+
+# ------------------------------------------------------------------------------- attention over the 8-bit cache
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class KVCache:
+    """One layer's 8-bit paged cache (mmq_kv_cache): int8 codes k, v [pages, kv_heads, page_size, head_dim] and f32
+    scales k_scale, v_scale [pages, kv_heads, page_size / block].  Holds the given tensors; nothing is copied."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim", "block", "_c", "_ref")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        if k.dtype != torch.int8 or v.dtype != torch.int8 or v.shape != k.shape:
+            raise MMQError("KVCache: k and v are int8 tensors of one shape [pages, kv_heads, page_size, head_dim]")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or v_scale.shape != k_scale.shape or \
+                k_scale.shape[:2] != k.shape[:2] or k_scale.dim() != 3 or not k_scale.shape[2] or \
+                self.page_size % k_scale.shape[2]:
+            raise MMQError("KVCache: the scales are f32 tensors [pages, kv_heads, page_size / block]")
+        self.block = self.page_size // k_scale.shape[2]
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = _Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages, self.kv_heads, self.head_dim,
+                         self.page_size, self.block)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 16, device="cuda"):
+        """A cache of unwritten pages (nothing has to be initialised)."""
+        shape = (pages, kv_heads, page_size, head_dim)
+        codes = [torch.empty(shape, dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.empty((pages, kv_heads, page_size // block), dtype=torch.float32, device=device)
+                  for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def _heads(t: torch.Tensor, what: str) -> _Heads:
+    if not t.is_cuda or t.dim() != 3 or t.dtype not in _DTYPES:
+        raise MMQError(f"{what}: expected a CUDA tensor [tokens, heads, head_dim] of f32, bf16 or f16")
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] > 1:
+        raise MMQError(f"{what}: the last dimension must be contiguous")
+    return _Heads(t.data_ptr(), _DTYPES[t.dtype], ts, hs)
+
+
+def _typed(t: torch.Tensor | None, dtype, what: str) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise MMQError(f"{what}: expected {dtype}")
+    return _ptr(t)
+
+
+def _vector(t: torch.Tensor | None, n: int, what: str) -> int | None:
+    if t is not None and t.numel() != n:
+        raise MMQError(f"{what}: expected {n} values")
+    return _typed(t, torch.float32, what)
+
+
+def _rotary(cos: torch.Tensor | None, sin: torch.Tensor | None, interleaved: bool):
+    if cos is None and sin is None:
+        return None
+    if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
+        raise MMQError("cos, sin: expected f32 tensors [positions, rot_dim / 2] of one shape")
+    r = _Rotary(_typed(cos, torch.float32, "cos"), _typed(sin, torch.float32, "sin"), cos.shape[0],
+                2 * cos.shape[1], 1 if interleaved else 0)
+    return ctypes.byref(r)
+
+
+def _seqs(page_table: torch.Tensor, kv_lens: torch.Tensor, cu_tokens: torch.Tensor | None) -> _Seqs:
+    n = kv_lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise MMQError("page_table: expected int32 [sequences, pages]")
+    if cu_tokens is not None and cu_tokens.numel() != n + 1:
+        raise MMQError("cu_tokens: expected int32 [sequences + 1]")
+    return _Seqs(_typed(page_table, torch.int32, "page_table"), page_table.shape[1],
+                 _typed(kv_lens, torch.int32, "kv_lens"), _typed(cu_tokens, torch.int32, "cu_tokens"), n)
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
+                 cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, dtype=None, stream=None):
+    """RMS norm of query and key heads [tokens, heads, head_dim] and position rotation in one pass
+    (mmq_qk_norm_rope): (q_out, k_out), of `dtype` (default: the inputs').  q_out = q works in place."""
+    x = q if q is not None else k
+    if x is None:
+        raise MMQError("qk_norm_rope: neither q nor k given")
+    T, _, D = x.shape
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise MMQError("qk_norm_rope: q and k differ in tokens or head_dim")
+    hq = hk = hqo = hko = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype or q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise MMQError("qk_norm_rope: q_out has another shape than q")
+        hq, hqo = ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(q_out, "q_out"))
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dtype or k.dtype, device=k.device)
+        elif k_out.shape != k.shape:
+            raise MMQError("qk_norm_rope: k_out has another shape than k")
+        hk, hko = ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(k_out, "k_out"))
+    if positions is not None and positions.numel() != T:
+        raise MMQError("qk_norm_rope: expected a position for each token")
+    _check(load().mmq_qk_norm_rope(hq, q.shape[1] if q is not None else 0, _vector(q_weight, D, "q_weight"), hqo,
+                                   hk, k.shape[1] if k is not None else 0, _vector(k_weight, D, "k_weight"), hko, T, D,
+                                   _typed(positions, torch.int32, "positions"), _rotary(cos, sin, interleaved), eps,
+                                   _stream(stream)), "mmq_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+              cu_tokens: torch.Tensor | None = None, cos: torch.Tensor | None = None, sin: torch.Tensor | None = None,
+              interleaved: bool = False, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+              q: torch.Tensor | None = None, q_weight: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+              q_dtype=None, stream=None):
+    """Quantize the new keys and values [tokens, kv_heads, head_dim] into the paged cache, normed and rotated on
+    the way (mmq_kv_append).  kv_lens: cached tokens of each sequence, the new ones included.  Returns q_out (the
+    queries normed and rotated in the same launch) where q is given."""
+    T, H, D = k.shape
+    if v.shape != k.shape or H != cache.kv_heads or D != cache.head_dim:
+        raise MMQError("kv_append: k and v are [tokens, kv_heads, head_dim] of the cache")
+    hq = hqo = None
+    if q is not None:
+        if q.shape[0] != T or q.shape[2] != D:
+            raise MMQError("kv_append: q and k differ in tokens or head_dim")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise MMQError("kv_append: q_out has another shape than q")
+        hq, hqo = ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(q_out, "q_out"))
+    sq = _seqs(page_table, kv_lens, cu_tokens)
+    _check(load().mmq_kv_append(cache._ref, ctypes.byref(sq), T, ctypes.byref(_heads(k, "k")),
+                                ctypes.byref(_heads(v, "v")), _vector(k_weight, D, "k_weight"), hq,
+                                q.shape[1] if q is not None else 0, _vector(q_weight, D, "q_weight"), hqo,
+                                _rotary(cos, sin, interleaved), eps, _stream(stream)), "mmq_kv_append")
+    return q_out
+
+
+def kv_read(cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, tokens: int,
+            cu_tokens: torch.Tensor | None = None, dtype=torch.bfloat16, stream=None):
+    """The last cu_tokens[s+1] - cu_tokens[s] cached tokens of each sequence, `tokens` in all, as rows (k, v)
+    [tokens, kv_heads, head_dim] of `dtype` (mmq_kv_read)."""
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    k, v = (torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
+    sq = _seqs(page_table, kv_lens, cu_tokens)
+    _check(load().mmq_kv_read(cache._ref, ctypes.byref(sq), tokens, ctypes.byref(_heads(k, "k")),
+                              ctypes.byref(_heads(v, "v")), _stream(stream)), "mmq_kv_read")
+    return k, v
+
+
+def attention_workspace_bytes(tokens: int, heads: int, kv_heads: int, head_dim: int, seqs: int, max_tokens: int,
+                              max_kv_len: int) -> int:
+    return int(load().mmq_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len))
+
+
+def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+              max_kv_len: int | None = None, cu_tokens: torch.Tensor | None = None, max_tokens: int | None = None,
+              scale: float | None = None, causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+              out_dtype=None, return_lse: bool = False, workspace: torch.Tensor | None = None, stream=None):
+    """softmax(scale q k^T) v over the 8-bit paged cache (mmq_attention): out [tokens, heads, head_dim], or
+    (out, lse f32 [tokens, heads]).  max_kv_len and max_tokens bound a sequence's length and new tokens (default:
+    what the page table holds; 1 without cu_tokens, else all tokens); scale defaults to head_dim ** -0.5."""
+    T, H, D = q.shape
+    if D != cache.head_dim:
+        raise MMQError("attention: q has another head_dim than the cache")
+    sq = _seqs(page_table, kv_lens, cu_tokens)
+    if max_kv_len is None:
+        max_kv_len = page_table.shape[1] * cache.page_size
+    if max_tokens is None:
+        max_tokens = 1 if cu_tokens is None else T
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise MMQError("attention: out has another shape than q")
+    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
+    lib = load()
+    need = lib.mmq_attention_workspace_bytes(T, H, cache.kv_heads, D, sq.seqs, max_tokens, max_kv_len)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib.mmq_attention(ctypes.byref(_heads(q, "q")), H, cache._ref, ctypes.byref(sq), T, max_tokens, max_kv_len,
+                             D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                             ctypes.byref(_heads(out, "out")), _ptr(lse), _ptr(workspace),
+                             workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                             _stream(stream)), "mmq_attention")
+    return (out, lse) if return_lse else out

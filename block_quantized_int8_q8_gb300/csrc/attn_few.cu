@@ -1,0 +1,511 @@
+// attn_few.cu -- attention of few query rows over the 8-bit paged cache: single new tokens (decode) and the few of a
+// verification step, up to 16 rows (new tokens x query heads) for each sequence and key/value head.
+//
+//   t_j = scale log2(e) ks_b (q . k_j) + log2(vs_b)      k_j, v_j: int8 codes, b the block of token j
+//   p_j = 2^(t_j - m),  O = sum_j p_j v_j,  l = sum_b (1/vs_b) sum_{j in b} p_j,  out = O / l,
+//   lse = ln(2) (m + log2 l)
+// The value scale enters the exponent, so that it costs nothing per value and the fp16 probabilities stay relative
+// to the largest term; O and l are f32.
+//
+// Bound by reading the cache.  Each warp takes tiles of 16 tokens straight from global memory into the registers of
+// the tensor-core fragments (no shared memory): the product S^T = K Q^T has 16 tokens as rows and 8 query rows as
+// columns, so a group of up to 8 query heads wastes nothing, and O^T = V^T P^T takes P^T from S^T by a transposing
+// register move.  Which head dimension a fragment element means is free as long as both operands agree, so
+// lanes read 16 contiguous bytes: K rows as quarters of 64 bytes, V rows as eighths.  int8 -> fp16 is exact (byte
+// spliced into the mantissa of 1024 + x).  The cache range is split over thread blocks in chunks; each thread block
+// joins its four warps in shared memory, a second launch joins the chunks.
+#include "attn_device.cuh"
+#include "internal.h"
+
+namespace mmq {
+
+namespace {
+
+constexpr int FEW_WARPS = 4;
+constexpr int FEW_THREADS = FEW_WARPS * 32;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float SCALE_FLOOR = 0x1p-64f;      // stands for a zero value scale (all codes zero) in log2 and 1/x
+constexpr float LAZY = 8.f;                  // the running maximum may trail by 2^8 before sums are rescaled
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// word of four codes (c0..c3) -> fp16 pairs (c0, c2) and (c1, c3), exactly
+__device__ __forceinline__ void codes_even_odd(uint32_t w, uint32_t& even, uint32_t& odd) {
+    const uint32_t bias = 0x64806480u;                        // 1024 + 128
+    const uint32_t e = (w & 0x00FF00FFu) ^ bias, o = ((w >> 8) & 0x00FF00FFu) ^ bias;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(bias));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(bias));
+}
+// byte I of two words -> the fp16 pair (a_I, b_I), exactly
+template <int I>
+__device__ __forceinline__ uint32_t codes_across(uint32_t a, uint32_t b) {
+    const uint32_t bias = 0x64806480u;
+    uint32_t r;
+    const uint32_t x = __byte_perm(a, b, I | I << 4 | (4 + I) << 8 | (4 + I) << 12);
+    const uint32_t y = (x & 0x00FF00FFu) ^ bias;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(bias));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 ld_cache(const int8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_cache8(const int8_t* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// The part of the cache that a sequence's rows can see, in tiles of 16 tokens, and its parts of `chunk` tokens.
+struct Range {
+    int tile0, tiles, parts;
+};
+__device__ __forceinline__ Range visible_range(const AttnArgs& a, const Seq& q, int chunk) {
+    const int n = min(q.n, a.max_tokens), end = min(q.end, a.max_kv), first = q.len - q.n;
+    const int j0 = a.window > 0 ? max(first - a.window + 1, 0) : 0;
+    const int j1 = a.causal ? min(end, first + n) : end;
+    Range r;
+    r.tile0 = j0 / 16;
+    r.tiles = max((j1 + 15) / 16 - r.tile0, 0);
+    r.parts = max((r.tiles * 16 + chunk - 1) / chunk, 1);
+    return r;
+}
+
+// Where dimension d of a row of partial sums lies in shared memory (padded so that a fragment's stores and a row's
+// reads fall on different banks).
+template <int D> struct Pad {
+    static constexpr int kShift = D == 64 ? 3 : 4;
+    static constexpr int kPitch = D + (D >> kShift) + 4;
+    __device__ static int at(int d) { return d + (d >> kShift); }
+};
+
+template <int D, int NT> struct FewSmem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kQ = kRows * (D + 8) * 2;                                   // fp16 queries
+    static constexpr int kO = FEW_WARPS * kRows * Pad<D>::kPitch * 4;                // warps' sums (reuses kQ)
+    static constexpr int kBytes = kQ > kO ? kQ : kO;
+};
+
+template <int D> struct KTile {              // two K rows of 16 tokens: 16-byte quarters of each 64 bytes
+    uint4 a[D / 64], b[D / 64];
+};
+template <int D> struct VTile {              // four V rows: D/8 bytes each
+    static constexpr int kWords = D / 32;
+    uint32_t w[4][kWords];
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(const AttnArgs& a, long long row, int g, int t, KTile<D>& k, VTile<D>& v) {
+    const int8_t* kp = a.c.k + (row + g) * D + 16 * t;
+#pragma unroll
+    for (int c = 0; c < D / 64; c++) {
+        k.a[c] = ld_cache(kp + 64 * c);
+        k.b[c] = ld_cache(kp + 8 * D + 64 * c);
+    }
+    const int8_t* vp = a.c.v + (row + 2 * t) * D;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int8_t* p = vp + ((i & 1) + 8 * (i >> 1)) * D;
+        if constexpr (D == 64) {
+            const uint2 x = ld_cache8(p + 8 * g);
+            v.w[i][0] = x.x; v.w[i][1] = x.y;
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 128; c++) {
+                const uint4 x = ld_cache(p + 128 * c + 16 * g);
+                v.w[i][4 * c] = x.x; v.w[i][4 * c + 1] = x.y; v.w[i][4 * c + 2] = x.z; v.w[i][4 * c + 3] = x.w;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float load_q(const void* p, long long i, bool bf16) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+                : __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_out(void* p, long long i, float x, int type) {
+    if (type == MMQ_F32) static_cast<float*>(p)[i] = x;
+    else if (type == MMQ_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+    else static_cast<__half*>(p)[i] = __float2half_rn(x);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int chunk, int splits, int row_blocks,
+                                                          int qt, int ot) {
+    pdl_trigger();
+    pdl_wait();
+    using P = Pad<D>;
+    constexpr int R = 8 * NT;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float s_rs[R], s_m[FEW_WARPS][R], s_l[FEW_WARPS][R];
+    const int split = blockIdx.x % splits, rb = blockIdx.x / splits % row_blocks;
+    const int sh = blockIdx.x / splits / row_blocks, head = sh % a.c.heads, s = sh / a.c.heads;
+    const Seq q = load_seq(a.sq, s, a.c.page);
+    const int n = min(q.n, a.max_tokens), r0 = rb * R, rows = min(n * a.group - r0, R);
+    if (rows <= 0) return;
+    const Range rg = visible_range(a, q, chunk);
+    if (split == 0 && head == 0 && rb == 0 && threadIdx.x == 0 && (q.n > n || min(q.end, a.max_kv) < q.len))
+        flag_error(DEVERR_LENGTH);
+    if (split >= rg.parts) return;
+    const int first = q.len - q.n, end = min(q.end, a.max_kv);
+    const int i0 = r0 / a.group, i1 = (r0 + rows - 1) / a.group;      // new tokens of the first and the last row
+    // tiles of this part that some row of the block sees
+    int t_begin = rg.tile0 + split * (chunk / 16), t_end = rg.tile0 + min(rg.tiles, (split + 1) * (chunk / 16));
+    if (a.causal) t_end = min(t_end, (min(end, first + i1 + 1) + 15) / 16);
+    if (a.window > 0) t_begin = max(t_begin, (first + i0 - a.window + 1) / 16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+    // queries to fp16, each row times the power of two that brings its largest magnitude to [1, 2)
+    __half* sq = reinterpret_cast<__half*>(smem);
+    constexpr int PER = D / 16;
+    for (int r = threadIdx.x / 16; r < R; r += FEW_THREADS / 16) {
+        const int l = threadIdx.x % 16;
+        float x[PER], m = 0.f;
+        const long long at = r < rows ? (long long)(q.n0 + (r0 + r) / a.group) * a.q.ts +
+                                            (long long)(head * a.group + (r0 + r) % a.group) * a.q.hs + l * PER
+                                      : 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            x[i] = r < rows ? load_q(a.q.data, at + i, qt == MMQ_BF16) : 0.f;
+            m = fmaxf(m, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
+        const float up = __uint_as_float((unsigned)(254 - e) << 23), down = __uint_as_float((unsigned)e << 23);
+#pragma unroll
+        for (int i = 0; i < PER; i++) sq[r * (D + 8) + l * PER + i] = __float2half_rn(m == 0.f ? 0.f : x[i] * up);
+        if (l == 0) s_rs[r] = m == 0.f ? 0.f : a.scale * LOG2E * down;
+    }
+    __syncthreads();
+    uint32_t qf[NT][D / 16][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int w = 0; w < D / 16; w++) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sq + (8 * nt + g) * (D + 8) + (w / 4) * 64 + 16 * t +
+                                                            4 * (w % 4));
+            qf[nt][w][0] = __byte_perm(v.x, v.y, 0x5410);
+            qf[nt][w][1] = __byte_perm(v.x, v.y, 0x7632);
+        }
+    float rs[NT][2], m[NT][2], l[NT][2];
+    int lim[NT][2], low[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const int r = 8 * nt + 2 * t + e, i = (r0 + min(r, rows - 1)) / a.group;
+            rs[nt][e] = s_rs[r];
+            lim[nt][e] = a.causal ? min(first + i, end - 1) : end - 1;
+            low[nt][e] = a.window > 0 ? first + i - a.window + 1 : 0;
+            m[nt][e] = -INFINITY;
+            l[nt][e] = 0.f;
+        }
+    // tiles whose 16 tokens every row sees need no mask
+    const int lim_all = a.causal ? min(first + i0, end - 1) : end - 1;
+    const int low_all = a.window > 0 ? first + i1 - a.window + 1 : 0;
+    float o[D / 16][NT][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; i++)
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[i][nt][e] = 0.f;
+
+    // this warp's tiles: t_begin + warp, + 4, ...; lane i looks up the page and the scales of the i-th of 32
+    const int blocks = a.c.page / a.c.block;
+    for (int base = t_begin + warp; base < t_end; base += 32 * FEW_WARPS) {
+        const int mine = base + FEW_WARPS * lane;
+        int ph = 0, off = 0;
+        float ks = 0.f, vs = 0.f;
+        bool dead = true;
+        if (mine < t_end) {
+            const int tok = mine * 16, page = tok / a.c.page;
+            off = tok - page * a.c.page;
+            const int pg = a.sq.table[s * a.sq.stride + page];
+            if ((unsigned)pg < (unsigned long long)a.c.pages) {
+                ph = pg * a.c.heads + head;
+                dead = false;
+                const long long sc = (long long)ph * blocks + off / a.c.block;
+                ks = a.c.ks[sc];
+                vs = a.c.vs[sc];
+            } else {
+                flag_error(DEVERR_PAGE);
+            }
+        }
+        const int here = min((t_end - base + FEW_WARPS - 1) / FEW_WARPS, 32);
+        auto row_of = [&](int i) {
+            return (long long)__shfl_sync(0xffffffffu, ph, i) * a.c.page + __shfl_sync(0xffffffffu, off, i);
+        };
+        KTile<D> kn;
+        VTile<D> vn;
+        load_tile<D>(a, row_of(0), g, t, kn, vn);
+        for (int i = 0; i < here; i++) {
+            const KTile<D> kt = kn;
+            const VTile<D> vt = vn;
+            if (i + 1 < here) load_tile<D>(a, row_of(i + 1), g, t, kn, vn);
+            const float ksc = __shfl_sync(0xffffffffu, ks, i), vsc = fmaxf(__shfl_sync(0xffffffffu, vs, i), SCALE_FLOOR);
+            const bool skip = __shfl_sync(0xffffffffu, (int)dead, i);
+            const int tok = (base + FEW_WARPS * i) * 16;
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sc[nt][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; c++) {
+                const uint32_t wa[4] = {kt.a[c].x, kt.a[c].y, kt.a[c].z, kt.a[c].w};
+                const uint32_t wb[4] = {kt.b[c].x, kt.b[c].y, kt.b[c].z, kt.b[c].w};
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_even_odd(wa[w], a0, a2);
+                    codes_even_odd(wb[w], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+                        mma16816(sc[nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
+                }
+            }
+            const float lv = __log2f(vsc), iv = __fdividef(1.f, vsc);
+            const bool masked = skip || tok + 15 > lim_all || tok < low_all;
+            float top[NT][2];
+            bool grow = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float f = rs[nt][e] * ksc;
+                    sc[nt][e] = fmaf(sc[nt][e], f, lv);
+                    sc[nt][2 + e] = fmaf(sc[nt][2 + e], f, lv);
+                    if (masked) {
+                        if (skip || tok + g > lim[nt][e] || tok + g < low[nt][e]) sc[nt][e] = -INFINITY;
+                        if (skip || tok + g + 8 > lim[nt][e] || tok + g + 8 < low[nt][e]) sc[nt][2 + e] = -INFINITY;
+                    }
+                    float x = fmaxf(sc[nt][e], sc[nt][2 + e]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    top[nt][e] = x;
+                    grow |= x > m[nt][e] + LAZY;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float mn = fmaxf(m[nt][e], top[nt][e]);
+                        const float f = mn == -INFINITY ? 1.f : ex2(m[nt][e] - mn);
+                        m[nt][e] = mn;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int d = 0; d < D / 16; d++) {
+                            o[d][nt][e] *= f;
+                            o[d][nt][2 + e] *= f;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float mu = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                    p[e] = ex2(sc[nt][e] - mu);
+                    p[2 + e] = ex2(sc[nt][2 + e] - mu);
+                    l[nt][e] = fmaf(p[e] + p[2 + e], iv, l[nt][e]);
+                }
+                pf[nt][0] = transpose8(pack2(p[0], p[1], __half()));
+                pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
+            }
+            // O^T += V^T P^T: fragment rows g, g+8 of product 2w+h are dimensions 4w + 2h, + 1 of this lane's bytes
+#pragma unroll
+            for (int w = 0; w < D / 32; w++) {
+                uint32_t a0, a1, a2, a3;
+                a0 = codes_across<0>(vt.w[0][w], vt.w[1][w]);
+                a1 = codes_across<1>(vt.w[0][w], vt.w[1][w]);
+                a2 = codes_across<0>(vt.w[2][w], vt.w[3][w]);
+                a3 = codes_across<1>(vt.w[2][w], vt.w[3][w]);
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                a0 = codes_across<2>(vt.w[0][w], vt.w[1][w]);
+                a1 = codes_across<3>(vt.w[0][w], vt.w[1][w]);
+                a2 = codes_across<2>(vt.w[2][w], vt.w[3][w]);
+                a3 = codes_across<3>(vt.w[2][w], vt.w[3][w]);
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
+        }
+    }
+
+    // join the warps: common maximum, scaled sums through shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            float x = l[nt][e];
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (g == 0) {
+                s_m[warp][8 * nt + 2 * t + e] = m[nt][e];
+                s_l[warp][8 * nt + 2 * t + e] = x;
+            }
+        }
+    __syncthreads();                                          // also: every warp has read its queries
+    float* so = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const int r = 8 * nt + 2 * t + e;
+            float mx = s_m[0][r];
+#pragma unroll
+            for (int w = 1; w < FEW_WARPS; w++) mx = fmaxf(mx, s_m[w][r]);
+            const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx);
+            float* row = so + (warp * R + r) * P::kPitch;
+#pragma unroll
+            for (int d = 0; d < D / 16; d++) {
+                // product d = 2w + h: word w of this lane's bytes (16 at 128c + 16g, or 8 at 8g), dimensions 2h, 2h + 1
+                const int w = d / 2, h = d % 2;
+                const int dim = (D == 64 ? 8 * g + 4 * w : 128 * (w / 4) + 16 * g + 4 * (w % 4)) + 2 * h;
+                row[P::at(dim)] = o[d][nt][e] * f;
+                row[P::at(dim + 1)] = o[d][nt][2 + e] * f;
+            }
+        }
+    __syncthreads();
+    const long long all_rows = (long long)a.sq.tokens * a.heads;
+    for (int i = threadIdx.x; i < rows * D; i += FEW_THREADS) {
+        const int r = i / D, d = i - r * D;
+        float mx = s_m[0][r], den = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 1; w < FEW_WARPS; w++) mx = fmaxf(mx, s_m[w][r]);
+#pragma unroll
+        for (int w = 0; w < FEW_WARPS; w++) {
+            den += s_l[w][r] * (s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - mx));
+            acc += so[(w * R + r) * P::kPitch + P::at(d)];
+        }
+        const long long tok = q.n0 + (r0 + r) / a.group;
+        const int h = head * a.group + (r0 + r) % a.group;
+        if (rg.parts == 1) {
+            store_out(a.out.data, tok * a.out.ts + h * a.out.hs + d, den == 0.f ? 0.f : acc / den, ot);
+            if (d == 0 && a.lse) a.lse[tok * a.heads + h] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
+        } else {
+            const long long row = split * all_rows + tok * a.heads + h;
+            a.part_o[row * D + d] = acc;
+            if (d == 0) a.part_ml[row] = make_float2(mx, den);
+        }
+    }
+}
+
+// One warp for each row of split sequences: the parts' sums on a common maximum, in order.
+constexpr int JOIN_THREADS = 128;
+template <int D>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, int chunk, int ot) {
+    pdl_wait();
+    constexpr int WARPS = JOIN_THREADS / 32, PER = D / 32;
+    const long long all_rows = (long long)a.sq.tokens * a.heads;
+    const long long row0 = (long long)blockIdx.x * WARPS, row = row0 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int t = (int)(min(row, all_rows - 1) / a.heads);
+    int s = t;
+    if (a.sq.cu) {
+        s = block_search<JOIN_THREADS>(a.sq.seqs, row0 / a.heads, [&](int i) { return (long long)a.sq.cu[i]; });
+        while (s + 1 < a.sq.seqs && a.sq.cu[s + 1] <= t) s++;
+    }
+    const Seq q = load_seq(a.sq, s, a.c.page);
+    if (row >= all_rows || t < q.n0 || t >= q.n0 + min(q.n, a.max_tokens)) return;
+    const int parts = visible_range(a, q, chunk).parts;
+    if (parts == 1) return;
+    float mx = -INFINITY;
+    for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, a.part_ml[p * all_rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float acc[PER], den = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; i++) acc[i] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; p++) {
+        const float2 ml = a.part_ml[p * all_rows + row];
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+        den += ml.y * f;
+        const float* po = a.part_o + (p * all_rows + row) * D + lane * PER;
+#pragma unroll
+        for (int i = 0; i < PER; i++) acc[i] += (f == 0.f ? 0.f : po[i] * f);
+    }
+    const int h = (int)(row - (long long)t * a.heads);
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        store_out(a.out.data, (long long)t * a.out.ts + h * a.out.hs + lane * PER + i, den == 0.f ? 0.f : acc[i] / den, ot);
+    if (lane == 0 && a.lse) a.lse[row] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
+}
+
+template <int D, int NT>
+cudaError_t launch_few(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+    const int row_blocks = (a.max_tokens * a.group + 8 * NT - 1) / (8 * NT);
+    const long long grid = (long long)a.sq.seqs * a.c.heads * p.splits * row_blocks;
+    if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = FewSmem<D, NT>::kBytes;
+    auto kern = few_kernel<D, NT>;
+    static bool configured[64] = {};
+    bool& done = device_flag(configured);
+    if (!done) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        done = true;
+    }
+    return launch_pdl_smem(kern, dim3((unsigned)grid), dim3(FEW_THREADS), bytes, s, a, p.chunk, p.splits, row_blocks,
+                           (int)qt, (int)ot);
+}
+
+template <int D>
+cudaError_t launch_few_rows(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+    return a.max_tokens * a.group <= 8 ? launch_few<D, 1>(qt, ot, a, p, s) : launch_few<D, 2>(qt, ot, a, p, s);
+}
+
+}  // namespace
+
+cudaError_t run_attention_few(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,
+                              cudaStream_t s) {
+    switch (dim) {
+        case 64: return launch_few_rows<64>(qt, ot, a, p, s);
+        case 128: return launch_few_rows<128>(qt, ot, a, p, s);
+        case 256: return launch_few_rows<256>(qt, ot, a, p, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t run_attention_join(int dim, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+    const long long grid = ((long long)a.sq.tokens * a.heads + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32);
+    if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    const dim3 g((unsigned)grid), b(JOIN_THREADS);
+    switch (dim) {
+        case 64: return launch_pdl(join_kernel<64>, g, b, s, a, p.chunk, (int)ot);
+        case 128: return launch_pdl(join_kernel<128>, g, b, s, a, p.chunk, (int)ot);
+        case 256: return launch_pdl(join_kernel<256>, g, b, s, a, p.chunk, (int)ot);
+    }
+    return cudaErrorInvalidValue;
+}
+
+MMQ_DEFINE_ERROR_READER(attn_few)
+
+}  // namespace mmq

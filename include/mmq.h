@@ -104,6 +104,10 @@ typedef enum {
 #define MMQ_DEVERR_TIMEOUT     1u  /* a pipeline wait exceeded its limit; the kernel ended early */
 #define MMQ_DEVERR_EXPERT_ID   2u  /* an expert id was outside [0, n_experts); that row was skipped */
 #define MMQ_DEVERR_DUP_EXPERT  4u  /* a token listed the same expert twice */
+#define MMQ_DEVERR_PAGE        8u  /* a page table entry in use was outside the cache; its rows were skipped */
+#define MMQ_DEVERR_POSITION   16u  /* a position was outside the rotation table; that token was skipped */
+#define MMQ_DEVERR_LENGTH     32u  /* a sequence was longer than its page table or the stated maximum, or
+                                      its length or token offsets were inconsistent; the excess was skipped */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mmq_status_string(mmq_status s);
@@ -240,6 +244,120 @@ mmq_status mmq_read_device_errors(unsigned* bits, mmq_stream_t stream);
  * Enqueues on `stream`; read the error bits with mmq_read_device_errors afterwards.
  */
 mmq_status mmq_selftest_bounded_wait(int32_t* result, mmq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------------
+ * Attention over an 8-bit paged key/value cache
+ *
+ * The operators between a fused q/k/v projection and the output projection.  Same conventions as above:
+ * caller-owned device buffers, 16-byte aligned; nothing is allocated or synchronised; argument errors are
+ * returned synchronously.  The structures below are host structures that hold device pointers; they are
+ * read during the call only.
+ *
+ * head_dim is 64, 128 or 256.  A batch packs the new tokens of all its sequences back to back.
+ */
+typedef enum { MMQ_F32 = 0, MMQ_BF16 = 1, MMQ_F16 = 2 } mmq_dtype;
+
+/* Rows of heads, [tokens][heads][head_dim] of dtype: element (t, h, d) at data + t*token_stride + h*head_stride
+ * + d (strides in elements, each a multiple of 16 bytes, so that slices of a fused projection's rows work). */
+typedef struct {
+    void* data;
+    mmq_dtype dtype;
+    int64_t token_stride, head_stride;
+} mmq_heads;
+
+/* Position rotation: f32 cos, sin [positions][rot_dim/2]; the first rot_dim values of a head turn (rot_dim a
+ * positive multiple of 8, at most head_dim) and the rest pass through.  Pair i is values (i, i + rot_dim/2),
+ * or (2i, 2i + 1) where interleaved is set:  (a, b) -> (a cos - b sin, a sin + b cos). */
+typedef struct {
+    const float* cos;
+    const float* sin;
+    int64_t positions;
+    int32_t rot_dim, interleaved;
+} mmq_rotary;
+
+/* The cache of one layer.  k, v: int8 codes [pages][kv_heads][page_size][head_dim]; k_scale, v_scale: f32
+ * [pages][kv_heads][page_size/block], one scale for each block of `block` tokens of one head.  value = scale *
+ * code.  block is 16, 32 or 64; page_size a multiple of block, at most 32768.  Nothing has to be initialised. */
+typedef struct {
+    int8_t* k;
+    int8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int32_t kv_heads, head_dim, page_size, block;
+} mmq_kv_cache;
+
+/* The sequences of a batch.  Sequence s has kv_lens[s] cached tokens, its new ones included; position p of it
+ * lies in page page_table[s*table_stride + p/page_size].  Its new tokens are packed rows cu_tokens[s] ..
+ * cu_tokens[s+1]-1 (cu_tokens int32 [seqs+1]; null: one token for each sequence) and are its last positions.
+ * Page table entries past a sequence's length are not read. */
+typedef struct {
+    const int32_t* page_table;
+    int64_t table_stride;          /* entries in a row of the table */
+    const int32_t* kv_lens;
+    const int32_t* cu_tokens;
+    int32_t seqs;
+} mmq_kv_seqs;
+
+/*
+ * mmq_qk_norm_rope -- RMS norm of each query and key head and the position rotation, in one pass.
+ * y = rotate(x / sqrt(mean(x^2) + eps) * weight) in f32, rounded once to the output's type.  weight: f32
+ * [head_dim], null for no norm.  q and k have one type, q_out and k_out one type.  q and q_out (k and k_out) may be
+ * the same rows (in place: same data, type and strides); q or k may be null with its output.  positions: int32
+ * [tokens].  rotary null: norm only, positions unused.  A token whose position is outside the table is left unwritten
+ * (MMQ_DEVERR_POSITION).
+ */
+mmq_status mmq_qk_norm_rope(const mmq_heads* q, int q_heads, const float* q_weight, const mmq_heads* q_out,
+                            const mmq_heads* k, int k_heads, const float* k_weight, const mmq_heads* k_out,
+                            int64_t tokens, int head_dim, const int32_t* positions, const mmq_rotary* rotary,
+                            float eps, mmq_stream_t stream);
+
+/*
+ * mmq_kv_append -- write the batch's new keys and values to the cache, normed and rotated on the way.
+ * k, v: [tokens][kv_heads][head_dim], one type.  Keys are normed where k_weight is given and rotated where
+ * rotary is, at their position in the sequence; all in f32, and the f32 result is quantized.  Where q is given,
+ * the queries [tokens][q_heads][head_dim] (k's type) are normed and rotated to q_out in the same launch.
+ * Quantization, for each block of tokens and head that gets new tokens:
+ *   s' = max(s, amax/127) with amax over the block's new values and s the block's scale (0 if the block's first
+ *   token is among the new ones; quotients below 2^-63 count as 0); codes already there become
+ *   round-half-even(code * (s/s')), new ones round-half-even(x/s') clamped to [-127, 127].
+ * Inputs must be finite.  Two sequences may share pages only if neither appends to a shared block.
+ */
+mmq_status mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const mmq_heads* k,
+                         const mmq_heads* v, const float* k_weight, const mmq_heads* q, int q_heads,
+                         const float* q_weight, const mmq_heads* q_out, const mmq_rotary* rotary, float eps,
+                         mmq_stream_t stream);
+
+/*
+ * mmq_kv_read -- the last cu_tokens[s+1] - cu_tokens[s] cached tokens of each sequence as rows scale*code (the
+ * f32 product rounded once to the output's type), packed like an append's inputs.  k_out or v_out may be null.
+ * Rows of positions below 0 or on an invalid page are written as zeros.
+ */
+mmq_status mmq_kv_read(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const mmq_heads* k_out,
+                       const mmq_heads* v_out, mmq_stream_t stream);
+
+/*
+ * mmq_attention -- out = softmax(scale * q k^T) v over the cache.
+ * q, out : [tokens][n_heads][head_dim]; n_heads a multiple of the cache's kv_heads, query head h reads key/value
+ *          head h / (n_heads / kv_heads).  q is bf16 or f16, out f32, bf16 or f16.
+ * lse    : f32 [tokens][n_heads], the log of the softmax denominator (natural log, with the scores' scale), or
+ *          null.
+ * Row i of a sequence's n new tokens sees positions j < kv_len; with causal set, j <= kv_len - n + i; with
+ * window > 0 (causal only) j > kv_len - n + i - window too.  A row that sees nothing gets 0 and lse = -inf.
+ * max_tokens, max_kv_len : upper bounds of a sequence's new tokens and of kv_lens; they size the launch.
+ * workspace : mmq_attention_workspace_bytes(...) bytes for the same sizes (0: may be null), 16-byte aligned; its
+ *          contents on entry do not matter.
+ * Arithmetic: cache codes and queries enter the tensor cores as fp16 (codes exactly; a query row is scaled by a
+ * power of two first, so bf16's range fits), probabilities as fp16 relative to the row's largest term; scores,
+ * statistics and sums are f32.  f32 outputs thus carry the probabilities' 2^-11 relative rounding.  Results do not
+ * depend on the order in which blocks of the launch run.
+ */
+size_t mmq_attention_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
+                                     int64_t max_tokens, int64_t max_kv_len);
+mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs,
+                         int64_t tokens, int64_t max_tokens, int64_t max_kv_len, float scale, int causal,
+                         int64_t window, const mmq_heads* out, float* lse, void* workspace,
+                         size_t workspace_bytes, mmq_stream_t stream);
 
 #ifdef __cplusplus
 }
