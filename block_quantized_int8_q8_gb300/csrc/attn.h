@@ -1,5 +1,6 @@
 // attn.h -- host-side interface between the attention boundary (attn_api.cu) and its kernels: norm and
-// rotation, the quantizing append, the cache read (kv_cache.cu) and attention (attn_few.cu).
+// rotation, the quantizing append, the cache read (kv_cache.cu), attention of few rows (attn_few.cu)
+// and of prompts (attn_tiled.cu).
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -85,6 +86,7 @@ struct AttnArgs {
 };
 // How a problem is split along the cache: chunk tokens per part, and the parts of the longest sequence.
 struct AttnPlan {
+    bool few;                  // the few-row kernel, else the tiled one
     int chunk, splits;
     size_t part_o, part_ml, total;     // workspace offsets and size
 };
@@ -92,10 +94,13 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
                         long long max_kv);
 cudaError_t run_attention_few(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,
                               cudaStream_t s);
+cudaError_t run_attention_tiled(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,
+                                cudaStream_t s);
 // Joins the parts of rows whose cache range was split (attn_few.cu).
 cudaError_t run_attention_join(int dim, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
 cudaError_t read_clear_errors_kv_cache(unsigned* bits, cudaStream_t s);
 cudaError_t read_clear_errors_attn_few(unsigned* bits, cudaStream_t s);
+cudaError_t read_clear_errors_attn_tiled(unsigned* bits, cudaStream_t s);
 
 }  // namespace mmq

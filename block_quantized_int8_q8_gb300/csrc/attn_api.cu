@@ -80,17 +80,21 @@ mmq_status done(cudaError_t e, const char* where) { return e == cudaSuccess ? MM
 
 namespace mmq {
 
-// The cache range is cut in chunks so that the launch fills the GPU several times over (ragged batches even out).
+// Few rows (new tokens x query heads of a key/value head <= 16) run on the few-row kernel, more on the tiled one.
+// The cache range is cut in chunks where the row blocks alone would not fill the GPU.
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
                         long long max_kv) {
     AttnPlan p{};
-    const long long pairs = (long long)seqs * kv_heads * ((max_tokens * (heads / kv_heads) + 15) / 16);
-    const long long target = 152 * 8;
+    const long long rows = max_tokens * (heads / kv_heads);
+    p.few = rows <= 16;
+    const int block = p.few ? 16 : (dim == 256 ? 128 : 256), granule = p.few ? 64 : 128;
+    const long long pairs = (long long)seqs * kv_heads * ((rows + block - 1) / block);
+    const long long target = p.few ? 152 * 8 : 152;
     const long long want = (target + pairs - 1) / pairs;
     long long chunk = (max_kv + want - 1) / want;
-    chunk = (chunk + 63) / 64 * 64;
-    if (chunk < 128) chunk = 128;
-    if (chunk > 2048) chunk = 2048;
+    chunk = (chunk + granule - 1) / granule * granule;
+    if (p.few && chunk > 2048) chunk = 2048;
+    if (chunk < (p.few ? 128 : 512)) chunk = p.few ? 128 : 512;
     p.chunk = (int)chunk;
     // a window or an unaligned start can shift the range by one tile
     p.splits = (int)((max_kv + 16 + chunk - 1) / chunk);
@@ -243,7 +247,8 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
         a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_o);
     }
     cudaStream_t s = stream_of(stream);
-    cudaError_t e = run_attention_few(cache->head_dim, q->dtype, out->dtype, a, p, s);
+    cudaError_t e = p.few ? run_attention_few(cache->head_dim, q->dtype, out->dtype, a, p, s)
+                          : run_attention_tiled(cache->head_dim, q->dtype, out->dtype, a, p, s);
     if (e == cudaSuccess && p.splits > 1) e = run_attention_join(cache->head_dim, out->dtype, a, p, s);
     return done(e, "mmq_attention");
 }

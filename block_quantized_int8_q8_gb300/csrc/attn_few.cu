@@ -15,6 +15,7 @@
 // spliced into the mantissa of 1024 + x).  The cache range is split over thread blocks in chunks; each thread block
 // joins its four warps in shared memory, a second launch joins the chunks.
 #include "attn_device.cuh"
+#include "attn_math.cuh"
 #include "internal.h"
 
 namespace mmq {
@@ -23,24 +24,6 @@ namespace {
 
 constexpr int FEW_WARPS = 4;
 constexpr int FEW_THREADS = FEW_WARPS * 32;
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float SCALE_FLOOR = 0x1p-64f;      // stands for a zero value scale (all codes zero) in log2 and 1/x
-constexpr float LAZY = 8.f;                  // the running maximum may trail by 2^8 before sums are rescaled
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// word of four codes (c0..c3) -> fp16 pairs (c0, c2) and (c1, c3), exactly
-__device__ __forceinline__ void codes_even_odd(uint32_t w, uint32_t& even, uint32_t& odd) {
-    const uint32_t bias = 0x64806480u;                        // 1024 + 128
-    const uint32_t e = (w & 0x00FF00FFu) ^ bias, o = ((w >> 8) & 0x00FF00FFu) ^ bias;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(bias));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(bias));
-}
 // byte I of two words -> the fp16 pair (a_I, b_I), exactly
 template <int I>
 __device__ __forceinline__ uint32_t codes_across(uint32_t a, uint32_t b) {
@@ -63,31 +46,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint4 ld_cache(const int8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
 __device__ __forceinline__ uint2 ld_cache8(const int8_t* p) {
     uint2 v;
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
-}
-
-// The part of the cache that a sequence's rows can see, in tiles of 16 tokens, and its parts of `chunk` tokens.
-struct Range {
-    int tile0, tiles, parts;
-};
-__device__ __forceinline__ Range visible_range(const AttnArgs& a, const Seq& q, int chunk) {
-    const int n = min(q.n, a.max_tokens), end = min(q.end, a.max_kv), first = q.len - q.n;
-    const int j0 = a.window > 0 ? max(first - a.window + 1, 0) : 0;
-    const int j1 = a.causal ? min(end, first + n) : end;
-    Range r;
-    r.tile0 = j0 / 16;
-    r.tiles = max((j1 + 15) / 16 - r.tile0, 0);
-    r.parts = max((r.tiles * 16 + chunk - 1) / chunk, 1);
-    return r;
 }
 
 // Where dimension d of a row of partial sums lies in shared memory (padded so that a fragment's stores and a row's
@@ -190,11 +152,11 @@ __global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int 
         }
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
-        const float up = __uint_as_float((unsigned)(254 - e) << 23), down = __uint_as_float((unsigned)e << 23);
+        float up, down;
+        row_scale(m, up, down);
 #pragma unroll
-        for (int i = 0; i < PER; i++) sq[r * (D + 8) + l * PER + i] = __float2half_rn(m == 0.f ? 0.f : x[i] * up);
-        if (l == 0) s_rs[r] = m == 0.f ? 0.f : a.scale * LOG2E * down;
+        for (int i = 0; i < PER; i++) sq[r * (D + 8) + l * PER + i] = __float2half_rn(x[i] * up);
+        if (l == 0) s_rs[r] = a.scale * LOG2E * down;
     }
     __syncthreads();
     uint32_t qf[NT][D / 16][2];

@@ -352,7 +352,8 @@ mmq_status mmq_read_device_errors(unsigned* bits, mmq_stream_t stream) {
                                                          read_clear_errors_q4_k,     read_clear_errors_iq1_m,
                                                          read_clear_errors_w8a8,     read_clear_errors_tma,
                                                          read_clear_errors_selftest, read_clear_errors_gemv,
-                                                         read_clear_errors_kv_cache, read_clear_errors_attn_few};
+                                                         read_clear_errors_kv_cache, read_clear_errors_attn_few,
+                                                         read_clear_errors_attn_tiled};
     for (auto r : readers) {
         cudaError_t ei = r(bits, s);
         if (ei != cudaSuccess) e = ei;
