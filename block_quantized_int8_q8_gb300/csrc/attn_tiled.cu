@@ -6,16 +6,16 @@
 // Bound by the tensor cores and the exponentials.  One thread block takes 256 rows (two tiles of 128; head_dim 256:
 // one) of one sequence and key/value head, rows = (new token, query head of the group), and walks the cache in tiles
 // of 128 tokens (head_dim 256: 64):
-//   * four converter warps read the codes of a tile from their pages, turn them into fp16 exactly and store them
-//     with the 128-byte swizzle.  K is the K-major operand of S, V the MN-major operand of O, so both have
-//     the same layout [token][64 dimensions of 128 bytes] and one routine makes them.  Within each four dimensions
-//     the order is 0 2 1 3 (two codes of a word convert at once); Q is stored in that order too, and the
-//     output undoes it.  They also publish the tile's block scales.
+//   * three converter warps read the codes in units of 16 tokens (each within one page), turn them into fp16 exactly
+//     and store them with the 128-byte swizzle.  K is the K-major operand of S, V the MN-major operand of O, so both
+//     have the same layout [token][64 dimensions of 128 bytes] and one routine makes them.  Within each four
+//     dimensions the order is 0 2 1 3 (two codes of a word convert at once); Q is stored in that order too, and the
+//     output undoes it.  They also publish the units' block scales.
 //   * one warp issues the products, S_i = Q_i K^T into TMEM and O_i += P_i V with P_i from TMEM.  The two row
 //     tiles alternate: while the softmax of one runs, the other's products do.
-//   * four softmax warps for each row tile, one thread a row: two passes over the row of S in TMEM (maximum, then
-//     exponentials), P as fp16 over the columns of S already read.  O is rescaled only when the maximum grows by
-//     more than 2^8, which happens a few times in a row's life.
+//   * four softmax warps for each row tile, one thread a row: the row of S in registers, its maximum, the
+//     exponentials, P as fp16 over the columns of S (in halves, so that the product can start on the first).  O is
+//     rescaled only when the maximum grows by more than 2^8, which happens a few times in a row's life.
 #include "attn_device.cuh"
 #include "attn_math.cuh"
 #include "internal.h"
@@ -42,14 +42,17 @@ template <int D> struct Tiled {
     static constexpr int kv_off = q_off + kQTiles * kQBytes;
     static constexpr int sc_off = kv_off + kStages * kStageBytes;              // float4 [slots][blocks]
     static constexpr int bar_off = sc_off + kScaleSlots * kBlocks * 16;
-    static constexpr int n_bars = 2 * kStages + kScaleSlots + 3 * 2 + 1 + 2 + 1;
+    static constexpr int n_bars = 2 * kStages + kScaleSlots + 2 + 4 + 2 + 3;
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int alloc = misc_off + 16 + 1024;
     static_assert(alloc <= 232448, "shared memory budget");
 };
 
-constexpr int T_CONV0 = 8, T_CONV_WARPS = 4, T_MMA = 12;
-constexpr int T_THREADS = 13 * 32;
+constexpr int T_CONV0 = 8, T_CONV_WARPS = 3, T_MMA = 11;
+constexpr int T_THREADS = 12 * 32;
+constexpr float MASKED = -3.0e38f;           // a hidden score: its term is below NOTHING for any scale above F_FLOOR
+constexpr float F_FLOOR = 1e-30f;
+constexpr float NOTHING = -1e8f;
 
 // tcgen05.mma with A from TMEM (fp16, two elements a column).
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -80,15 +83,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+// 64 columns of 32-bit TMEM values for this warp's 32 lanes, and the wait that makes them usable.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait64(uint32_t (&r)[64]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+                   "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+                   "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+                   "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+                   "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
                  :
                  : "memory");
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 template <int D> struct TBars {
@@ -98,11 +125,13 @@ template <int D> struct TBars {
     __device__ uint32_t empty(int i) const { return b + 8u * (C::kStages + i); }
     __device__ uint32_t scale(int i) const { return b + 8u * (2 * C::kStages + i); }   // scales published
     __device__ uint32_t sfull(int i) const { return b + 8u * (2 * C::kStages + C::kScaleSlots + i); }
-    __device__ uint32_t pready(int i) const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 2 + i); }
-    __device__ uint32_t odone(int i) const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 4 + i); }
-    __device__ uint32_t qfull() const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 6); }
-    __device__ uint32_t pvdone() const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 7); }
-    __device__ uint32_t done() const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 8); }
+    __device__ uint32_t pready(int i, int h) const {                                   // halves of P
+        return b + 8u * (2 * C::kStages + C::kScaleSlots + 2 + 2 * i + h);
+    }
+    __device__ uint32_t odone(int i) const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 6 + i); }
+    __device__ uint32_t qfull() const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 8); }
+    __device__ uint32_t pvdone() const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 9); }
+    __device__ uint32_t done() const { return b + 8u * (2 * C::kStages + C::kScaleSlots + 10); }
 };
 
 // The cache tiles [s, e) of a row tile, counted from the part's first token.
@@ -165,13 +194,14 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     if (warp == T_MMA) {
         if (lane == 0) {
             for (int i = 0; i < C::kStages; i++) {
-                mbar_init(bar.full(i), T_CONV_WARPS);
+                mbar_init(bar.full(i), C::kBlocks);
                 mbar_init(bar.empty(i), 1);
             }
-            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), T_CONV_WARPS);
+            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), C::kBlocks);
             for (int i = 0; i < 2; i++) {
                 mbar_init(bar.sfull(i), 1);
-                mbar_init(bar.pready(i), 4);
+                mbar_init(bar.pready(i, 0), 4);
+                mbar_init(bar.pready(i, 1), 4);
                 mbar_init(bar.odone(i), 1);
             }
             mbar_init(bar.qfull(), 4 * NQ);
@@ -191,103 +221,88 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
 
     if (warp >= T_CONV0 && warp < T_CONV0 + T_CONV_WARPS) {
         // =========================================================== converters
-        // warp w: rows w*KT/4 .. of the tile, in 16-token groups; lane (g, t): rows g, g+8 of a group, 16 bytes at
-        // 16t of each 64.  A quarter-warp stores two rows of four 16-byte chunks: all 32 banks.
-        constexpr int GROUPS = KT / 4 / 16, CH = D / 64;
+        // Units of 16 tokens, K's of a tile and then V's; warp w takes every third.  Lane (g, t) of a unit: rows g, g+8,
+        // 16 bytes at 16t of each 64.  A quarter-warp stores two rows of four 16-byte chunks: all 32 banks.
+        constexpr int CH = D / 64, PF = D == 256 ? 2 : 4;     // units in flight
         const int w = warp - T_CONV0, g = lane >> 2, t = lane & 3;
-        const int blocks = a.c.page / a.c.block;
-        int ph[GROUPS], off[GROUPS];                          // page and head, row in the page; ph < 0: zeros
-        float ks = 0.f, lv = -INFINITY, iv = 0.f;             // lane i < GROUPS: scales of group i
-        auto lookup = [&](int j) {
-            int myph = -1, myoff = 0;
-            ks = 0.f, lv = -INFINITY, iv = 0.f;
-            if (lane < GROUPS && j < j1) {
-                const int tok = base + j * KT + (w * GROUPS + lane) * 16;
-                if (tok < end) {
-                    const int page = tok / a.c.page;
-                    myoff = tok - page * a.c.page;
-                    const int pg = a.sq.table[s * a.sq.stride + page];
-                    if ((unsigned)pg < (unsigned long long)a.c.pages) {
-                        myph = pg * a.c.heads + head;
-                        const long long sc = (long long)myph * blocks + myoff / a.c.block;
-                        ks = a.c.ks[sc];
-                        const float vs = fmaxf(a.c.vs[sc], SCALE_FLOOR);
-                        lv = __log2f(vs);
-                        iv = __fdividef(1.f, vs);
-                    } else {
-                        flag_error(DEVERR_PAGE);
+        const int blocks = a.c.page / a.c.block, units = (j1 - j0) * 2 * C::kBlocks;
+        // lane i looks up the i-th of the warp's next 32 units
+        int ph = -1, off = 0;                                 // page and head (negative: zeros), row in the page
+        float ks = 0.f, lv = -INFINITY, iv = 0.f;
+        auto lookup = [&](int u0) {
+            const int u = u0 + T_CONV_WARPS * lane;
+            ph = -1, off = 0, ks = 0.f, lv = -INFINITY, iv = 0.f;
+            const int tok = base + (j0 + u / (2 * C::kBlocks)) * KT + (u % C::kBlocks) * 16;
+            if (u < units && tok < end) {
+                const int page = tok / a.c.page;
+                off = tok - page * a.c.page;
+                const int pg = a.sq.table[s * a.sq.stride + page];
+                if ((unsigned)pg < (unsigned long long)a.c.pages) {
+                    ph = pg * a.c.heads + head;
+                    const long long sc = (long long)ph * blocks + off / a.c.block;
+                    ks = a.c.ks[sc];
+                    const float vs = fmaxf(a.c.vs[sc], SCALE_FLOOR);
+                    lv = __log2f(vs);
+                    iv = __fdividef(1.f, vs);
+                } else {
+                    flag_error(DEVERR_PAGE);
+                }
+            }
+        };
+        uint4 r[PF][2][CH];
+        auto load = [&](int u, int i, uint4 (&x)[2][CH]) {    // unit u, the i-th of the looked-up ones
+            const int p = __shfl_sync(0xffffffffu, ph, i), o = __shfl_sync(0xffffffffu, off, i);
+            const int8_t* codes = (u / C::kBlocks) & 1 ? a.c.v : a.c.k;
+            const int8_t* src = codes + ((long long)max(p, 0) * a.c.page + o + g) * D + 16 * t;
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int c = 0; c < CH; c++)
+                    x[h][c] = p >= 0 ? ld_cache(src + 8 * h * D + 64 * c) : make_uint4(0, 0, 0, 0);
+        };
+        bool ok = true;
+        for (int u0 = w; ok && u0 < units; u0 += 32 * T_CONV_WARPS) {
+            lookup(u0);
+            const int here = min((units - u0 + T_CONV_WARPS - 1) / T_CONV_WARPS, 32);
+#pragma unroll
+            for (int i = 0; i < PF; i++)
+                if (i < here) load(u0 + T_CONV_WARPS * i, i, r[i]);
+            for (int i0 = 0; ok && i0 < here; i0 += PF) {
+#pragma unroll
+                for (int ii = 0; ii < PF; ii++) {
+                    const int i = i0 + ii, u = u0 + T_CONV_WARPS * i;
+                    if (i >= here || !ok) break;
+                    const int x = u / C::kBlocks, st = x % C::kStages, unit = u % C::kBlocks;    // stored tile x
+                    if (!mbar_wait_relaxed(bar.empty(st), ((x / C::kStages) & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
                     }
-                }
-            }
+                    const uint32_t tile = sb + C::kv_off + st * C::kStageBytes;
 #pragma unroll
-            for (int i = 0; i < GROUPS; i++) {
-                ph[i] = __shfl_sync(0xffffffffu, myph, i);
-                off[i] = __shfl_sync(0xffffffffu, myoff, i);
-            }
-        };
-        auto load = [&](const int8_t* codes, uint4 (&r)[GROUPS][2][CH]) {
+                    for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int i = 0; i < GROUPS; i++) {
-                const int8_t* p = codes + ((long long)max(ph[i], 0) * a.c.page + off[i] + g) * D + 16 * t;
-#pragma unroll
-                for (int h = 0; h < 2; h++)
-#pragma unroll
-                    for (int c = 0; c < CH; c++)
-                        r[i][h][c] = ph[i] >= 0 ? ld_cache(p + 8 * h * D + 64 * c) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        auto store = [&](uint32_t tile, const uint4 (&r)[GROUPS][2][CH]) {
-#pragma unroll
-            for (int i = 0; i < GROUPS; i++)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int row = (w * GROUPS + i) * 16 + 8 * h + g;
-#pragma unroll
-                    for (int c = 0; c < CH; c++) {
-                        const uint4 x = r[i][h][c];
-                        uint32_t y[8];
-                        codes_even_odd(x.x, y[0], y[1]);
-                        codes_even_odd(x.y, y[2], y[3]);
-                        codes_even_odd(x.z, y[4], y[5]);
-                        codes_even_odd(x.w, y[6], y[7]);
-                        const uint32_t at = tile + c * KT * 128;
-                        st_shared_v4(at + sw128_off(row, 2 * t), y[0], y[1], y[2], y[3]);
-                        st_shared_v4(at + sw128_off(row, 2 * t + 1), y[4], y[5], y[6], y[7]);
+                        for (int c = 0; c < CH; c++) {
+                            const uint4 v = r[ii][h][c];
+                            uint32_t y[8];
+                            codes_even_odd(v.x, y[0], y[1]);
+                            codes_even_odd(v.y, y[2], y[3]);
+                            codes_even_odd(v.z, y[4], y[5]);
+                            codes_even_odd(v.w, y[6], y[7]);
+                            const uint32_t row = unit * 16 + 8 * h + g, at = tile + c * KT * 128;
+                            st_shared_v4(at + sw128_off(row, 2 * t), y[0], y[1], y[2], y[3]);
+                            st_shared_v4(at + sw128_off(row, 2 * t + 1), y[4], y[5], y[6], y[7]);
+                        }
+                    // scales with the K units; the slot's last reader was four tiles ago (its S is complete)
+                    const int slot = (x >> 1) % C::kScaleSlots;
+                    if (!(x & 1) && lane == i) scales[slot * C::kBlocks + unit] = make_float4(ks, lv, iv, 0.f);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar.full(st));
+                        if (!(x & 1)) mbar_arrive(bar.scale(slot));
                     }
+                    if (i + PF < here) load(u + T_CONV_WARPS * PF, i + PF, r[ii]);
                 }
-        };
-        uint4 rk[GROUPS][2][CH], rv[GROUPS][2][CH];
-        lookup(j0);
-        load(a.c.k, rk);
-        int it = 0;                                           // tiles stored, K and V
-        for (int j = j0; j < j1; j++) {
-            load(a.c.v, rv);
-            // scales of this tile: the slot's last reader was four tiles ago (its S is complete)
-            const int slot = (j - j0) % C::kScaleSlots;
-            const float ks0 = ks, lv0 = lv, iv0 = iv;
-            {
-                const int st = it % C::kStages;
-                if (!mbar_wait_relaxed(bar.empty(st), ((it / C::kStages) & 1) ^ 1, abort_flag)) break;
-                if (lane < GROUPS) scales[slot * C::kBlocks + w * GROUPS + lane] = make_float4(ks0, lv0, iv0, 0.f);
-                store(sb + C::kv_off + st * C::kStageBytes, rk);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar.full(st));
-                    mbar_arrive(bar.scale(slot));
-                }
-                it++;
-            }
-            lookup(j + 1);
-            if (j + 1 < j1) load(a.c.k, rk);
-            {
-                const int st = it % C::kStages;
-                if (!mbar_wait_relaxed(bar.empty(st), ((it / C::kStages) & 1) ^ 1, abort_flag)) break;
-                store(sb + C::kv_off + st * C::kStageBytes, rv);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar.full(st));
-                it++;
             }
         }
     } else if (warp == T_MMA) {
@@ -308,17 +323,19 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             }
             __syncwarp();
         };
-        auto product_o = [&](int i, int j) {                  // O of row tile i
+        auto product_o = [&](int i, int j, int h) {           // O of row tile i, half h of the cache tile's tokens
             const int st = (2 * (j - j0) + 1) % C::kStages;
             const uint32_t kv = sb + C::kv_off + st * C::kStageBytes;
             const uint32_t buf = NQ == 2 ? i : (j - j0) & 1;
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < KT / 16; k++)
-                    umma_f16_ts(tmem + C::kOCol + i * D, tmem + buf * KT + 8 * k,
-                                sdesc_mn_sw128(kv + k * 2048, KT * 128), idesc_o, j > span[i].s || k > 0);
-                if (j + 1 == span[i].e) umma_commit(bar.odone(i));
-                if (NQ == 1) umma_commit(bar.pvdone());
+                for (int k = 0; k < KT / 32; k++) {
+                    const int kk = h * (KT / 32) + k;
+                    umma_f16_ts(tmem + C::kOCol + i * D, tmem + buf * KT + 8 * kk,
+                                sdesc_mn_sw128(kv + kk * 2048, KT * 128), idesc_o, j > span[i].s || kk > 0);
+                }
+                if (h == 1 && j + 1 == span[i].e) umma_commit(bar.odone(i));
+                if (h == 1 && NQ == 1) umma_commit(bar.pvdone());
             }
             __syncwarp();
         };
@@ -356,11 +373,15 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             for (int i = 0; i < NQ; i++) {
                 if (active(i, j)) {
                     const int buf = NQ == 2 ? i : (j - j0) & 1;
-                    ok = ok && mbar_wait(bar.pready(buf), (np >> buf) & 1, abort_flag);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        ok = ok && mbar_wait(bar.pready(buf, h), (np >> buf) & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        product_o(i, j, h);
+                    }
                     np ^= 1u << buf;
                     if (!ok) break;
-                    tc_fence_after();
-                    product_o(i, j);
                 }
                 if (NQ == 2 && more && active(i, j + 1)) {
                     tc_fence_after();
@@ -442,35 +463,33 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             const float4* sc = scales + slot * C::kBlocks;
             const int t0 = base + j * KT;
             const bool masked = t0 + KT - 1 > lim_all || t0 < low_all;
-            uint32_t va[32], vb[32];
-            // pass 1: largest term of the row
-            float top = -INFINITY;
-            tmem_ld32(ts, va);
+            float x[KT];                                      // the row of S
+            {
+                uint32_t(&v)[KT / 64][64] = reinterpret_cast<uint32_t(&)[KT / 64][64]>(x);
 #pragma unroll
-            for (int c = 0; c < KT / 32; c++) {
-                uint32_t(&cur)[32] = (c & 1) ? vb : va;
-                uint32_t(&nxt)[32] = (c & 1) ? va : vb;
-                tmem_wait32(cur);
-                tmem_ld32(ts + (c + 1 < KT / 32 ? 32 * (c + 1) : 0), nxt);        // the last one: pass 2's first
+                for (int c = 0; c < KT / 64; c++) tmem_ld64(ts + 64 * c, v[c]);
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const float4 b = sc[2 * c + h];
-                    const int tb = t0 + 32 * c + 16 * h;
-                    float mx = -3.0e38f;
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 16; e++) {
-                            const float x = __uint_as_float(cur[16 * h + e]);
-                            mx = fmaxf(mx, (tb + e <= lim && tb + e >= low) ? x : -3.0e38f);
-                        }
-                        if (tb <= lim && tb + 15 >= low) top = fmaxf(top, fmaf(mx, b.x * rs, b.y));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e++) mx = fmaxf(mx, __uint_as_float(cur[16 * h + e]));
-                        top = fmaxf(top, fmaf(mx, b.x * rs, b.y));
-                    }
-                }
+                for (int c = 0; c < KT / 64; c++) tmem_wait64(v[c]);
             }
+            if (masked) {
+                const int hi = lim - t0, lo = low - t0;
+#pragma unroll
+                for (int e = 0; e < KT; e++)
+                    if (e > hi || e < lo) x[e] = MASKED;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < KT / 16; k++) {
+                const float* v = x + 16 * k;
+                float m0 = fmaxf(fmaxf(v[0], v[1]), v[2]), m1 = fmaxf(fmaxf(v[3], v[4]), v[5]);
+                float m2 = fmaxf(fmaxf(v[6], v[7]), v[8]), m3 = fmaxf(fmaxf(v[9], v[10]), v[11]);
+                m0 = fmaxf(fmaxf(m0, v[12]), v[13]);
+                m1 = fmaxf(fmaxf(m1, v[14]), v[15]);
+                m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                const float4 b = sc[k];
+                top = fmaxf(top, fmaf(m0, fmaxf(b.x * rs, F_FLOOR), b.y));
+            }
+            if (top < NOTHING) top = -INFINITY;
             if (NQ == 1 && j > span[i].s) {                   // the product that reads and writes O is complete
                 if (!mbar_wait(bar.pvdone(), (j - span[i].s - 1) & 1, abort_flag)) {
                     ok = false;
@@ -484,7 +503,6 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 m = mn;
                 l *= f;
                 if (j > span[i].s) {                          // all products so far are complete: S came after them
-                    tmem_wait32(va);
 #pragma unroll 1
                     for (int c = 0; c < D / 16; c++) {
                         uint32_t o[16];
@@ -497,39 +515,38 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 }
             }
             const float mu = m == -INFINITY ? 0.f : m;
-            // pass 2: the terms, P over the columns of S that are read
 #pragma unroll
-            for (int c = 0; c < KT / 32; c++) {
-                uint32_t(&cur)[32] = (c & 1) ? vb : va;
-                uint32_t(&nxt)[32] = (c & 1) ? va : vb;
-                tmem_wait32(cur);
-                if (c + 1 < KT / 32) tmem_ld32(ts + 32 * (c + 1), nxt);
-                uint32_t p[16];
+            for (int h = 0; h < 2; h++) {
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const float4 b = sc[2 * c + h];
-                    const int tb = t0 + 32 * c + 16 * h;
-                    const float f = b.x * rs, shift = b.y - mu;
-                    float sum = 0.f;
+                for (int c = 0; c < KT / 64; c++) {           // 32 columns: two blocks
+                    uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float p0 = ex2(fmaf(__uint_as_float(cur[16 * h + e]), f, shift));
-                        float p1 = ex2(fmaf(__uint_as_float(cur[16 * h + e + 1]), f, shift));
-                        if (masked) {
-                            if (tb + e > lim || tb + e < low) p0 = 0.f;
-                            if (tb + e + 1 > lim || tb + e + 1 < low) p1 = 0.f;
+                    for (int k2 = 0; k2 < 2; k2++) {
+                        const int k = h * (KT / 32) + 2 * c + k2;
+                        const float4 b = sc[k];
+                        const float f = fmaxf(b.x * rs, F_FLOOR), shift = b.y - mu;
+                        const uint64_t f2 = f2_pack(f, f), s2 = f2_pack(shift, shift);
+                        uint64_t sum2 = 0ull;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float p0, p1;
+                            f2_unpack(f2_fma(f2_pack(x[16 * k + e], x[16 * k + e + 1]), f2, s2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum2 = f2_add(sum2, f2_pack(p0, p1));
+                            p[8 * k2 + e / 2] = pack2(p0, p1, __half());
                         }
-                        sum += p0 + p1;
-                        p[8 * h + e / 2] = pack2(p0, p1, __half());
+                        float a0, a1;
+                        f2_unpack(sum2, a0, a1);
+                        l = fmaf(a0 + a1, b.z, l);
                     }
-                    l = fmaf(sum, b.z, l);
+                    tmem_st16(ts + (h * (KT / 64) + c) * 16, p);
                 }
-                tmem_st16(ts + 16 * c, p);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.pready(buf, h));
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar.pready(buf));
         }
         // ---- output row
         if (ok && span[i].e > span[i].s) {
