@@ -6,7 +6,7 @@
 // Bound by the tensor cores and the exponentials.  One thread block takes 256 rows (two tiles of 128; head_dim 256:
 // one) of one sequence and key/value head, rows = (new token, query head of the group), and walks the cache in tiles
 // of 128 tokens (head_dim 256: 64):
-//   * three converter warps read the codes in units of 16 tokens (each within one page), turn them into fp16 exactly
+//   * seven converter warps read the codes in units of 16 tokens (each within one page), turn them into fp16 exactly
 //     and store them with the 128-byte swizzle.  K is the K-major operand of S, V the MN-major operand of O, so both
 //     have the same layout [token][64 dimensions of 128 bytes] and one routine makes them.  Within each four
 //     dimensions the order is 0 2 1 3 (two codes of a word convert at once); Q is stored in that order too, and the
@@ -48,8 +48,11 @@ template <int D> struct Tiled {
     static_assert(alloc <= 232448, "shared memory budget");
 };
 
-constexpr int T_CONV0 = 8, T_CONV_WARPS = 3, T_MMA = 11;
-constexpr int T_THREADS = 12 * 32;
+constexpr int T_CONV0 = 8, T_CONV_WARPS = 7, T_MMA = 15;
+constexpr int T_THREADS = 16 * 32;
+// registers a thread: 128 at launch, moved from the converter and product warps to the softmax warps
+constexpr int T_REGS_SOFTMAX = 176, T_REGS_REST = 80;
+static_assert(8 * 32 * (T_REGS_SOFTMAX + T_REGS_REST) <= T_THREADS * 128, "register budget");
 constexpr float MASKED = -3.0e38f;           // a hidden score: its term is below NOTHING for any scale above F_FLOOR
 constexpr float F_FLOOR = 1e-30f;
 constexpr float NOTHING = -1e8f;
@@ -218,12 +221,13 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-
-    if (warp >= T_CONV0 && warp < T_CONV0 + T_CONV_WARPS) {
+    if (warp >= T_CONV0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T_REGS_REST));
+    if (warp != T_MMA) {
         // =========================================================== converters
-        // Units of 16 tokens, K's of a tile and then V's; warp w takes every third.  Lane (g, t) of a unit: rows g, g+8,
+        // Units of 16 tokens, K's of a tile and then V's; warp w takes every seventh.  Lane (g, t) of a unit: rows g, g+8,
         // 16 bytes at 16t of each 64.  A quarter-warp stores two rows of four 16-byte chunks: all 32 banks.
-        constexpr int CH = D / 64, PF = D == 256 ? 2 : 4;     // units in flight
+        constexpr int CH = D / 64, PF = D == 256 ? 1 : 2;     // units in flight
         const int w = warp - T_CONV0, g = lane >> 2, t = lane & 3;
         const int blocks = a.c.page / a.c.block, units = (j1 - j0) * 2 * C::kBlocks;
         // lane i looks up the i-th of the warp's next 32 units
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 }
             }
         }
-    } else if (warp == T_MMA) {
+    } else {
         // =========================================================== products
         constexpr uint32_t idesc_s = idesc_f16_f32(128, KT);
         constexpr uint32_t idesc_o = idesc_f16_f32(128, D) | (1u << 16);         // B is MN-major
@@ -396,7 +400,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         __syncwarp();
         mbar_wait_final(bar.done(), 0);
         __syncwarp();
-    } else if (warp < 4 * NQ) {
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T_REGS_SOFTMAX));
+    if (warp < 4 * NQ) {
         // =========================================================== softmax: one thread a row
         const int i = warp >> 2, r = 128 * i + (warp & 3) * 32 + lane;           // row of the block
         const bool real = r < rows;
@@ -584,6 +591,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         }
     }
 
+    }
     // ---- teardown
     tc_fence_before();
     __syncthreads();
