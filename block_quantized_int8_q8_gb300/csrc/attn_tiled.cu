@@ -28,11 +28,14 @@ template <int D> struct Tiled {
     static constexpr int kQTiles = D == 256 ? 1 : 2;          // row tiles of 128
     static constexpr int kSBufs = 2;                          // S buffers: one a row tile, or two of one tile
     static constexpr int kTokens = D == 256 ? 64 : 128;       // cache tokens of a tile
-    static constexpr int kStages = D == 64 ? 6 : 4;           // K and V tiles in turn
+    static constexpr int kStages = D == 64 ? 6 : 5;           // K and V tiles in turn
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = kTokens * D * 2;
     static constexpr int kBlocks = kTokens / 16;              // 16-token groups, each within a page and a scale block
     static constexpr int kScaleSlots = 4;
+    // registers a thread, moved from the converter and product warps to the softmax warps (a row of S each)
+    static constexpr int kRegsSoftmax = D == 256 ? 128 : 176, kRegsRest = D == 256 ? 128 : 80;
+    static_assert(kRegsSoftmax + kRegsRest <= 256, "register budget: as many warps of either kind, 128 at launch");
     // TMEM columns: S buffers (P over their first half), then O
     static constexpr int kOCol = kSBufs * kTokens;
     static constexpr int kCols = 512;
@@ -50,32 +53,34 @@ template <int D> struct Tiled {
 
 constexpr int T_CONV0 = 8, T_CONV_WARPS = 7, T_MMA = 15;
 constexpr int T_THREADS = 16 * 32;
-// registers a thread: 128 at launch, moved from the converter and product warps to the softmax warps
-constexpr int T_REGS_SOFTMAX = 176, T_REGS_REST = 80;
-static_assert(8 * 32 * (T_REGS_SOFTMAX + T_REGS_REST) <= T_THREADS * 128, "register budget");
 constexpr float MASKED = -3.0e38f;           // a hidden score: its term is below NOTHING for any scale above F_FLOOR
 constexpr float F_FLOOR = 1e-30f;
 constexpr float NOTHING = -1e8f;
 
-// tcgen05.mma with A from TMEM (fp16, two elements a column).
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Shared-memory matrix descriptors as two words: the upper one is constant for a layout (8-row groups 1024 bytes
+// apart, 128-byte swizzle), the lower one holds the start address / 16 and the leading offset / 16, so that stepping
+// along an operand adds to the lower word.  K-major: leading offset unused (1).  MN-major (64 elements of MN contiguous):
+// leading offset = bytes to the next 64 elements of MN.
+constexpr uint32_t DESC_HI = (uint32_t)(((uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61) >> 32);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
+    return ((saddr & 0x3FFFFu) >> 4) | (leading >> 4) << 16;
+}
+// D[tmem] (+)= A[smem] B[smem]^T, and with A from TMEM (fp16, two elements a column).
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(DESC_HI)
         : "memory");
 }
-// MN-major operand with the 128-byte swizzle: 64 elements of MN contiguous, `slab` bytes to the next 64, 8-row groups
-// of K 1024 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t slab) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(slab >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(DESC_HI)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -197,10 +202,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     if (warp == T_MMA) {
         if (lane == 0) {
             for (int i = 0; i < C::kStages; i++) {
-                mbar_init(bar.full(i), C::kBlocks);
+                mbar_init(bar.full(i), KT / 32);
                 mbar_init(bar.empty(i), 1);
             }
-            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), C::kBlocks);
+            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), KT / 32);
             for (int i = 0; i < 2; i++) {
                 mbar_init(bar.sfull(i), 1);
                 mbar_init(bar.pready(i, 0), 4);
@@ -222,27 +227,29 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (warp >= T_CONV0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T_REGS_REST));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     if (warp != T_MMA) {
         // =========================================================== converters
-        // Units of 16 tokens, K's of a tile and then V's; warp w takes every seventh.  Lane (g, t) of a unit: rows g, g+8,
-        // 16 bytes at 16t of each 64.  A quarter-warp stores two rows of four 16-byte chunks: all 32 banks.
-        constexpr int CH = D / 64, PF = D == 256 ? 1 : 2;     // units in flight
+        // Units of 32 tokens (two groups of 16, each within one page), K's of a tile and then V's; warp w takes every
+        // seventh.  Lane (g, t) of a group: rows g, g+8, 16 bytes at 16t of each 64.  A quarter-warp stores two rows
+        // of four 16-byte chunks: all 32 banks.
+        constexpr int CH = D / 64, UNITS = KT / 32;           // units of a stored tile
         const int w = warp - T_CONV0, g = lane >> 2, t = lane & 3;
-        const int blocks = a.c.page / a.c.block, units = (j1 - j0) * 2 * C::kBlocks;
-        // lane i looks up the i-th of the warp's next 32 units
-        int ph = -1, off = 0;                                 // page and head (negative: zeros), row in the page
+        const int blocks = a.c.page / a.c.block, units = (j1 - j0) * 2 * UNITS;
+        const uint32_t sts0 = sb + C::kv_off + sw128_off(g, 2 * t), sts1 = sb + C::kv_off + sw128_off(g, 2 * t + 1);
+        // lanes 2i, 2i+1 look up the groups of the i-th of the warp's next 16 units
+        long long src = -1;                                   // first code of the group (negative: zeros)
         float ks = 0.f, lv = -INFINITY, iv = 0.f;
         auto lookup = [&](int u0) {
-            const int u = u0 + T_CONV_WARPS * lane;
-            ph = -1, off = 0, ks = 0.f, lv = -INFINITY, iv = 0.f;
-            const int tok = base + (j0 + u / (2 * C::kBlocks)) * KT + (u % C::kBlocks) * 16;
+            const int u = u0 + T_CONV_WARPS * (lane >> 1);
+            src = -1, ks = 0.f, lv = -INFINITY, iv = 0.f;
+            const int tok = base + (j0 + u / (2 * UNITS)) * KT + (u % UNITS) * 32 + (lane & 1) * 16;
             if (u < units && tok < end) {
-                const int page = tok / a.c.page;
-                off = tok - page * a.c.page;
+                const int page = tok / a.c.page, off = tok - page * a.c.page;
                 const int pg = a.sq.table[s * a.sq.stride + page];
                 if ((unsigned)pg < (unsigned long long)a.c.pages) {
-                    ph = pg * a.c.heads + head;
+                    const int ph = pg * a.c.heads + head;
+                    src = ((long long)ph * a.c.page + off) * D;
                     const long long sc = (long long)ph * blocks + off / a.c.block;
                     ks = a.c.ks[sc];
                     const float vs = fmaxf(a.c.vs[sc], SCALE_FLOOR);
@@ -253,90 +260,87 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 }
             }
         };
-        uint4 r[PF][2][CH];
-        auto load = [&](int u, int i, uint4 (&x)[2][CH]) {    // unit u, the i-th of the looked-up ones
-            const int p = __shfl_sync(0xffffffffu, ph, i), o = __shfl_sync(0xffffffffu, off, i);
-            const int8_t* codes = (u / C::kBlocks) & 1 ? a.c.v : a.c.k;
-            const int8_t* src = codes + ((long long)max(p, 0) * a.c.page + o + g) * D + 16 * t;
+        uint4 r[2][2][CH];
+        auto load = [&](int x, int i) {                       // i-th looked-up unit, of stored tile x
+            const int8_t* codes = (x & 1 ? a.c.v : a.c.k) + g * D + 16 * t;
 #pragma unroll
-            for (int h = 0; h < 2; h++)
+            for (int q2 = 0; q2 < 2; q2++) {
+                const long long at = __shfl_sync(0xffffffffu, src, 2 * i + q2);
 #pragma unroll
-                for (int c = 0; c < CH; c++)
-                    x[h][c] = p >= 0 ? ld_cache(src + 8 * h * D + 64 * c) : make_uint4(0, 0, 0, 0);
-        };
-        bool ok = true;
-        for (int u0 = w; ok && u0 < units; u0 += 32 * T_CONV_WARPS) {
-            lookup(u0);
-            const int here = min((units - u0 + T_CONV_WARPS - 1) / T_CONV_WARPS, 32);
+                for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int i = 0; i < PF; i++)
-                if (i < here) load(u0 + T_CONV_WARPS * i, i, r[i]);
-            for (int i0 = 0; ok && i0 < here; i0 += PF) {
-#pragma unroll
-                for (int ii = 0; ii < PF; ii++) {
-                    const int i = i0 + ii, u = u0 + T_CONV_WARPS * i;
-                    if (i >= here || !ok) break;
-                    const int x = u / C::kBlocks, st = x % C::kStages, unit = u % C::kBlocks;    // stored tile x
-                    if (!mbar_wait_relaxed(bar.empty(st), ((x / C::kStages) & 1) ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t tile = sb + C::kv_off + st * C::kStageBytes;
-#pragma unroll
-                    for (int h = 0; h < 2; h++)
-#pragma unroll
-                        for (int c = 0; c < CH; c++) {
-                            const uint4 v = r[ii][h][c];
-                            uint32_t y[8];
-                            codes_even_odd(v.x, y[0], y[1]);
-                            codes_even_odd(v.y, y[2], y[3]);
-                            codes_even_odd(v.z, y[4], y[5]);
-                            codes_even_odd(v.w, y[6], y[7]);
-                            const uint32_t row = unit * 16 + 8 * h + g, at = tile + c * KT * 128;
-                            st_shared_v4(at + sw128_off(row, 2 * t), y[0], y[1], y[2], y[3]);
-                            st_shared_v4(at + sw128_off(row, 2 * t + 1), y[4], y[5], y[6], y[7]);
-                        }
-                    // scales with the K units; the slot's last reader was four tiles ago (its S is complete)
-                    const int slot = (x >> 1) % C::kScaleSlots;
-                    if (!(x & 1) && lane == i) scales[slot * C::kBlocks + unit] = make_float4(ks, lv, iv, 0.f);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar.full(st));
-                        if (!(x & 1)) mbar_arrive(bar.scale(slot));
-                    }
-                    if (i + PF < here) load(u + T_CONV_WARPS * PF, i + PF, r[ii]);
-                }
+                    for (int c = 0; c < CH; c++)
+                        r[q2][h][c] = at >= 0 ? ld_cache(codes + at + 8 * h * D + 64 * c) : make_uint4(0, 0, 0, 0);
             }
+        };
+        int i = 0;
+        lookup(w);
+        if (w < units) load(w / UNITS, 0);
+        for (int u = w; u < units; u += T_CONV_WARPS) {
+            const int x = u / UNITS, st = x % C::kStages, unit = u % UNITS;      // stored tile x
+            if (!mbar_wait(bar.empty(st), ((x / C::kStages) & 1) ^ 1, abort_flag)) break;
+            const uint32_t to = st * C::kStageBytes + unit * 32 * 128;
+#pragma unroll
+            for (int q2 = 0; q2 < 2; q2++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int c = 0; c < CH; c++) {
+                        const uint4 v = r[q2][h][c];
+                        uint32_t y[8];
+                        codes_even_odd(v.x, y[0], y[1]);
+                        codes_even_odd(v.y, y[2], y[3]);
+                        codes_even_odd(v.z, y[4], y[5]);
+                        codes_even_odd(v.w, y[6], y[7]);
+                        const uint32_t at = to + c * KT * 128 + q2 * 2048 + h * 1024;
+                        st_shared_v4(sts0 + at, y[0], y[1], y[2], y[3]);
+                        st_shared_v4(sts1 + at, y[4], y[5], y[6], y[7]);
+                    }
+            // scales with the K units; the slot's last reader was four tiles ago (its S is complete)
+            const int slot = (x >> 1) % C::kScaleSlots;
+            if (!(x & 1) && (lane >> 1) == i) scales[slot * C::kBlocks + 2 * unit + (lane & 1)] = make_float4(ks, lv, iv, 0.f);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar.full(st));
+                if (!(x & 1)) mbar_arrive(bar.scale(slot));
+            }
+            if (++i == 16) {
+                lookup(u + T_CONV_WARPS);
+                i = 0;
+            }
+            if (u + T_CONV_WARPS < units) load((u + T_CONV_WARPS) / UNITS, i);
         }
     } else {
         // =========================================================== products
         constexpr uint32_t idesc_s = idesc_f16_f32(128, KT);
         constexpr uint32_t idesc_o = idesc_f16_f32(128, D) | (1u << 16);         // B is MN-major
+        const uint32_t q_lo = desc_lo(sb + C::q_off, 16), k_lo = desc_lo(sb + C::kv_off, 16);
+        const uint32_t v_lo = desc_lo(sb + C::kv_off, KT * 128);
         auto active = [&](int i, int j) { return j >= span[i].s && j < span[i].e; };
         auto product_s = [&](int i, int j) {                  // S of row tile i, cache tile j
             const int st = 2 * (j - j0) % C::kStages;
-            const uint32_t qs = sb + C::q_off + i * C::kQBytes, kv = sb + C::kv_off + st * C::kStageBytes;
+            const uint32_t qs = q_lo + i * (C::kQBytes >> 4), kv = k_lo + st * (C::kStageBytes >> 4);
             const uint32_t buf = NQ == 2 ? i : (j - j0) & 1;
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; k++)
-                    umma_f16(tmem + buf * KT, sdesc_sw128(qs + (k / 4) * 16384) + 2 * (k % 4),
-                             sdesc_sw128(kv + (k / 4) * KT * 128) + 2 * (k % 4), idesc_s, k > 0);
+                    umma_ss(tmem + buf * KT, qs + (k / 4) * (16384 >> 4) + 2 * (k % 4),
+                            kv + (k / 4) * (KT * 128 >> 4) + 2 * (k % 4), idesc_s, k > 0);
                 umma_commit(bar.sfull(buf));
             }
             __syncwarp();
         };
         auto product_o = [&](int i, int j, int h) {           // O of row tile i, half h of the cache tile's tokens
             const int st = (2 * (j - j0) + 1) % C::kStages;
-            const uint32_t kv = sb + C::kv_off + st * C::kStageBytes;
+            const uint32_t kv = v_lo + st * (C::kStageBytes >> 4);
             const uint32_t buf = NQ == 2 ? i : (j - j0) & 1;
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < KT / 32; k++) {
                     const int kk = h * (KT / 32) + k;
-                    umma_f16_ts(tmem + C::kOCol + i * D, tmem + buf * KT + 8 * kk,
-                                sdesc_mn_sw128(kv + kk * 2048, KT * 128), idesc_o, j > span[i].s || kk > 0);
+                    umma_ts(tmem + C::kOCol + i * D, tmem + buf * KT + 8 * kk, kv + kk * (2048 >> 4), idesc_o,
+                            j > span[i].s || kk > 0);
                 }
                 if (h == 1 && j + 1 == span[i].e) umma_commit(bar.odone(i));
                 if (h == 1 && NQ == 1) umma_commit(bar.pvdone());
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         __syncwarp();
     }
     } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T_REGS_SOFTMAX));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
     if (warp < 4 * NQ) {
         // =========================================================== softmax: one thread a row
         const int i = warp >> 2, r = 128 * i + (warp & 3) * 32 + lane;           // row of the block
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 }
             }
             if (real) {
-                if (part) a.part_ml[split * all_rows + row] = make_float2(m, l);
+                if (part) a.part_ml[split * all_rows + row] = make_float2(l == 0.f ? -INFINITY : m, l);
                 else if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : LN2 * (m + log2f(l));
             }
         }
