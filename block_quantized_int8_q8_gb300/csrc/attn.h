@@ -84,6 +84,8 @@ struct AttnArgs {
     float* part_o;             // [splits][rows][dim], not divided by the denominator
     float2* part_ml;           // [splits][rows]: running maximum (log2) and denominator
 };
+// Thread blocks of the few-row kernel that fit on an SM (its launch bound), for head_dim and 8 or 16 rows.
+constexpr int few_blocks(int dim, int nt) { return dim == 256 ? 2 : (nt == 2 ? 3 : 4); }
 // How a problem is split along the cache: chunk tokens per part, and the parts of the longest sequence.
 struct AttnPlan {
     bool few;                  // the few-row kernel, else the tiled one

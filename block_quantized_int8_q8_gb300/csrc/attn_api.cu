@@ -82,19 +82,34 @@ namespace mmq {
 
 // Few rows (new tokens x query heads of a key/value head <= 16) run on the few-row kernel, more on the tiled one.
 // The cache range is cut in chunks where the row blocks alone would not fill the GPU.
+//   few rows: all thread blocks do equal work on equal lengths, so the chunks are cut to make one wave; ragged lengths even out from 2048 tokens down.
+//   tiled: one thread block fits on an SM.  With B of them the last wave leaves SMs idle; cutting the range in c
+//     parts takes ceil(c B / 152) / c waves of the whole range's time, plus the join (about 3 % of a 512-token part).
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
                         long long max_kv) {
     AttnPlan p{};
+    constexpr long long SMS = 152;
     const long long rows = max_tokens * (heads / kv_heads);
     p.few = rows <= 16;
-    const int block = p.few ? 16 : (dim == 256 ? 128 : 256), granule = p.few ? 64 : 128;
-    const long long pairs = (long long)seqs * kv_heads * ((rows + block - 1) / block);
-    const long long target = p.few ? 152 * 8 : 152;
-    const long long want = (target + pairs - 1) / pairs;
-    long long chunk = (max_kv + want - 1) / want;
-    chunk = (chunk + granule - 1) / granule * granule;
-    if (p.few && chunk > 2048) chunk = 2048;
-    if (chunk < (p.few ? 128 : 512)) chunk = p.few ? 128 : 512;
+    const long long pairs = (long long)seqs * kv_heads;
+    long long chunk;
+    if (p.few) {
+        const long long want = (few_blocks(dim, rows <= 8 ? 1 : 2) * SMS + pairs - 1) / pairs;
+        chunk = (max_kv + want - 1) / want;
+        chunk = (chunk + 63) / 64 * 64;
+        chunk = chunk < 128 ? 128 : (chunk > 2048 ? 2048 : chunk);
+    } else {
+        const int block = dim == 256 ? 128 : 256;
+        const long long blocks = pairs * ((rows + block - 1) / block);
+        long long best = 1;
+        double cost = 1e30;
+        for (long long c = 1; c <= 32 && (c == 1 || max_kv / c >= 512); c++) {
+            const double t = (double)((c * blocks + SMS - 1) / SMS) / c * (c == 1 ? 1.0 : 1.02 + 16.0 * c / max_kv);
+            if (t < cost) cost = t, best = c;
+        }
+        chunk = ((max_kv + best - 1) / best + 127) / 128 * 128;
+        if (chunk < 512) chunk = 512;
+    }
     p.chunk = (int)chunk;
     // a window or an unaligned start can shift the range by one tile
     p.splits = (int)((max_kv + 16 + chunk - 1) / chunk);

@@ -75,25 +75,27 @@ template <int D> struct VTile {              // four V rows: D/8 bytes each
     uint32_t w[4][kWords];
 };
 
+// kp, vp: this lane's first byte of the tile's K rows (row g, 16t) and V rows (row 2t, its eighth of the bytes).
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, long long row, int g, int t, KTile<D>& k, VTile<D>& v) {
-    const int8_t* kp = a.c.k + (row + g) * D + 16 * t;
+__device__ __forceinline__ void load_k(const int8_t* kp, KTile<D>& k) {
 #pragma unroll
     for (int c = 0; c < D / 64; c++) {
         k.a[c] = ld_cache(kp + 64 * c);
         k.b[c] = ld_cache(kp + 8 * D + 64 * c);
     }
-    const int8_t* vp = a.c.v + (row + 2 * t) * D;
+}
+template <int D>
+__device__ __forceinline__ void load_v(const int8_t* vp, VTile<D>& v) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int8_t* p = vp + ((i & 1) + 8 * (i >> 1)) * D;
         if constexpr (D == 64) {
-            const uint2 x = ld_cache8(p + 8 * g);
+            const uint2 x = ld_cache8(p);
             v.w[i][0] = x.x; v.w[i][1] = x.y;
         } else {
 #pragma unroll
             for (int c = 0; c < D / 128; c++) {
-                const uint4 x = ld_cache(p + 128 * c + 16 * g);
+                const uint4 x = ld_cache(p + 128 * c);
                 v.w[i][4 * c] = x.x; v.w[i][4 * c + 1] = x.y; v.w[i][4 * c + 2] = x.z; v.w[i][4 * c + 3] = x.w;
             }
         }
@@ -111,7 +113,7 @@ __device__ __forceinline__ void store_out(void* p, long long i, float x, int typ
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int chunk, int splits, int row_blocks,
+__global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(const AttnArgs a, int chunk, int splits, int row_blocks,
                                                           int qt, int ot) {
     pdl_trigger();
     pdl_wait();
@@ -136,6 +138,41 @@ __global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int 
     if (a.window > 0) t_begin = max(t_begin, (first + i0 - a.window + 1) / 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
+    // this warp's tiles: t_begin + warp, + 4, ...; lane i looks up the place and the scales of the i-th of the next 32
+    const int blocks = a.c.page / a.c.block;
+    const int tiles = max((t_end - t_begin - warp + FEW_WARPS - 1) / FEW_WARPS, 0);
+    long long src = 0;                                        // first code of the tile
+    float ks = 0.f, lv = -INFINITY, iv = 0.f;                 // (no place: the tile's terms vanish)
+    auto lookup = [&](int n0) {
+        const int tok = (t_begin + warp + FEW_WARPS * (n0 + lane)) * 16;
+        src = 0, ks = 0.f, lv = -INFINITY, iv = 0.f;
+        if (n0 + lane < tiles) {
+            const int page = tok / a.c.page, off = tok - page * a.c.page;
+            const int pg = a.sq.table[s * a.sq.stride + page];
+            if ((unsigned)pg < (unsigned long long)a.c.pages) {
+                const int ph = pg * a.c.heads + head;
+                src = ((long long)ph * a.c.page + off) * D;
+                const long long sc = (long long)ph * blocks + off / a.c.block;
+                ks = a.c.ks[sc];
+                const float vs = fmaxf(a.c.vs[sc], SCALE_FLOOR);
+                lv = __log2f(vs);
+                iv = __fdividef(1.f, vs);
+            } else {
+                flag_error(DEVERR_PAGE);
+            }
+        }
+    };
+    const int8_t* kbase = a.c.k + g * D + 16 * t;
+    const int8_t* vbase = a.c.v + 2 * t * D + (D == 64 ? 8 : 16) * g;
+    KTile<D> kt;
+    VTile<D> vt;
+    lookup(0);
+    if (tiles > 0) {                                          // the first tile is on its way while the queries convert
+        const long long at = __shfl_sync(0xffffffffu, src, 0);
+        load_k<D>(kbase + at, kt);
+        load_v<D>(vbase + at, vt);
+    }
+
     // queries to fp16, each row times the power of two that brings its largest magnitude to [1, 2)
     __half* sq = reinterpret_cast<__half*>(smem);
     constexpr int PER = D / 16;
@@ -159,26 +196,25 @@ __global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int 
         if (l == 0) s_rs[r] = a.scale * LOG2E * down;
     }
     __syncthreads();
-    uint32_t qf[NT][D / 16][2];
+    // fragments of the queries: in registers, but for the largest shape, which reads them from shared memory each time
+    constexpr bool QREG = D * NT <= 256;
+    auto q_frag = [&](int nt, int w) {
+        const uint2 v = *reinterpret_cast<const uint2*>(sq + (8 * nt + g) * (D + 8) + (w / 4) * 64 + 16 * t + 4 * (w % 4));
+        return make_uint2(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632));
+    };
+    uint2 qf[QREG ? NT : 1][QREG ? D / 16 : 1];
+    if constexpr (QREG) {
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++)
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int w = 0; w < D / 16; w++) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sq + (8 * nt + g) * (D + 8) + (w / 4) * 64 + 16 * t +
-                                                            4 * (w % 4));
-            qf[nt][w][0] = __byte_perm(v.x, v.y, 0x5410);
-            qf[nt][w][1] = __byte_perm(v.x, v.y, 0x7632);
-        }
+            for (int w = 0; w < D / 16; w++) qf[nt][w] = q_frag(nt, w);
+    }
     float rs[NT][2], m[NT][2], l[NT][2];
-    int lim[NT][2], low[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            const int r = 8 * nt + 2 * t + e, i = (r0 + min(r, rows - 1)) / a.group;
-            rs[nt][e] = s_rs[r];
-            lim[nt][e] = a.causal ? min(first + i, end - 1) : end - 1;
-            low[nt][e] = a.window > 0 ? first + i - a.window + 1 : 0;
+            rs[nt][e] = s_rs[8 * nt + 2 * t + e];
             m[nt][e] = -INFINITY;
             l[nt][e] = 0.f;
         }
@@ -193,130 +229,109 @@ __global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int 
 #pragma unroll
             for (int e = 0; e < 4; e++) o[i][nt][e] = 0.f;
 
-    // this warp's tiles: t_begin + warp, + 4, ...; lane i looks up the page and the scales of the i-th of 32
-    const int blocks = a.c.page / a.c.block;
-    for (int base = t_begin + warp; base < t_end; base += 32 * FEW_WARPS) {
-        const int mine = base + FEW_WARPS * lane;
-        int ph = 0, off = 0;
-        float ks = 0.f, vs = 0.f;
-        bool dead = true;
-        if (mine < t_end) {
-            const int tok = mine * 16, page = tok / a.c.page;
-            off = tok - page * a.c.page;
-            const int pg = a.sq.table[s * a.sq.stride + page];
-            if ((unsigned)pg < (unsigned long long)a.c.pages) {
-                ph = pg * a.c.heads + head;
-                dead = false;
-                const long long sc = (long long)ph * blocks + off / a.c.block;
-                ks = a.c.ks[sc];
-                vs = a.c.vs[sc];
-            } else {
-                flag_error(DEVERR_PAGE);
-            }
-        }
-        const int here = min((t_end - base + FEW_WARPS - 1) / FEW_WARPS, 32);
-        auto row_of = [&](int i) {
-            return (long long)__shfl_sync(0xffffffffu, ph, i) * a.c.page + __shfl_sync(0xffffffffu, off, i);
-        };
-        KTile<D> kn;
-        VTile<D> vn;
-        load_tile<D>(a, row_of(0), g, t, kn, vn);
-        for (int i = 0; i < here; i++) {
-            const KTile<D> kt = kn;
-            const VTile<D> vt = vn;
-            if (i + 1 < here) load_tile<D>(a, row_of(i + 1), g, t, kn, vn);
-            const float ksc = __shfl_sync(0xffffffffu, ks, i), vsc = fmaxf(__shfl_sync(0xffffffffu, vs, i), SCALE_FLOOR);
-            const bool skip = __shfl_sync(0xffffffffu, (int)dead, i);
-            const int tok = (base + FEW_WARPS * i) * 16;
-            float sc[NT][4];
+    for (int n = 0; n < tiles; n++) {
+        const int i = n & 31, tok = (t_begin + warp + FEW_WARPS * n) * 16;
+        const float ksc = __shfl_sync(0xffffffffu, ks, i), lvc = __shfl_sync(0xffffffffu, lv, i);
+        const float ivc = __shfl_sync(0xffffffffu, iv, i);
+        float sc[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++)
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) sc[nt][e] = 0.f;
+            for (int e = 0; e < 4; e++) sc[nt][e] = 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 64; c++) {
-                const uint32_t wa[4] = {kt.a[c].x, kt.a[c].y, kt.a[c].z, kt.a[c].w};
-                const uint32_t wb[4] = {kt.b[c].x, kt.b[c].y, kt.b[c].z, kt.b[c].w};
+        for (int c = 0; c < D / 64; c++) {
+            const uint32_t wa[4] = {kt.a[c].x, kt.a[c].y, kt.a[c].z, kt.a[c].w};
+            const uint32_t wb[4] = {kt.b[c].x, kt.b[c].y, kt.b[c].z, kt.b[c].w};
 #pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_even_odd(wa[w], a0, a2);
-                    codes_even_odd(wb[w], a1, a3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-                        mma16816(sc[nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
-                }
-            }
-            const float lv = __log2f(vsc), iv = __fdividef(1.f, vsc);
-            const bool masked = skip || tok + 15 > lim_all || tok < low_all;
-            float top[NT][2];
-            bool grow = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const float f = rs[nt][e] * ksc;
-                    sc[nt][e] = fmaf(sc[nt][e], f, lv);
-                    sc[nt][2 + e] = fmaf(sc[nt][2 + e], f, lv);
-                    if (masked) {
-                        if (skip || tok + g > lim[nt][e] || tok + g < low[nt][e]) sc[nt][e] = -INFINITY;
-                        if (skip || tok + g + 8 > lim[nt][e] || tok + g + 8 < low[nt][e]) sc[nt][2 + e] = -INFINITY;
-                    }
-                    float x = fmaxf(sc[nt][e], sc[nt][2 + e]);
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    top[nt][e] = x;
-                    grow |= x > m[nt][e] + LAZY;
-                }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float mn = fmaxf(m[nt][e], top[nt][e]);
-                        const float f = mn == -INFINITY ? 1.f : ex2(m[nt][e] - mn);
-                        m[nt][e] = mn;
-                        l[nt][e] *= f;
-#pragma unroll
-                        for (int d = 0; d < D / 16; d++) {
-                            o[d][nt][e] *= f;
-                            o[d][nt][2 + e] *= f;
-                        }
-                    }
-            }
-            uint32_t pf[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++) {
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const float mu = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-                    p[e] = ex2(sc[nt][e] - mu);
-                    p[2 + e] = ex2(sc[nt][2 + e] - mu);
-                    l[nt][e] = fmaf(p[e] + p[2 + e], iv, l[nt][e]);
-                }
-                pf[nt][0] = transpose8(pack2(p[0], p[1], __half()));
-                pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
-            }
-            // O^T += V^T P^T: fragment rows g, g+8 of product 2w+h are dimensions 4w + 2h, + 1 of this lane's bytes
-#pragma unroll
-            for (int w = 0; w < D / 32; w++) {
+            for (int w = 0; w < 4; w++) {
                 uint32_t a0, a1, a2, a3;
-                a0 = codes_across<0>(vt.w[0][w], vt.w[1][w]);
-                a1 = codes_across<1>(vt.w[0][w], vt.w[1][w]);
-                a2 = codes_across<0>(vt.w[2][w], vt.w[3][w]);
-                a3 = codes_across<1>(vt.w[2][w], vt.w[3][w]);
+                codes_even_odd(wa[w], a0, a2);
+                codes_even_odd(wb[w], a1, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                a0 = codes_across<2>(vt.w[0][w], vt.w[1][w]);
-                a1 = codes_across<3>(vt.w[0][w], vt.w[1][w]);
-                a2 = codes_across<2>(vt.w[2][w], vt.w[3][w]);
-                a3 = codes_across<3>(vt.w[2][w], vt.w[3][w]);
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                for (int nt = 0; nt < NT; nt++) {
+                    const uint2 f = QREG ? qf[QREG ? nt : 0][QREG ? 4 * c + w : 0] : q_frag(nt, 4 * c + w);
+                    mma16816(sc[nt], a0, a1, a2, a3, f.x, f.y);
+                }
             }
         }
+        // the registers of K are free: the next tile's loads start here, V's after its product
+        long long next = 0;
+        if (n + 1 < tiles) {
+            if (i == 31) lookup(n + 1);
+            next = __shfl_sync(0xffffffffu, src, (n + 1) & 31);
+            load_k<D>(kbase + next, kt);
+        }
+        const bool masked = tok + 15 > lim_all || tok < low_all;
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float f = rs[nt][e] * ksc;
+                sc[nt][e] = fmaf(sc[nt][e], f, lvc);
+                sc[nt][2 + e] = fmaf(sc[nt][2 + e], f, lvc);
+                if (masked) {
+                    const int at = (r0 + min(8 * nt + 2 * t + e, rows - 1)) / a.group;       // new token of the row
+                    const int lim = a.causal ? min(first + at, end - 1) : end - 1;
+                    const int low = a.window > 0 ? first + at - a.window + 1 : 0;
+                    if (tok + g > lim || tok + g < low) sc[nt][e] = -INFINITY;
+                    if (tok + g + 8 > lim || tok + g + 8 < low) sc[nt][2 + e] = -INFINITY;
+                }
+                grow |= fmaxf(sc[nt][e], sc[nt][2 + e]) > m[nt][e] + LAZY;
+            }
+        // the reference of a row (one for the lanes that share its column) is raised when a term passes it by 2^8
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float top = fmaxf(sc[nt][e], sc[nt][2 + e]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float mn = fmaxf(m[nt][e], top);
+                    const float f = mn == -INFINITY ? 1.f : ex2(m[nt][e] - mn);
+                    m[nt][e] = mn;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int d = 0; d < D / 16; d++) {
+                        o[d][nt][e] *= f;
+                        o[d][nt][2 + e] *= f;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float mu = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                p[e] = ex2(sc[nt][e] - mu);
+                p[2 + e] = ex2(sc[nt][2 + e] - mu);
+                l[nt][e] = fmaf(p[e] + p[2 + e], ivc, l[nt][e]);
+            }
+            pf[nt][0] = transpose8(pack2(p[0], p[1], __half()));
+            pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
+        }
+        // O^T += V^T P^T: fragment rows g, g+8 of product 2w+h are dimensions 4w + 2h, + 1 of this lane's bytes
+#pragma unroll
+        for (int w = 0; w < D / 32; w++) {
+            uint32_t a0, a1, a2, a3;
+            a0 = codes_across<0>(vt.w[0][w], vt.w[1][w]);
+            a1 = codes_across<1>(vt.w[0][w], vt.w[1][w]);
+            a2 = codes_across<0>(vt.w[2][w], vt.w[3][w]);
+            a3 = codes_across<1>(vt.w[2][w], vt.w[3][w]);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            a0 = codes_across<2>(vt.w[0][w], vt.w[1][w]);
+            a1 = codes_across<3>(vt.w[0][w], vt.w[1][w]);
+            a2 = codes_across<2>(vt.w[2][w], vt.w[3][w]);
+            a3 = codes_across<3>(vt.w[2][w], vt.w[3][w]);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        }
+        if (n + 1 < tiles) load_v<D>(vbase + next, vt);
     }
 
     // join the warps: common maximum, scaled sums through shared memory
@@ -379,15 +394,18 @@ __global__ void __launch_bounds__(FEW_THREADS) few_kernel(const AttnArgs a, int 
     }
 }
 
-// One warp for each row of split sequences: the parts' sums on a common maximum, in order.
+// Rows of split sequences: the parts' sums on a common maximum, in a fixed order.  W warps a row (four for few rows,
+// whose parts are many; one for many).
 constexpr int JOIN_THREADS = 128;
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, int chunk, int ot) {
     pdl_wait();
-    constexpr int WARPS = JOIN_THREADS / 32, PER = D / 32;
+    constexpr int ROWS = JOIN_THREADS / 32 / W, PER = D / 32;
+    __shared__ float s_acc[W > 1 ? W : 1][W > 1 ? D : 1], s_den[W];
     const long long all_rows = (long long)a.sq.tokens * a.heads;
-    const long long row0 = (long long)blockIdx.x * WARPS, row = row0 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const long long row0 = (long long)blockIdx.x * ROWS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = W > 1 ? warp : 0;
+    const long long row = W > 1 ? row0 : row0 + warp;
     const int t = (int)(min(row, all_rows - 1) / a.heads);
     int s = t;
     if (a.sq.cu) {
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
         while (s + 1 < a.sq.seqs && a.sq.cu[s + 1] <= t) s++;
     }
     const Seq q = load_seq(a.sq, s, a.c.page);
-    if (row >= all_rows || t < q.n0 || t >= q.n0 + min(q.n, a.max_tokens)) return;
+    if (row >= all_rows || t < q.n0 || t >= q.n0 + min(q.n, a.max_tokens)) return;           // W > 1: the whole block
     const int parts = visible_range(a, q, chunk).parts;
     if (parts == 1) return;
     float mx = -INFINITY;
@@ -405,19 +423,42 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
     float acc[PER], den = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; i++) acc[i] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < parts; p++) {
-        const float2 ml = a.part_ml[p * all_rows + row];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
-        den += ml.y * f;
-        const float* po = a.part_o + (p * all_rows + row) * D + lane * PER;
+    for (int p0 = w; p0 < parts; p0 += 32 * W) {              // lane i: weight of part p0 + W i
+        const int mine = p0 + W * lane;
+        float f = 0.f;
+        if (mine < parts) {
+            const float2 ml = a.part_ml[mine * all_rows + row];
+            f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+            den += ml.y * f;
+        }
+        const int here = min((parts - p0 + W - 1) / W, 32);
+#pragma unroll 8
+        for (int i = 0; i < here; i++) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (fi == 0.f) continue;                          // a part that saw nothing wrote no sums
+            const float* po = a.part_o + ((p0 + W * i) * all_rows + row) * D + lane * PER;
 #pragma unroll
-        for (int i = 0; i < PER; i++) acc[i] += (f == 0.f ? 0.f : po[i] * f);
+            for (int e = 0; e < PER; e++) acc[e] = fmaf(po[e], fi, acc[e]);
+        }
+    }
+    den = lane_sum<32>(den);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < PER; e++) s_acc[w][lane * PER + e] = acc[e];
+        if (lane == 0) s_den[w] = den;
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int u = 1; u < W; u++) {
+            den += s_den[u];
+#pragma unroll
+            for (int e = 0; e < PER; e++) acc[e] += s_acc[u][lane * PER + e];
+        }
     }
     const int h = (int)(row - (long long)t * a.heads);
 #pragma unroll
-    for (int i = 0; i < PER; i++)
-        store_out(a.out.data, (long long)t * a.out.ts + h * a.out.hs + lane * PER + i, den == 0.f ? 0.f : acc[i] / den, ot);
+    for (int e = 0; e < PER; e++)
+        store_out(a.out.data, (long long)t * a.out.ts + h * a.out.hs + lane * PER + e, den == 0.f ? 0.f : acc[e] / den, ot);
     if (lane == 0 && a.lse) a.lse[row] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
 }
 
@@ -457,13 +498,15 @@ cudaError_t run_attention_few(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArg
 }
 
 cudaError_t run_attention_join(int dim, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-    const long long grid = ((long long)a.sq.tokens * a.heads + JOIN_THREADS / 32 - 1) / (JOIN_THREADS / 32);
+    const long long rows = (long long)a.sq.tokens * a.heads;
+    const bool four = rows <= 152 * 16;                       // fewer rows than resident blocks: four warps for each
+    const long long grid = four ? rows : (rows + 3) / 4;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), b(JOIN_THREADS);
     switch (dim) {
-        case 64: return launch_pdl(join_kernel<64>, g, b, s, a, p.chunk, (int)ot);
-        case 128: return launch_pdl(join_kernel<128>, g, b, s, a, p.chunk, (int)ot);
-        case 256: return launch_pdl(join_kernel<256>, g, b, s, a, p.chunk, (int)ot);
+        case 64: return launch_pdl(four ? join_kernel<64, 4> : join_kernel<64, 1>, g, b, s, a, p.chunk, (int)ot);
+        case 128: return launch_pdl(four ? join_kernel<128, 4> : join_kernel<128, 1>, g, b, s, a, p.chunk, (int)ot);
+        case 256: return launch_pdl(four ? join_kernel<256, 4> : join_kernel<256, 1>, g, b, s, a, p.chunk, (int)ot);
     }
     return cudaErrorInvalidValue;
 }

@@ -120,6 +120,11 @@ __device__ __forceinline__ void tmem_wait64(uint32_t (&r)[64]) {
                  :
                  : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -273,6 +278,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                         r[q2][h][c] = at >= 0 ? ld_cache(codes + at + 8 * h * D + 64 * c) : make_uint4(0, 0, 0, 0);
             }
         };
+        // A barrier shows a phase's parity only, so a warp must not be two phases off.  It is not lapped, since its
+        // own unit completes the tile; and as stages are released in the order of the tiles, the wait for its unit
+        // before, at most kStages tiles back, shows that the phase before this one is complete.
+        static_assert((T_CONV_WARPS + UNITS - 1) / UNITS <= C::kStages, "a warp's units at most kStages tiles apart");
         int i = 0;
         lookup(w);
         if (w < units) load(w / UNITS, 0);
@@ -371,7 +380,6 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 if (!ok) break;
                 tc_fence_after();
                 product_s(0, j + 1);
-                release(x + 2);
             }
             ok = wait_tile(x + 1);
             if (!ok) break;
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             }
             if (!ok) break;
             release(x + 1);
-            if (NQ == 2 && more) release(x + 2);
+            if (more) release(x + 2);
         }
         if (elect_one()) umma_commit(bar.done());
         __syncwarp();
@@ -420,31 +428,46 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             // the scale goes into the row
             const long long at = tok * a.q.ts + hrow * a.q.hs;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.data) + at);
+            constexpr int HOLD = D == 256 ? 8 : D / 8;        // 16-byte words of the row held between the passes
+            uint4 raw[HOLD];
             float m = 0.f;
-#pragma unroll 8
-            for (int c = 0; c < D / 8; c++) {
-                float x[8];
-                unpack8(src[c], qt == MMQ_BF16, x);
 #pragma unroll
-                for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[e]));
+            for (int c0 = 0; c0 < D / 8; c0 += HOLD) {
+#pragma unroll
+                for (int c = 0; c < HOLD; c++) raw[c] = src[c0 + c];
+#pragma unroll
+                for (int c = 0; c < HOLD; c++) {
+                    float x[8];
+                    unpack8(raw[c], qt == MMQ_BF16, x);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[e]));
+                }
             }
             float up, down;
             row_scale(m, up, down);
             if (!real) up = 0.f;
             if (a.scale < 0.f) up = -up;
             rs = fabsf(a.scale) * LOG2E * down;
-#pragma unroll 8
-            for (int c = 0; c < D / 8; c++) {
-                float x[8];
-                unpack8(src[c], qt == MMQ_BF16, x);
-                uint32_t y[4];
 #pragma unroll
-                for (int e = 0; e < 2; e++) {                 // dimension order 0 2 1 3
-                    y[2 * e] = pack2(x[4 * e] * up, x[4 * e + 2] * up, __half());
-                    y[2 * e + 1] = pack2(x[4 * e + 1] * up, x[4 * e + 3] * up, __half());
+            for (int c0 = 0; c0 < D / 8; c0 += HOLD) {
+                if (HOLD < D / 8) {
+#pragma unroll
+                    for (int c = 0; c < HOLD; c++) raw[c] = src[c0 + c];
                 }
-                st_shared_v4(sb + C::q_off + i * C::kQBytes + (c / 8) * 16384 + sw128_off(r & 127, c % 8), y[0], y[1],
-                             y[2], y[3]);
+#pragma unroll
+                for (int cc = 0; cc < HOLD; cc++) {
+                    const int c = c0 + cc;
+                    float x[8];
+                    unpack8(raw[cc], qt == MMQ_BF16, x);
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {             // dimension order 0 2 1 3
+                        y[2 * e] = pack2(x[4 * e] * up, x[4 * e + 2] * up, __half());
+                        y[2 * e + 1] = pack2(x[4 * e + 1] * up, x[4 * e + 3] * up, __half());
+                    }
+                    st_shared_v4(sb + C::q_off + i * C::kQBytes + (c / 8) * 16384 + sw128_off(r & 127, c % 8), y[0],
+                                 y[1], y[2], y[3]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -492,11 +515,11 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
 #pragma unroll
             for (int k = 0; k < KT / 16; k++) {
                 const float* v = x + 16 * k;
-                float m0 = fmaxf(fmaxf(v[0], v[1]), v[2]), m1 = fmaxf(fmaxf(v[3], v[4]), v[5]);
-                float m2 = fmaxf(fmaxf(v[6], v[7]), v[8]), m3 = fmaxf(fmaxf(v[9], v[10]), v[11]);
-                m0 = fmaxf(fmaxf(m0, v[12]), v[13]);
-                m1 = fmaxf(fmaxf(m1, v[14]), v[15]);
-                m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]), m2 = max3(v[6], v[7], v[8]);
+                m0 = max3(m0, v[9], v[10]);
+                m1 = max3(m1, v[11], v[12]);
+                m2 = max3(m2, v[13], v[14]);
+                m0 = fmaxf(max3(m0, m1, m2), v[15]);
                 const float4 b = sc[k];
                 top = fmaxf(top, fmaf(m0, fmaxf(b.x * rs, F_FLOOR), b.y));
             }
