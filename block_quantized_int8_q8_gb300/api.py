@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -33,25 +34,12 @@ class MMQError(RuntimeError):
     pass
 
 
-class _Heads(ctypes.Structure):                  # mmq_heads
-    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
-
-
-class _Rotary(ctypes.Structure):                 # mmq_rotary
-    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_int64),
-                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
-
-
-class _Cache(ctypes.Structure):                  # mmq_kv_cache
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("block", ctypes.c_int32)]
-
-
-class _Seqs(ctypes.Structure):                   # mmq_kv_seqs
-    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
-                ("cu_tokens", ctypes.c_void_p), ("seqs", ctypes.c_int32)]
+# The structures of include/mmq.h as packed bytes, which ctypes passes by address (a ctypes.Structure takes three
+# times as long to fill, and these are made on every call).
+_HEADS = struct.Struct("@Pi4xqq")                # mmq_heads: data, dtype, token_stride, head_stride
+_ROTARY = struct.Struct("@PPqii")                # mmq_rotary: cos, sin, positions, rot_dim, interleaved
+_CACHE = struct.Struct("@PPPPqiiii")             # mmq_kv_cache: k, v, k_scale, v_scale, pages, kv_heads, head_dim, page_size, block
+_SEQS = struct.Struct("@PqPPi4x")                # mmq_kv_seqs: page_table, table_stride, kv_lens, cu_tokens, seqs
 
 
 def library_path() -> str:
@@ -98,7 +86,7 @@ def load():
     lib.mmq_gemm_id_noalloc.restype = I
     lib.mmq_read_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), P]
     lib.mmq_read_device_errors.restype = I
-    F = ctypes.c_float                           # structures are passed by address (ctypes.byref), as P
+    F = ctypes.c_float
     lib.mmq_qk_norm_rope.argtypes = [P, I, P, P, P, I, P, P, I64, I, P, P, F, P]
     lib.mmq_kv_append.argtypes = [P, P, I64, P, P, P, P, I, P, P, P, F, P]
     lib.mmq_kv_read.argtypes = [P, P, I64, P, P, P]
@@ -120,8 +108,11 @@ def _check(rc: int, what: str):
 
 
 def _stream(stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # the current stream's handle straight from the runtime: building torch's stream object for it takes 2.8 us
+    return stream.cuda_stream if stream is not None else _raw_stream(_current_device())
+
+
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -280,21 +271,19 @@ class KVCache:
     """One layer's 8-bit paged cache (mmq_kv_cache): int8 codes k, v [pages, kv_heads, page_size, head_dim] and f32
     scales k_scale, v_scale [pages, kv_heads, page_size / block].  Holds the given tensors; nothing is copied."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim", "block", "_c", "_ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim", "block", "_packed")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
-        if k.dtype != torch.int8 or v.dtype != torch.int8 or v.shape != k.shape:
+        shape, per = k.shape, k_scale.shape
+        if k.dtype != torch.int8 or v.dtype != torch.int8 or v.shape != shape or len(shape) != 4:
             raise MMQError("KVCache: k and v are int8 tensors of one shape [pages, kv_heads, page_size, head_dim]")
-        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or v_scale.shape != k_scale.shape or \
-                k_scale.shape[:2] != k.shape[:2] or k_scale.dim() != 3 or not k_scale.shape[2] or \
-                self.page_size % k_scale.shape[2]:
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim = shape
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or v_scale.shape != per or \
+                len(per) != 3 or per[0] != pages or per[1] != heads or not per[2] or page % per[2]:
             raise MMQError("KVCache: the scales are f32 tensors [pages, kv_heads, page_size / block]")
-        self.block = self.page_size // k_scale.shape[2]
+        self.block = page // per[2]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._c = _Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages, self.kv_heads, self.head_dim,
-                         self.page_size, self.block)
-        self._ref = ctypes.byref(self._c)
+        self._packed = _CACHE.pack(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, heads, dim, page, self.block)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 16, device="cuda"):
@@ -306,47 +295,58 @@ class KVCache:
         return cls(*codes, *scales)
 
 
-def _heads(t: torch.Tensor, what: str) -> _Heads:
-    if not t.is_cuda or t.dim() != 3 or t.dtype not in _DTYPES:
+def _heads(t: torch.Tensor, what: str) -> bytes:
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None or not t.is_cuda or t.dim() != 3:
         raise MMQError(f"{what}: expected a CUDA tensor [tokens, heads, head_dim] of f32, bf16 or f16")
     ts, hs, ds = t.stride()
-    if ds != 1 and t.shape[2] > 1:
+    if ds != 1:
         raise MMQError(f"{what}: the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), _DTYPES[t.dtype], ts, hs)
+    return _HEADS.pack(t.data_ptr(), dtype, ts, hs)
 
 
 def _typed(t: torch.Tensor | None, dtype, what: str) -> int | None:
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise MMQError(f"{what}: expected {dtype}")
     return _ptr(t)
 
 
 def _vector(t: torch.Tensor | None, n: int, what: str) -> int | None:
-    if t is not None and t.numel() != n:
+    if t is None:
+        return None
+    if t.numel() != n:
         raise MMQError(f"{what}: expected {n} values")
     return _typed(t, torch.float32, what)
 
 
-def _rotary(cos: torch.Tensor | None, sin: torch.Tensor | None, interleaved: bool):
+def _rotary(cos: torch.Tensor | None, sin: torch.Tensor | None, interleaved: bool) -> bytes | None:
     if cos is None and sin is None:
         return None
     if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
         raise MMQError("cos, sin: expected f32 tensors [positions, rot_dim / 2] of one shape")
-    r = _Rotary(_typed(cos, torch.float32, "cos"), _typed(sin, torch.float32, "sin"), cos.shape[0],
-                2 * cos.shape[1], 1 if interleaved else 0)
-    return ctypes.byref(r)
+    n, half = cos.shape
+    return _ROTARY.pack(_typed(cos, torch.float32, "cos"), _typed(sin, torch.float32, "sin"), n, 2 * half,
+                        1 if interleaved else 0)
 
 
-def _seqs(page_table: torch.Tensor, kv_lens: torch.Tensor, cu_tokens: torch.Tensor | None) -> _Seqs:
+def _seqs(page_table: torch.Tensor, kv_lens: torch.Tensor, cu_tokens: torch.Tensor | None) -> tuple[bytes, int]:
     n = kv_lens.numel()
     if page_table.dim() != 2 or page_table.shape[0] != n:
         raise MMQError("page_table: expected int32 [sequences, pages]")
     if cu_tokens is not None and cu_tokens.numel() != n + 1:
         raise MMQError("cu_tokens: expected int32 [sequences + 1]")
-    return _Seqs(_typed(page_table, torch.int32, "page_table"), page_table.shape[1],
-                 _typed(kv_lens, torch.int32, "kv_lens"), _typed(cu_tokens, torch.int32, "cu_tokens"), n)
+    return _SEQS.pack(_typed(page_table, torch.int32, "page_table"), page_table.shape[1],
+                      _typed(kv_lens, torch.int32, "kv_lens"), _typed(cu_tokens, torch.int32, "cu_tokens") or 0, n), n
+
+
+def _rows_out(like: torch.Tensor, out: torch.Tensor | None, dtype, what: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(like.shape, dtype=dtype or like.dtype, device=like.device)
+    if out.shape != like.shape:
+        raise MMQError(f"{what}: the output has another shape")
+    return out
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
@@ -361,25 +361,21 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     T, _, D = x.shape
     if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
         raise MMQError("qk_norm_rope: q and k differ in tokens or head_dim")
-    hq = hk = hqo = hko = None
-    if q is not None:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype or q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
-            raise MMQError("qk_norm_rope: q_out has another shape than q")
-        hq, hqo = ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(q_out, "q_out"))
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dtype or k.dtype, device=k.device)
-        elif k_out.shape != k.shape:
-            raise MMQError("qk_norm_rope: k_out has another shape than k")
-        hk, hko = ctypes.byref(_heads(k, "k")), ctypes.byref(_heads(k_out, "k_out"))
     if positions is not None and positions.numel() != T:
         raise MMQError("qk_norm_rope: expected a position for each token")
-    _check(load().mmq_qk_norm_rope(hq, q.shape[1] if q is not None else 0, _vector(q_weight, D, "q_weight"), hqo,
-                                   hk, k.shape[1] if k is not None else 0, _vector(k_weight, D, "k_weight"), hko, T, D,
-                                   _typed(positions, torch.int32, "positions"), _rotary(cos, sin, interleaved), eps,
-                                   _stream(stream)), "mmq_qk_norm_rope")
+    pq = pqo = pk = pko = None
+    if q is not None:
+        q_out = _rows_out(q, q_out, dtype, "qk_norm_rope")
+        pq, pqo = _heads(q, "q"), _heads(q_out, "q_out")
+    if k is not None:
+        k_out = _rows_out(k, k_out, dtype, "qk_norm_rope")
+        pk, pko = _heads(k, "k"), _heads(k_out, "k_out")
+    rc = load().mmq_qk_norm_rope(pq, q.shape[1] if pq else 0, _vector(q_weight, D, "q_weight"), pqo,
+                                 pk, k.shape[1] if pk else 0, _vector(k_weight, D, "k_weight"), pko, T, D,
+                                 _typed(positions, torch.int32, "positions"), _rotary(cos, sin, interleaved), eps,
+                                 _stream(stream))
+    if rc:
+        _check(rc, "mmq_qk_norm_rope")
     return q_out, k_out
 
 
@@ -394,20 +390,18 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torc
     T, H, D = k.shape
     if v.shape != k.shape or H != cache.kv_heads or D != cache.head_dim:
         raise MMQError("kv_append: k and v are [tokens, kv_heads, head_dim] of the cache")
-    hq = hqo = None
+    pq = pqo = None
     if q is not None:
         if q.shape[0] != T or q.shape[2] != D:
             raise MMQError("kv_append: q and k differ in tokens or head_dim")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
-            raise MMQError("kv_append: q_out has another shape than q")
-        hq, hqo = ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(q_out, "q_out"))
-    sq = _seqs(page_table, kv_lens, cu_tokens)
-    _check(load().mmq_kv_append(cache._ref, ctypes.byref(sq), T, ctypes.byref(_heads(k, "k")),
-                                ctypes.byref(_heads(v, "v")), _vector(k_weight, D, "k_weight"), hq,
-                                q.shape[1] if q is not None else 0, _vector(q_weight, D, "q_weight"), hqo,
-                                _rotary(cos, sin, interleaved), eps, _stream(stream)), "mmq_kv_append")
+        q_out = _rows_out(q, q_out, q_dtype, "kv_append")
+        pq, pqo = _heads(q, "q"), _heads(q_out, "q_out")
+    sq, _ = _seqs(page_table, kv_lens, cu_tokens)
+    rc = load().mmq_kv_append(cache._packed, sq, T, _heads(k, "k"), _heads(v, "v"), _vector(k_weight, D, "k_weight"),
+                              pq, q.shape[1] if pq else 0, _vector(q_weight, D, "q_weight"), pqo,
+                              _rotary(cos, sin, interleaved), eps, _stream(stream))
+    if rc:
+        _check(rc, "mmq_kv_append")
     return q_out
 
 
@@ -415,11 +409,12 @@ def kv_read(cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, tok
             cu_tokens: torch.Tensor | None = None, dtype=torch.bfloat16, stream=None):
     """The last cu_tokens[s+1] - cu_tokens[s] cached tokens of each sequence, `tokens` in all, as rows (k, v)
     [tokens, kv_heads, head_dim] of `dtype` (mmq_kv_read)."""
-    shape = (tokens, cache.kv_heads, cache.head_dim)
-    k, v = (torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
-    sq = _seqs(page_table, kv_lens, cu_tokens)
-    _check(load().mmq_kv_read(cache._ref, ctypes.byref(sq), tokens, ctypes.byref(_heads(k, "k")),
-                              ctypes.byref(_heads(v, "v")), _stream(stream)), "mmq_kv_read")
+    shape, device = (tokens, cache.kv_heads, cache.head_dim), cache.k.device
+    k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+    sq, _ = _seqs(page_table, kv_lens, cu_tokens)
+    rc = load().mmq_kv_read(cache._packed, sq, tokens, _heads(k, "k"), _heads(v, "v"), _stream(stream))
+    if rc:
+        _check(rc, "mmq_kv_read")
     return k, v
 
 
@@ -438,23 +433,23 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens
     T, H, D = q.shape
     if D != cache.head_dim:
         raise MMQError("attention: q has another head_dim than the cache")
-    sq = _seqs(page_table, kv_lens, cu_tokens)
+    sq, seqs = _seqs(page_table, kv_lens, cu_tokens)
     if max_kv_len is None:
         max_kv_len = page_table.shape[1] * cache.page_size
     if max_tokens is None:
         max_tokens = 1 if cu_tokens is None else T
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise MMQError("attention: out has another shape than q")
+    out = _rows_out(q, out, out_dtype, "attention")
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
     lib = load()
-    need = lib.mmq_attention_workspace_bytes(T, H, cache.kv_heads, D, sq.seqs, max_tokens, max_kv_len)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(lib.mmq_attention(ctypes.byref(_heads(q, "q")), H, cache._ref, ctypes.byref(sq), T, max_tokens, max_kv_len,
-                             D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-                             ctypes.byref(_heads(out, "out")), _ptr(lse), _ptr(workspace),
-                             workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                             _stream(stream)), "mmq_attention")
+    if workspace is None:
+        size = lib.mmq_attention_workspace_bytes(T, H, cache.kv_heads, D, seqs, max_tokens, max_kv_len)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    rc = lib.mmq_attention(_heads(q, "q"), H, cache._packed, sq, T, max_tokens, max_kv_len,
+                           D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _heads(out, "out"),
+                           lse.data_ptr() if return_lse else None, _ptr(workspace), size, _stream(stream))
+    if rc:
+        _check(rc, "mmq_attention")
     return (out, lse) if return_lse else out

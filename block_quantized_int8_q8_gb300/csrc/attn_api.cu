@@ -82,9 +82,11 @@ namespace mmq {
 
 // Few rows (new tokens x query heads of a key/value head <= 16) run on the few-row kernel, more on the tiled one.
 // The cache range is cut in chunks where the row blocks alone would not fill the GPU.
-//   few rows: all thread blocks do equal work on equal lengths, so the chunks are cut to make one wave; ragged lengths even out from 2048 tokens down.
-//   tiled: one thread block fits on an SM.  With B of them the last wave leaves SMs idle; cutting the range in c
-//     parts takes ceil(c B / 152) / c waves of the whole range's time, plus the join (about 3 % of a 512-token part).
+//   few rows: all thread blocks do equal work on equal lengths, so the chunks are cut to make one wave; ragged
+//     lengths even out from 2048 tokens down.
+//   tiled: one thread block fits on an SM, and its start and end cost about as much as six tiles, so a cut only
+//     pays where it turns idle SMs busy: as many parts as fit beside each other.  (128 blocks of 250 tiles each: 423 us
+//     whole, 455 us in two parts, 464 us in seven.)
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
                         long long max_kv) {
     AttnPlan p{};
@@ -101,13 +103,8 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
     } else {
         const int block = dim == 256 ? 128 : 256;
         const long long blocks = pairs * ((rows + block - 1) / block);
-        long long best = 1;
-        double cost = 1e30;
-        for (long long c = 1; c <= 32 && (c == 1 || max_kv / c >= 512); c++) {
-            const double t = (double)((c * blocks + SMS - 1) / SMS) / c * (c == 1 ? 1.0 : 1.02 + 16.0 * c / max_kv);
-            if (t < cost) cost = t, best = c;
-        }
-        chunk = ((max_kv + best - 1) / best + 127) / 128 * 128;
+        const long long parts = blocks < SMS ? SMS / blocks : 1;
+        chunk = ((max_kv + parts - 1) / parts + 127) / 128 * 128;
         if (chunk < 512) chunk = 512;
     }
     p.chunk = (int)chunk;

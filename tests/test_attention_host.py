@@ -1,7 +1,5 @@
 """Host-side checks of the attention operators' boundary (no GPU needed): refusals and sizes.  Arguments are refused
 before any CUDA call, so the pointers here are fake and never dereferenced."""
-import ctypes
-
 import pytest
 
 from block_quantized_int8_q8_gb300 import _build, api
@@ -18,23 +16,23 @@ def lib():
 
 
 def heads(data=FAKE, dtype=BF16, ts=1024, hs=128):
-    return api._Heads(data, dtype, ts, hs)
+    return api._HEADS.pack(data or 0, dtype, ts, hs)
 
 
 def cache(k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, pages=10, h=2, d=128, page=64, block=16):
-    return api._Cache(k, v, ks, vs, pages, h, d, page, block)
+    return api._CACHE.pack(k or 0, v or 0, ks or 0, vs or 0, pages, h, d, page, block)
 
 
 def seqs(table=FAKE, stride=4, lens=FAKE, cu=FAKE, n=3):
-    return api._Seqs(table, stride, lens, cu, n)
+    return api._SEQS.pack(table or 0, stride, lens or 0, cu or 0, n)
 
 
 def rotary(cos=FAKE, sin=FAKE, positions=100, rot=128, inter=0):
-    return api._Rotary(cos, sin, positions, rot, inter)
+    return api._ROTARY.pack(cos or 0, sin or 0, positions, rot, inter)
 
 
 def ref(x):
-    return None if x is None else ctypes.byref(x)
+    return x                                                  # packed structures go by address
 
 
 def norm_rope(lib, q=heads(), hq=4, qo=heads(), k=heads(), hk=2, ko=heads(), tokens=5, dim=128, pos=FAKE,
