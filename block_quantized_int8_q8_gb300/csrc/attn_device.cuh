@@ -68,43 +68,59 @@ inline cudaError_t launch_pdl_smem(void (*k)(Params...), dim3 grid, dim3 block, 
 }
 
 // ------------------------------------------------------------------------------------------ sequences
-// Largest s in [0, n) with key(s) <= x, for a non-decreasing key with key(0) <= x; every thread of the block
-// takes part (one round of loads for n up to the block size).
-template <int THREADS, typename Key>
-__device__ __forceinline__ int block_search(int n, long long x, Key key) {
-    int lo = 0, len = n;
-    while (len > 1) {
-        const int step = (len + THREADS - 1) / THREADS;
-        const int at = (int)threadIdx.x * step;
-        const int c = __syncthreads_count(at < len && key(lo + at) <= x);
-        const int skip = max(c - 1, 0) * step;
-        lo += skip;
-        len = min(step, len - skip);
-    }
-    return lo;
-}
-
-// New tokens and length of sequence s, held within the packed rows and the page table.
+// New tokens and length of a sequence, held within the packed rows and the page table.
 struct Seq {
     int n0, n;                 // first packed row, new tokens
     int len;                   // cached tokens as stated
     int end;                   // tokens the page table can hold, at most len
 };
-__device__ __forceinline__ Seq load_seq(const SeqArgs& a, int s, int page) {
+__device__ __forceinline__ Seq make_seq(const SeqArgs& a, int page, int n0, int n1, int len) {
     Seq q;
-    int n1;
-    if (a.cu) {
-        q.n0 = max(a.cu[s], 0);
-        n1 = min(a.cu[s + 1], a.tokens);
-    } else {
-        q.n0 = s;
-        n1 = s + 1;
-    }
-    q.n = max(n1 - q.n0, 0);
-    q.len = max(a.lens[s], 0);
+    q.n0 = max(n0, 0);
+    q.n = max(min(n1, a.tokens) - q.n0, 0);
+    q.len = max(len, 0);
     const long long cap = a.stride * page;
     q.end = (long long)q.len > cap ? (int)cap : q.len;
     return q;
+}
+__device__ __forceinline__ Seq load_seq(const SeqArgs& a, int s, int page) {
+    return a.cu ? make_seq(a, page, a.cu[s], a.cu[s + 1], a.lens[s]) : make_seq(a, page, s, s + 1, a.lens[s]);
+}
+
+// The largest s with key(cu[s], s) <= x, for a non-decreasing key with key of 0 <= x, and that sequence; every thread of
+// the block takes part.  Up to THREADS sequences in one round of loads, which brings the sequence's figures too; more by
+// a THREADS-fold narrowing.
+template <int THREADS, typename Key>
+__device__ __forceinline__ int find_seq(const SeqArgs& a, int page, long long x, Key key, Seq& q) {
+    __shared__ int s_seq[3];
+    if (a.seqs <= THREADS) {
+        const int i = threadIdx.x;
+        int c0 = 0, c1 = 0, len = 0;
+        if (i < a.seqs) {
+            c0 = a.cu[i];
+            c1 = a.cu[i + 1];
+            len = a.lens[i];
+        }
+        const int s = max(__syncthreads_count(i < a.seqs && key(c0, i) <= x) - 1, 0);
+        if (i == s) {
+            s_seq[0] = c0;
+            s_seq[1] = c1;
+            s_seq[2] = len;
+        }
+        __syncthreads();
+        q = make_seq(a, page, s_seq[0], s_seq[1], s_seq[2]);
+        return s;
+    }
+    int lo = 0, len = a.seqs;
+    while (len > 1) {
+        const int step = (len + THREADS - 1) / THREADS, at = (int)threadIdx.x * step;
+        const int c = __syncthreads_count(at < len && key(a.cu[lo + at], lo + at) <= x);
+        const int skip = max(c - 1, 0) * step;
+        lo += skip;
+        len = min(step, len - skip);
+    }
+    q = load_seq(a, lo, page);
+    return lo;
 }
 
 // ------------------------------------------------------------------------------------------ norm and rotation

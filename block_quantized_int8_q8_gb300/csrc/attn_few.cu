@@ -123,6 +123,14 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     __shared__ float s_rs[R], s_m[FEW_WARPS][R], s_l[FEW_WARPS][R];
     const int split = blockIdx.x % splits, rb = blockIdx.x / splits % row_blocks;
     const int sh = blockIdx.x / splits / row_blocks, head = sh % a.c.heads, s = sh / a.c.heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // Without a window this part starts at a place known before the sequence's length is: the page table entries of
+    // the warp's first 32 tiles are read together with it (within the row of the table; used only if in the range).
+    int early = -1;
+    if (a.window == 0) {
+        const int page = (split * (chunk / 16) + warp + FEW_WARPS * lane) * 16 / a.c.page;
+        if (page < a.sq.stride) early = a.sq.table[s * a.sq.stride + page];
+    }
     const Seq q = load_seq(a.sq, s, a.c.page);
     const int n = min(q.n, a.max_tokens), r0 = rb * R, rows = min(n * a.group - r0, R);
     if (rows <= 0) return;
@@ -136,8 +144,6 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     int t_begin = rg.tile0 + split * (chunk / 16), t_end = rg.tile0 + min(rg.tiles, (split + 1) * (chunk / 16));
     if (a.causal) t_end = min(t_end, (min(end, first + i1 + 1) + 15) / 16);
     if (a.window > 0) t_begin = max(t_begin, (first + i0 - a.window + 1) / 16);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-
     // this warp's tiles: t_begin + warp, + 4, ...; lane i looks up the place and the scales of the i-th of the next 32
     const int blocks = a.c.page / a.c.block;
     const int tiles = max((t_end - t_begin - warp + FEW_WARPS - 1) / FEW_WARPS, 0);
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
         src = 0, ks = 0.f, lv = -INFINITY, iv = 0.f;
         if (n0 + lane < tiles) {
             const int page = tok / a.c.page, off = tok - page * a.c.page;
-            const int pg = a.sq.table[s * a.sq.stride + page];
+            const int pg = n0 == 0 && a.window == 0 ? early : a.sq.table[s * a.sq.stride + page];
             if ((unsigned)pg < (unsigned long long)a.c.pages) {
                 const int ph = pg * a.c.heads + head;
                 src = ((long long)ph * a.c.page + off) * D;
@@ -408,11 +414,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
     const long long row = W > 1 ? row0 : row0 + warp;
     const int t = (int)(min(row, all_rows - 1) / a.heads);
     int s = t;
+    Seq q;
     if (a.sq.cu) {
-        s = block_search<JOIN_THREADS>(a.sq.seqs, row0 / a.heads, [&](int i) { return (long long)a.sq.cu[i]; });
-        while (s + 1 < a.sq.seqs && a.sq.cu[s + 1] <= t) s++;
+        s = find_seq<JOIN_THREADS>(a.sq, a.c.page, row0 / a.heads, [](int cu, int) { return (long long)cu; }, q);
+        if (t >= q.n0 + q.n) {
+            while (s + 1 < a.sq.seqs && a.sq.cu[s + 1] <= t) s++;
+            q = load_seq(a.sq, s, a.c.page);
+        }
+    } else {
+        q = load_seq(a.sq, s, a.c.page);
     }
-    const Seq q = load_seq(a.sq, s, a.c.page);
     if (row >= all_rows || t < q.n0 || t >= q.n0 + min(q.n, a.max_tokens)) return;           // W > 1: the whole block
     const int parts = visible_range(a, q, chunk).parts;
     if (parts == 1) return;

@@ -290,7 +290,7 @@ typedef struct {
 /* The sequences of a batch.  Sequence s has kv_lens[s] cached tokens, its new ones included; position p of it
  * lies in page page_table[s*table_stride + p/page_size].  Its new tokens are packed rows cu_tokens[s] ..
  * cu_tokens[s+1]-1 (cu_tokens int32 [seqs+1]; null: one token for each sequence) and are its last positions.
- * Page table entries past a sequence's length are not read. */
+ * Page table entries past a sequence's length are not used. */
 typedef struct {
     const int32_t* page_table;
     int64_t table_stride;          /* entries in a row of the table */
