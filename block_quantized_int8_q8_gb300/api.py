@@ -1,4 +1,5 @@
-"""Thin Python binding of libmmq_gb300.so (argument marshalling only).
+"""Thin Python binding of libmmq_gb300.so (argument marshalling only): ctypes, and for the attention operators, whose
+calls are too short for that, a C++ module (bind/attention.cpp).
 
 Every function forwards device pointers, sizes and the current CUDA stream to the C ABI declared in
 include/mmq.h; all arithmetic runs in the library's sm_103a kernels.  PyTorch is used only for device
@@ -8,8 +9,9 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -28,18 +30,11 @@ EXPORTS = ("mmq_status_string", "mmq_last_cuda_error", "mmq_q8_1_bytes", "mmq_we
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
 _lib = None
+_bind = None
 
 
 class MMQError(RuntimeError):
     pass
-
-
-# The structures of include/mmq.h as packed bytes, which ctypes passes by address (a ctypes.Structure takes three
-# times as long to fill, and these are made on every call).
-_HEADS = struct.Struct("@Pi4xqq")                # mmq_heads: data, dtype, token_stride, head_stride
-_ROTARY = struct.Struct("@PPqii")                # mmq_rotary: cos, sin, positions, rot_dim, interleaved
-_CACHE = struct.Struct("@PPPPqiiii")             # mmq_kv_cache: k, v, k_scale, v_scale, pages, kv_heads, head_dim, page_size, block
-_SEQS = struct.Struct("@PqPPi4x")                # mmq_kv_seqs: page_table, table_stride, kv_lens, cu_tokens, seqs
 
 
 def library_path() -> str:
@@ -86,7 +81,7 @@ def load():
     lib.mmq_gemm_id_noalloc.restype = I
     lib.mmq_read_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), P]
     lib.mmq_read_device_errors.restype = I
-    F = ctypes.c_float
+    F = ctypes.c_float                           # structures as P
     lib.mmq_qk_norm_rope.argtypes = [P, I, P, P, P, I, P, P, I64, I, P, P, F, P]
     lib.mmq_kv_append.argtypes = [P, P, I64, P, P, P, P, I, P, P, P, F, P]
     lib.mmq_kv_read.argtypes = [P, P, I64, P, P, P]
@@ -264,7 +259,20 @@ def selftest_bounded_wait(device="cuda", stream=None) -> list[int]:
 
 
 # ------------------------------------------------------------------------------- attention over the 8-bit cache
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+def _binding():
+    """The C++ half of this binding (bind/attention.cpp), which marshals the calls below."""
+    global _bind
+    if _bind is None:
+        load()
+        path = _build.BIND_LIB
+        if not os.path.exists(path):
+            raise MMQError(f"binding not built: {path} is missing (run __graft_entry__.build())")
+        loader = importlib.machinery.ExtensionFileLoader("_attention", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_attention", path, loader=loader))
+        loader.exec_module(module)
+        module.set_errors(MMQError, torch.OutOfMemoryError)
+        _bind = module
+    return _bind
 
 
 class KVCache:
@@ -274,16 +282,9 @@ class KVCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim", "block", "_packed")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        shape, per = k.shape, k_scale.shape
-        if k.dtype != torch.int8 or v.dtype != torch.int8 or v.shape != shape or len(shape) != 4:
-            raise MMQError("KVCache: k and v are int8 tensors of one shape [pages, kv_heads, page_size, head_dim]")
-        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim = shape
-        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or v_scale.shape != per or \
-                len(per) != 3 or per[0] != pages or per[1] != heads or not per[2] or page % per[2]:
-            raise MMQError("KVCache: the scales are f32 tensors [pages, kv_heads, page_size / block]")
-        self.block = page // per[2]
+        self._packed, self.pages, self.kv_heads, self.page_size, self.head_dim, self.block = \
+            (_bind or _binding()).make_cache(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._packed = _CACHE.pack(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, heads, dim, page, self.block)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 16, device="cuda"):
@@ -295,58 +296,8 @@ class KVCache:
         return cls(*codes, *scales)
 
 
-def _heads(t: torch.Tensor, what: str) -> bytes:
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None or not t.is_cuda or t.dim() != 3:
-        raise MMQError(f"{what}: expected a CUDA tensor [tokens, heads, head_dim] of f32, bf16 or f16")
-    ts, hs, ds = t.stride()
-    if ds != 1:
-        raise MMQError(f"{what}: the last dimension must be contiguous")
-    return _HEADS.pack(t.data_ptr(), dtype, ts, hs)
-
-
-def _typed(t: torch.Tensor | None, dtype, what: str) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise MMQError(f"{what}: expected {dtype}")
-    return _ptr(t)
-
-
-def _vector(t: torch.Tensor | None, n: int, what: str) -> int | None:
-    if t is None:
-        return None
-    if t.numel() != n:
-        raise MMQError(f"{what}: expected {n} values")
-    return _typed(t, torch.float32, what)
-
-
-def _rotary(cos: torch.Tensor | None, sin: torch.Tensor | None, interleaved: bool) -> bytes | None:
-    if cos is None and sin is None:
-        return None
-    if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
-        raise MMQError("cos, sin: expected f32 tensors [positions, rot_dim / 2] of one shape")
-    n, half = cos.shape
-    return _ROTARY.pack(_typed(cos, torch.float32, "cos"), _typed(sin, torch.float32, "sin"), n, 2 * half,
-                        1 if interleaved else 0)
-
-
-def _seqs(page_table: torch.Tensor, kv_lens: torch.Tensor, cu_tokens: torch.Tensor | None) -> tuple[bytes, int]:
-    n = kv_lens.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n:
-        raise MMQError("page_table: expected int32 [sequences, pages]")
-    if cu_tokens is not None and cu_tokens.numel() != n + 1:
-        raise MMQError("cu_tokens: expected int32 [sequences + 1]")
-    return _SEQS.pack(_typed(page_table, torch.int32, "page_table"), page_table.shape[1],
-                      _typed(kv_lens, torch.int32, "kv_lens"), _typed(cu_tokens, torch.int32, "cu_tokens") or 0, n), n
-
-
-def _rows_out(like: torch.Tensor, out: torch.Tensor | None, dtype, what: str) -> torch.Tensor:
-    if out is None:
-        return torch.empty(like.shape, dtype=dtype or like.dtype, device=like.device)
-    if out.shape != like.shape:
-        raise MMQError(f"{what}: the output has another shape")
-    return out
+def _handle(stream) -> int | None:
+    return None if stream is None else stream.cuda_stream
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None = None,
@@ -355,28 +306,8 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
                  q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, dtype=None, stream=None):
     """RMS norm of query and key heads [tokens, heads, head_dim] and position rotation in one pass
     (mmq_qk_norm_rope): (q_out, k_out), of `dtype` (default: the inputs').  q_out = q works in place."""
-    x = q if q is not None else k
-    if x is None:
-        raise MMQError("qk_norm_rope: neither q nor k given")
-    T, _, D = x.shape
-    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
-        raise MMQError("qk_norm_rope: q and k differ in tokens or head_dim")
-    if positions is not None and positions.numel() != T:
-        raise MMQError("qk_norm_rope: expected a position for each token")
-    pq = pqo = pk = pko = None
-    if q is not None:
-        q_out = _rows_out(q, q_out, dtype, "qk_norm_rope")
-        pq, pqo = _heads(q, "q"), _heads(q_out, "q_out")
-    if k is not None:
-        k_out = _rows_out(k, k_out, dtype, "qk_norm_rope")
-        pk, pko = _heads(k, "k"), _heads(k_out, "k_out")
-    rc = load().mmq_qk_norm_rope(pq, q.shape[1] if pq else 0, _vector(q_weight, D, "q_weight"), pqo,
-                                 pk, k.shape[1] if pk else 0, _vector(k_weight, D, "k_weight"), pko, T, D,
-                                 _typed(positions, torch.int32, "positions"), _rotary(cos, sin, interleaved), eps,
-                                 _stream(stream))
-    if rc:
-        _check(rc, "mmq_qk_norm_rope")
-    return q_out, k_out
+    return (_bind or _binding()).qk_norm_rope(q, k, positions, cos, sin, q_weight, k_weight, eps, interleaved, q_out,
+                                              k_out, dtype, _handle(stream))
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -387,35 +318,16 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torc
     """Quantize the new keys and values [tokens, kv_heads, head_dim] into the paged cache, normed and rotated on
     the way (mmq_kv_append).  kv_lens: cached tokens of each sequence, the new ones included.  Returns q_out (the
     queries normed and rotated in the same launch) where q is given."""
-    T, H, D = k.shape
-    if v.shape != k.shape or H != cache.kv_heads or D != cache.head_dim:
-        raise MMQError("kv_append: k and v are [tokens, kv_heads, head_dim] of the cache")
-    pq = pqo = None
-    if q is not None:
-        if q.shape[0] != T or q.shape[2] != D:
-            raise MMQError("kv_append: q and k differ in tokens or head_dim")
-        q_out = _rows_out(q, q_out, q_dtype, "kv_append")
-        pq, pqo = _heads(q, "q"), _heads(q_out, "q_out")
-    sq, _ = _seqs(page_table, kv_lens, cu_tokens)
-    rc = load().mmq_kv_append(cache._packed, sq, T, _heads(k, "k"), _heads(v, "v"), _vector(k_weight, D, "k_weight"),
-                              pq, q.shape[1] if pq else 0, _vector(q_weight, D, "q_weight"), pqo,
-                              _rotary(cos, sin, interleaved), eps, _stream(stream))
-    if rc:
-        _check(rc, "mmq_kv_append")
-    return q_out
+    return (_bind or _binding()).kv_append(cache._packed, k, v, page_table, kv_lens, cu_tokens, cos, sin, interleaved,
+                                           k_weight, eps, q, q_weight, q_out, q_dtype, _handle(stream))
 
 
 def kv_read(cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, tokens: int,
             cu_tokens: torch.Tensor | None = None, dtype=torch.bfloat16, stream=None):
     """The last cu_tokens[s+1] - cu_tokens[s] cached tokens of each sequence, `tokens` in all, as rows (k, v)
     [tokens, kv_heads, head_dim] of `dtype` (mmq_kv_read)."""
-    shape, device = (tokens, cache.kv_heads, cache.head_dim), cache.k.device
-    k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
-    sq, _ = _seqs(page_table, kv_lens, cu_tokens)
-    rc = load().mmq_kv_read(cache._packed, sq, tokens, _heads(k, "k"), _heads(v, "v"), _stream(stream))
-    if rc:
-        _check(rc, "mmq_kv_read")
-    return k, v
+    return (_bind or _binding()).kv_read(cache._packed, cache.k, page_table, kv_lens, tokens, cu_tokens, dtype,
+                                         _handle(stream))
 
 
 def attention_workspace_bytes(tokens: int, heads: int, kv_heads: int, head_dim: int, seqs: int, max_tokens: int,
@@ -430,26 +342,6 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens
     """softmax(scale q k^T) v over the 8-bit paged cache (mmq_attention): out [tokens, heads, head_dim], or
     (out, lse f32 [tokens, heads]).  max_kv_len and max_tokens bound a sequence's length and new tokens (default:
     what the page table holds; 1 without cu_tokens, else all tokens); scale defaults to head_dim ** -0.5."""
-    T, H, D = q.shape
-    if D != cache.head_dim:
-        raise MMQError("attention: q has another head_dim than the cache")
-    sq, seqs = _seqs(page_table, kv_lens, cu_tokens)
-    if max_kv_len is None:
-        max_kv_len = page_table.shape[1] * cache.page_size
-    if max_tokens is None:
-        max_tokens = 1 if cu_tokens is None else T
-    out = _rows_out(q, out, out_dtype, "attention")
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
-    lib = load()
-    if workspace is None:
-        size = lib.mmq_attention_workspace_bytes(T, H, cache.kv_heads, D, seqs, max_tokens, max_kv_len)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    else:
-        size = workspace.numel() * workspace.element_size()
-    rc = lib.mmq_attention(_heads(q, "q"), H, cache._packed, sq, T, max_tokens, max_kv_len,
-                           D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _heads(out, "out"),
-                           lse.data_ptr() if return_lse else None, _ptr(workspace), size, _stream(stream))
-    if rc:
-        _check(rc, "mmq_attention")
-    return (out, lse) if return_lse else out
+    return (_bind or _binding()).attention(q, cache._packed, page_table, kv_lens, max_kv_len, cu_tokens, max_tokens,
+                                           scale, causal, window, out, out_dtype, return_lse, workspace,
+                                           _handle(stream))

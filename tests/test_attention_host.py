@@ -1,9 +1,16 @@
 """Host-side checks of the attention operators' boundary (no GPU needed): refusals and sizes.  Arguments are refused
 before any CUDA call, so the pointers here are fake and never dereferenced."""
+import struct
+
 import pytest
 
 from block_quantized_int8_q8_gb300 import _build, api
 
+# the structures of include/mmq.h as packed bytes (ctypes passes bytes by address)
+HEADS = struct.Struct("@Pi4xqq")                              # data, dtype, token_stride, head_stride
+ROTARY = struct.Struct("@PPqii")                              # cos, sin, positions, rot_dim, interleaved
+CACHE = struct.Struct("@PPPPqiiii")                           # k, v, k_scale, v_scale, pages, kv_heads, head_dim, page_size, block
+SEQS = struct.Struct("@PqPPi4x")                              # page_table, table_stride, kv_lens, cu_tokens, seqs
 FAKE = 1 << 20
 INVALID, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4, 6
 F32, BF16, F16 = 0, 1, 2
@@ -16,19 +23,19 @@ def lib():
 
 
 def heads(data=FAKE, dtype=BF16, ts=1024, hs=128):
-    return api._HEADS.pack(data or 0, dtype, ts, hs)
+    return HEADS.pack(data or 0, dtype, ts, hs)
 
 
 def cache(k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, pages=10, h=2, d=128, page=64, block=16):
-    return api._CACHE.pack(k or 0, v or 0, ks or 0, vs or 0, pages, h, d, page, block)
+    return CACHE.pack(k or 0, v or 0, ks or 0, vs or 0, pages, h, d, page, block)
 
 
 def seqs(table=FAKE, stride=4, lens=FAKE, cu=FAKE, n=3):
-    return api._SEQS.pack(table or 0, stride, lens or 0, cu or 0, n)
+    return SEQS.pack(table or 0, stride, lens or 0, cu or 0, n)
 
 
 def rotary(cos=FAKE, sin=FAKE, positions=100, rot=128, inter=0):
-    return api._ROTARY.pack(cos or 0, sin or 0, positions, rot, inter)
+    return ROTARY.pack(cos or 0, sin or 0, positions, rot, inter)
 
 
 def ref(x):
