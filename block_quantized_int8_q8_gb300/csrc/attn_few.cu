@@ -7,13 +7,14 @@
 // The value scale enters the exponent, so that it costs nothing per value and the fp16 probabilities stay relative
 // to the largest term; O and l are f32.
 //
-// Bound by reading the cache.  Each warp takes tiles of 16 tokens straight from global memory into the registers of
-// the tensor-core fragments (no shared memory): the product S^T = K Q^T has 16 tokens as rows and 8 query rows as
-// columns, so a group of up to 8 query heads wastes nothing, and O^T = V^T P^T takes P^T from S^T by a transposing
-// register move.  Which head dimension a fragment element means is free as long as both operands agree, so
-// lanes read 16 contiguous bytes: K rows as quarters of 64 bytes, V rows as eighths.  int8 -> fp16 is exact (byte
-// spliced into the mantissa of 1024 + x).  The cache range is split over thread blocks in chunks; each thread block
-// joins its four warps in shared memory, a second launch joins the chunks.
+// Bound by reading the cache.  Each warp walks tiles of 16 tokens of its own: asynchronous 16-byte copies into a ring in
+// shared memory, two to five tiles ahead, then 16-byte reads straight into tensor-core fragments.  The product
+// S^T = K Q^T has 16 tokens as rows and 8 query rows as columns, so a group of up to 8 query heads wastes nothing,
+// and O^T = V^T P^T takes P^T from S^T by a transposing register move.  Which head dimension a fragment element means
+// is free as long as both operands agree, so lanes read contiguous bytes: K rows as quarters of 64 bytes, V rows as
+// eighths; the copies permute each row's 16-byte chunks so that neither read meets a bank twice.  int8 -> fp16 is exact
+// (byte spliced into the mantissa of 1024 + x).  The cache range is split over thread blocks in chunks; each thread
+// block joins its four warps in shared memory, a second launch joins the chunks.
 #include "attn_device.cuh"
 #include "attn_math.cuh"
 #include "internal.h"
@@ -46,11 +47,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint2 ld_cache8(const int8_t* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
 
 // Where dimension d of a row of partial sums lies in shared memory (padded so that a fragment's stores and a row's
 // reads fall on different banks).
@@ -60,48 +56,32 @@ template <int D> struct Pad {
     __device__ static int at(int d) { return d + (d >> kShift); }
 };
 
+// Shared memory: fp16 queries, the warps' rings, and over these at the end the warps' sums.
 template <int D, int NT> struct FewSmem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kQ = kRows * (D + 8) * 2;                                   // fp16 queries
-    static constexpr int kO = FEW_WARPS * kRows * Pad<D>::kPitch * 4;                // warps' sums (reuses kQ)
-    static constexpr int kBytes = kQ > kO ? kQ : kO;
+    static constexpr int kStages = D == 64 ? 6 : 3;                                  // 12 KB a warp (head_dim 256: 24)
+    static constexpr int kTile = 16 * D;                                             // bytes of a tile's K or V
+    static constexpr int kScale = kRows * (D + 8) * 2;
+    static constexpr int kRing = kScale + FEW_WARPS * kStages * 16;
+    static constexpr int kBytes = kRing + FEW_WARPS * kStages * 2 * kTile;
+    static_assert(FEW_WARPS * kRows * Pad<D>::kPitch * 4 <= kBytes - kRing, "the sums fit over the rings");
 };
 
-template <int D> struct KTile {              // two K rows of 16 tokens: 16-byte quarters of each 64 bytes
-    uint4 a[D / 64], b[D / 64];
-};
-template <int D> struct VTile {              // four V rows: D/8 bytes each
-    static constexpr int kWords = D / 32;
-    uint32_t w[4][kWords];
-};
-
-// kp, vp: this lane's first byte of the tile's K rows (row g, 16t) and V rows (row 2t, its eighth of the bytes).
-template <int D>
-__device__ __forceinline__ void load_k(const int8_t* kp, KTile<D>& k) {
-#pragma unroll
-    for (int c = 0; c < D / 64; c++) {
-        k.a[c] = ld_cache(kp + 64 * c);
-        k.b[c] = ld_cache(kp + 8 * D + 64 * c);
-    }
+// Where 16-byte chunk c of row r of a tile lies.  K is read as four neighbouring chunks of rows 2i, 2i+1 at a time, V as
+// the same one or two chunks of rows 0, 2, 4, 6 (or 1, 3, 5, 7).
+template <int D> __device__ __forceinline__ int k_at(int r, int c) {
+    return D == 64 ? r * 64 + c * 16 : r * D + ((c ^ ((r & 1) << 2)) << 4);
 }
-template <int D>
-__device__ __forceinline__ void load_v(const int8_t* vp, VTile<D>& v) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int8_t* p = vp + ((i & 1) + 8 * (i >> 1)) * D;
-        if constexpr (D == 64) {
-            const uint2 x = ld_cache8(p);
-            v.w[i][0] = x.x; v.w[i][1] = x.y;
-        } else {
-#pragma unroll
-            for (int c = 0; c < D / 128; c++) {
-                const uint4 x = ld_cache(p + 128 * c);
-                v.w[i][4 * c] = x.x; v.w[i][4 * c + 1] = x.y; v.w[i][4 * c + 2] = x.z; v.w[i][4 * c + 3] = x.w;
-            }
-        }
-    }
+template <int D> __device__ __forceinline__ int v_at(int r, int c) {
+    if (D == 64) return (r >> 1) * 128 + (((r & 1) ^ ((r >> 2) & 1)) << 6) + ((c ^ (r & 2)) << 4);
+    return r * D + ((c ^ (r & 6)) << 4);
 }
 
+__device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ float load_q(const void* p, long long i, bool bf16) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
                 : __half2float(static_cast<const __half*>(p)[i]);
@@ -168,16 +148,31 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             }
         }
     };
-    const int8_t* kbase = a.c.k + g * D + 16 * t;
-    const int8_t* vbase = a.c.v + 2 * t * D + (D == 64 ? 8 : 16) * g;
-    KTile<D> kt;
-    VTile<D> vt;
+    using M = FewSmem<D, NT>;
+    constexpr int ST = M::kStages;
+    float4* ring_scale = reinterpret_cast<float4*>(smem + M::kScale) + warp * ST;
+    uint8_t* ring = smem + M::kRing + warp * (ST * 2 * M::kTile);
+    // copies of tile x: lane -> chunk lane % (D/16) of rows lane / (D/16) + ...
+    constexpr int CHUNKS = D / 16, PASS = 32 / CHUNKS > 0 ? 32 / CHUNKS : 1;          // rows of one pass
+    const int cr = lane / CHUNKS, cc = lane % CHUNKS;
+    auto fetch = [&](int x) {
+        if (x < tiles) {
+            const int i = x & 31, slot = x % ST;
+            if (i == 0 && x > 0) lookup(x);
+            const long long at = __shfl_sync(0xffffffffu, src, i) + lane * 16;
+            if (lane == i) ring_scale[slot] = make_float4(ks, lv, iv, 0.f);
+            const uint32_t to = smem_u32(ring + slot * 2 * M::kTile);
+#pragma unroll
+            for (int r = 0; r < 16; r += PASS) {
+                cp_async_16(to + k_at<D>(r + cr, cc), a.c.k + at + r * D, 16);
+                cp_async_16(to + M::kTile + v_at<D>(r + cr, cc), a.c.v + at + r * D, 16);
+            }
+        }
+        cp_async_commit();
+    };
     lookup(0);
-    if (tiles > 0) {                                          // the first tile is on its way while the queries convert
-        const long long at = __shfl_sync(0xffffffffu, src, 0);
-        load_k<D>(kbase + at, kt);
-        load_v<D>(vbase + at, vt);
-    }
+#pragma unroll
+    for (int x = 0; x < ST - 1; x++) fetch(x);               // on their way while the queries convert
 
     // queries to fp16, each row times the power of two that brings its largest magnitude to [1, 2)
     __half* sq = reinterpret_cast<__half*>(smem);
@@ -236,9 +231,13 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             for (int e = 0; e < 4; e++) o[i][nt][e] = 0.f;
 
     for (int n = 0; n < tiles; n++) {
-        const int i = n & 31, tok = (t_begin + warp + FEW_WARPS * n) * 16;
-        const float ksc = __shfl_sync(0xffffffffu, ks, i), lvc = __shfl_sync(0xffffffffu, lv, i);
-        const float ivc = __shfl_sync(0xffffffffu, iv, i);
+        const int slot = n % ST, tok = (t_begin + warp + FEW_WARPS * n) * 16;
+        cp_async_wait<ST - 2>();
+        __syncwarp();                                         // every lane's copies of tile n are here, tile n-1 is read
+        fetch(n + ST - 1);
+        const uint32_t kv = smem_u32(ring + slot * 2 * M::kTile);
+        const float4 b = ring_scale[slot];
+        const float ksc = b.x, lvc = b.y, ivc = b.z;
         float sc[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
@@ -246,8 +245,8 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             for (int e = 0; e < 4; e++) sc[nt][e] = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 64; c++) {
-            const uint32_t wa[4] = {kt.a[c].x, kt.a[c].y, kt.a[c].z, kt.a[c].w};
-            const uint32_t wb[4] = {kt.b[c].x, kt.b[c].y, kt.b[c].z, kt.b[c].w};
+            const uint4 ka = ld_shared_u4(kv + k_at<D>(g, 4 * c + t)), kb = ld_shared_u4(kv + k_at<D>(g + 8, 4 * c + t));
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
             for (int w = 0; w < 4; w++) {
                 uint32_t a0, a1, a2, a3;
@@ -259,13 +258,6 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                     mma16816(sc[nt], a0, a1, a2, a3, f.x, f.y);
                 }
             }
-        }
-        // the registers of K are free: the next tile's loads start here, V's after its product
-        long long next = 0;
-        if (n + 1 < tiles) {
-            if (i == 31) lookup(n + 1);
-            next = __shfl_sync(0xffffffffu, src, (n + 1) & 31);
-            load_k<D>(kbase + next, kt);
         }
         const bool masked = tok + 15 > lim_all || tok < low_all;
         bool grow = false;
@@ -321,24 +313,41 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
         }
         // O^T += V^T P^T: fragment rows g, g+8 of product 2w+h are dimensions 4w + 2h, + 1 of this lane's bytes
+        constexpr int WORDS = D == 64 ? 2 : 4;                // words of one read: 8 or 16 bytes
 #pragma unroll
-        for (int w = 0; w < D / 32; w++) {
-            uint32_t a0, a1, a2, a3;
-            a0 = codes_across<0>(vt.w[0][w], vt.w[1][w]);
-            a1 = codes_across<1>(vt.w[0][w], vt.w[1][w]);
-            a2 = codes_across<0>(vt.w[2][w], vt.w[3][w]);
-            a3 = codes_across<1>(vt.w[2][w], vt.w[3][w]);
+        for (int c = 0; c < D / 32 / WORDS; c++) {
+            uint32_t vw[4][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-            a0 = codes_across<2>(vt.w[0][w], vt.w[1][w]);
-            a1 = codes_across<3>(vt.w[0][w], vt.w[1][w]);
-            a2 = codes_across<2>(vt.w[2][w], vt.w[3][w]);
-            a3 = codes_across<3>(vt.w[2][w], vt.w[3][w]);
+            for (int i = 0; i < 4; i++) {
+                const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+                if constexpr (D == 64) {
+                    const uint2 x = ld_shared_u2(kv + M::kTile + v_at<D>(row, g >> 1) + 8 * (g & 1));
+                    vw[i][0] = x.x; vw[i][1] = x.y;
+                } else {
+                    const uint4 x = ld_shared_u4(kv + M::kTile + v_at<D>(row, 8 * c + g));
+                    vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
+                }
+            }
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++) mma16816(o[2 * w + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            for (int w = 0; w < WORDS; w++) {
+                uint32_t a0, a1, a2, a3;
+                a0 = codes_across<0>(vw[0][w], vw[1][w]);
+                a1 = codes_across<1>(vw[0][w], vw[1][w]);
+                a2 = codes_across<0>(vw[2][w], vw[3][w]);
+                a3 = codes_across<1>(vw[2][w], vw[3][w]);
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) mma16816(o[2 * (WORDS * c + w)][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                a0 = codes_across<2>(vw[0][w], vw[1][w]);
+                a1 = codes_across<3>(vw[0][w], vw[1][w]);
+                a2 = codes_across<2>(vw[2][w], vw[3][w]);
+                a3 = codes_across<3>(vw[2][w], vw[3][w]);
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+                    mma16816(o[2 * (WORDS * c + w) + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
         }
-        if (n + 1 < tiles) load_v<D>(vbase + next, vt);
     }
+    cp_async_wait<0>();
 
     // join the warps: common maximum, scaled sums through shared memory
 #pragma unroll
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             }
         }
     __syncthreads();                                          // also: every warp has read its queries
-    float* so = reinterpret_cast<float*>(smem);
+    float* so = reinterpret_cast<float*>(smem + FewSmem<D, NT>::kRing);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
