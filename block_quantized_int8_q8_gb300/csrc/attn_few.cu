@@ -11,8 +11,8 @@
 // shared memory, two to five tiles ahead, then 16-byte reads straight into tensor-core fragments.  The product
 // S^T = K Q^T has 16 tokens as rows and 8 query rows as columns, so a group of up to 8 query heads wastes nothing,
 // and O^T = V^T P^T takes P^T from S^T by a transposing register move.  Which head dimension a fragment element means
-// is free as long as both operands agree, so lanes read contiguous bytes: K rows as quarters of 64 bytes, V rows as
-// eighths; the copies permute each row's 16-byte chunks so that neither read meets a bank twice.  int8 -> fp16 is exact
+// is free as long as both operands agree, so lanes read contiguous bytes: K rows as quarters of 64 bytes, V through
+// transposed reads; the copies permute each row's 16-byte chunks so that neither read meets a bank twice.  int8 -> fp16 is exact
 // (byte spliced into the mantissa of 1024 + x).  The cache range is split over thread blocks in chunks; each thread
 // block joins its four warps in shared memory, a second launch joins the chunks.
 #include "attn_device.cuh"
@@ -25,17 +25,6 @@ namespace {
 
 constexpr int FEW_WARPS = 4;
 constexpr int FEW_THREADS = FEW_WARPS * 32;
-// byte I of two words -> the fp16 pair (a_I, b_I), exactly
-template <int I>
-__device__ __forceinline__ uint32_t codes_across(uint32_t a, uint32_t b) {
-    const uint32_t bias = 0x64806480u;
-    uint32_t r;
-    const uint32_t x = __byte_perm(a, b, I | I << 4 | (4 + I) << 8 | (4 + I) << 12);
-    const uint32_t y = (x & 0x00FF00FFu) ^ bias;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(bias));
-    return r;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -48,13 +37,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Where dimension d of a row of partial sums lies in shared memory (padded so that a fragment's stores and a row's
-// reads fall on different banks).
-template <int D> struct Pad {
-    static constexpr int kShift = D == 64 ? 3 : 4;
-    static constexpr int kPitch = D + (D >> kShift) + 4;
-    __device__ static int at(int d) { return d + (d >> kShift); }
-};
+// Pitch of a row of partial sums in shared memory: a fragment's 8-byte stores (columns 2t, dimensions 2g) fall on
+// different banks.
+template <int D> constexpr int kSumPitch = D + 4;
 
 // Shared memory: fp16 queries, the warps' rings, and over these at the end the warps' sums.
 template <int D, int NT> struct FewSmem {
@@ -64,23 +49,23 @@ template <int D, int NT> struct FewSmem {
     static constexpr int kScale = kRows * (D + 8) * 2;
     static constexpr int kRing = kScale + FEW_WARPS * kStages * 16;
     static constexpr int kBytes = kRing + FEW_WARPS * kStages * 2 * kTile;
-    static_assert(FEW_WARPS * kRows * Pad<D>::kPitch * 4 <= kBytes - kRing, "the sums fit over the rings");
+    static_assert(FEW_WARPS * kRows * kSumPitch<D> * 4 <= kBytes - kRing, "the sums fit over the rings");
 };
 
 // Where 16-byte chunk c of row r of a tile lies.  K is read as four neighbouring chunks of rows 2i, 2i+1 at a time, V as
-// the same one or two chunks of rows 0, 2, 4, 6 (or 1, 3, 5, 7).
+// one chunk of eight rows.
 template <int D> __device__ __forceinline__ int k_at(int r, int c) {
     return D == 64 ? r * 64 + c * 16 : r * D + ((c ^ ((r & 1) << 2)) << 4);
 }
 template <int D> __device__ __forceinline__ int v_at(int r, int c) {
-    if (D == 64) return (r >> 1) * 128 + (((r & 1) ^ ((r >> 2) & 1)) << 6) + ((c ^ (r & 2)) << 4);
-    return r * D + ((c ^ (r & 6)) << 4);
+    return D == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * D + ((c ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
+// Four 8 x 16-byte matrices, transposed in 2-byte units: register i of lane (g, t) holds bytes 2g, 2g+1 of rows 2t and 2t+1
+// of matrix i, whose row r is at lane 8i + r's address.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ float load_q(const void* p, long long i, bool bf16) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
@@ -97,7 +82,6 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                                                           int qt, int ot) {
     pdl_trigger();
     pdl_wait();
-    using P = Pad<D>;
     constexpr int R = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_rs[R], s_m[FEW_WARPS][R], s_l[FEW_WARPS][R];
@@ -312,38 +296,19 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             pf[nt][0] = transpose8(pack2(p[0], p[1], __half()));
             pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
         }
-        // O^T += V^T P^T: fragment rows g, g+8 of product 2w+h are dimensions 4w + 2h, + 1 of this lane's bytes
-        constexpr int WORDS = D == 64 ? 2 : 4;                // words of one read: 8 or 16 bytes
+        // O^T += V^T P^T: a transposed read brings dimensions 2g, 2g+1 of 16-byte chunk c for tokens 2t, 2t+1 (and + 8);
+        // fragment rows g, g+8 of product c are dimensions 16c + 2g and + 1
 #pragma unroll
-        for (int c = 0; c < D / 32 / WORDS; c++) {
-            uint32_t vw[4][4];
+        for (int c = 0; c < D / 16; c += 2) {
+            uint32_t vw[4];
+            ldmatrix_trans(kv + M::kTile + v_at<D>(lane & 15, c + (lane >> 4)), vw);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-                if constexpr (D == 64) {
-                    const uint2 x = ld_shared_u2(kv + M::kTile + v_at<D>(row, g >> 1) + 8 * (g & 1));
-                    vw[i][0] = x.x; vw[i][1] = x.y;
-                } else {
-                    const uint4 x = ld_shared_u4(kv + M::kTile + v_at<D>(row, 8 * c + g));
-                    vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < WORDS; w++) {
+            for (int h = 0; h < 2; h++) {
                 uint32_t a0, a1, a2, a3;
-                a0 = codes_across<0>(vw[0][w], vw[1][w]);
-                a1 = codes_across<1>(vw[0][w], vw[1][w]);
-                a2 = codes_across<0>(vw[2][w], vw[3][w]);
-                a3 = codes_across<1>(vw[2][w], vw[3][w]);
+                codes_even_odd(vw[2 * h], a0, a1);
+                codes_even_odd(vw[2 * h + 1], a2, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) mma16816(o[2 * (WORDS * c + w)][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                a0 = codes_across<2>(vw[0][w], vw[1][w]);
-                a1 = codes_across<3>(vw[0][w], vw[1][w]);
-                a2 = codes_across<2>(vw[2][w], vw[3][w]);
-                a3 = codes_across<3>(vw[2][w], vw[3][w]);
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-                    mma16816(o[2 * (WORDS * c + w) + 1][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                for (int nt = 0; nt < NT; nt++) mma16816(o[c + h][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
             }
         }
     }
@@ -374,15 +339,10 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
 #pragma unroll
             for (int w = 1; w < FEW_WARPS; w++) mx = fmaxf(mx, s_m[w][r]);
             const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx);
-            float* row = so + (warp * R + r) * P::kPitch;
+            float* row = so + (warp * R + r) * kSumPitch<D> + 2 * g;
 #pragma unroll
-            for (int d = 0; d < D / 16; d++) {
-                // product d = 2w + h: word w of this lane's bytes (16 at 128c + 16g, or 8 at 8g), dimensions 2h, 2h + 1
-                const int w = d / 2, h = d % 2;
-                const int dim = (D == 64 ? 8 * g + 4 * w : 128 * (w / 4) + 16 * g + 4 * (w % 4)) + 2 * h;
-                row[P::at(dim)] = o[d][nt][e] * f;
-                row[P::at(dim + 1)] = o[d][nt][2 + e] * f;
-            }
+            for (int c = 0; c < D / 16; c++)
+                *reinterpret_cast<float2*>(row + 16 * c) = make_float2(o[c][nt][e] * f, o[c][nt][2 + e] * f);
         }
     __syncthreads();
     const long long all_rows = (long long)a.sq.tokens * a.heads;
@@ -394,7 +354,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
 #pragma unroll
         for (int w = 0; w < FEW_WARPS; w++) {
             den += s_l[w][r] * (s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - mx));
-            acc += so[(w * R + r) * P::kPitch + P::at(d)];
+            acc += so[(w * R + r) * kSumPitch<D> + d];
         }
         const long long tok = q.n0 + (r0 + r) / a.group;
         const int h = head * a.group + (r0 + r) % a.group;
