@@ -412,13 +412,29 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
             den += ml.y * f;
         }
         const int here = min((parts - p0 + W - 1) / W, 32);
-#pragma unroll 8
-        for (int i = 0; i < here; i++) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            if (fi == 0.f) continue;                          // a part that saw nothing wrote no sums
-            const float* po = a.part_o + ((p0 + W * i) * all_rows + row) * D + lane * PER;
+        for (int i0 = 0; i0 < here; i0 += 8) {                // eight parts' loads in flight
+            float x[8][PER], fi[8];
 #pragma unroll
-            for (int e = 0; e < PER; e++) acc[e] = fmaf(po[e], fi, acc[e]);
+            for (int i = 0; i < 8; i++) {
+                fi[i] = __shfl_sync(0xffffffffu, f, i0 + i);  // 0 past the last part
+                const long long part = min(p0 + W * (i0 + i), parts - 1);
+                const float* po = a.part_o + (part * all_rows + row) * D + lane * PER;
+                if constexpr (PER == 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(po);
+                    x[i][0] = v.x; x[i][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < PER; e += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(po + e);
+                        x[i][e] = v.x; x[i][e + 1] = v.y; x[i][e + 2] = v.z; x[i][e + 3] = v.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+#pragma unroll
+                for (int e = 0; e < PER; e++)                 // a part that saw nothing wrote no sums
+                    acc[e] = fmaf(fi[i] == 0.f ? 0.f : x[i][e], fi[i], acc[e]);
         }
     }
     den = lane_sum<32>(den);
