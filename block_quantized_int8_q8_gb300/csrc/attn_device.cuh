@@ -16,21 +16,39 @@ constexpr unsigned DEVERR_LENGTH = 32u;
 __device__ __forceinline__ void flag_error(unsigned bit) { atomicOr(&g_mmq_device_errors, bit); }
 
 // ------------------------------------------------------------------------------------------ typed rows
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// Four neighbouring values as two packed f32 pairs: the arithmetic on rows is packed throughout, since these operators
+// move so few bytes a value that plain instructions would bound them.
+using Quad = uint64_t[2];
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// the bytes as loaded (half the registers while a load is in flight), and their values
+template <typename T> struct RawOf { using type = uint2; };
+template <> struct RawOf<float> { using type = uint4; };
+template <typename T> using Raw = typename RawOf<T>::type;
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) { return *reinterpret_cast<const Raw<T>*>(p); }
+__device__ __forceinline__ void expand(const uint4& v, Quad& x, float) {
+    x[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ void load4(const __half* p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ void expand(const uint2& v, Quad& x, __nv_bfloat16) {
+    x[0] = f2_pack(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+    x[1] = f2_pack(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void expand(const uint2& v, Quad& x, __half) {
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+    x[0] = f2_pack(a.x, a.y);
+    x[1] = f2_pack(b.x, b.y);
 }
+__device__ __forceinline__ void load4(const float* p, Quad& x) { expand(load_raw(p), x, float()); }
 __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -39,16 +57,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ void store4(float* p, const Quad& x) {
+    *reinterpret_cast<float4*>(p) = make_float4(f2_lo(x[0]), f2_hi(x[0]), f2_lo(x[1]), f2_hi(x[1]));
 }
 template <typename T>
-__device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()));
+__device__ __forceinline__ void store4(T* p, const Quad& x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f2_lo(x[0]), f2_hi(x[0]), T()), pack2(f2_lo(x[1]), f2_hi(x[1]), T()));
 }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void store1(__half* p, float x) { *p = __float2half_rn(x); }
 
 // launch_pdl with dynamic shared memory.
 template <typename... Params, typename... Args>
@@ -156,35 +171,38 @@ __device__ __forceinline__ float lane_sum(float v) {
 
 // x / rms(x) * weight over the D values that D/8 lanes hold (unchanged where `on` is false; every lane takes part).
 template <int D>
-__device__ __forceinline__ void head_norm(float (&x0)[4], float (&x1)[4], const float (&w0)[4], const float (&w1)[4],
-                                          float eps, bool on = true) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) s += x0[i] * x0[i] + x1[i] * x1[i];
-    s = lane_sum<D / 8>(s);
+__device__ __forceinline__ void head_norm(Quad& x0, Quad& x1, const Quad& w0, const Quad& w1, float eps, bool on = true) {
+    const uint64_t s2 = f2_fma(x1[1], x1[1], f2_fma(x1[0], x1[0], f2_fma(x0[1], x0[1], f2_mul(x0[0], x0[0]))));
+    const float s = lane_sum<D / 8>(f2_lo(s2) + f2_hi(s2));
     const float r = on ? rsqrtf(s * (1.0f / D) + eps) : 1.0f;
+    const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        x0[i] = x0[i] * r * w0[i];
-        x1[i] = x1[i] * r * w1[i];
+    for (int i = 0; i < 2; i++) {
+        x0[i] = f2_mul(f2_mul(x0[i], r2), w0[i]);
+        x1[i] = f2_mul(f2_mul(x1[i], r2), w1[i]);
     }
 }
 
-__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
-    const float ra = a * c - b * s;
-    b = a * s + b * c;
-    a = ra;
-}
-__device__ __forceinline__ void head_turn(float (&x0)[4], float (&x1)[4], const float (&c)[4], const float (&s)[4],
-                                          bool interleaved) {
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+// (a, b) -> (a c - b s, a s + b c) for the lane's four pairs
+__device__ __forceinline__ void head_turn(Quad& x0, Quad& x1, const Quad& c, const Quad& s, bool interleaved) {
     if (interleaved) {
-        turn(x0[0], x0[1], c[0], s[0]);
-        turn(x0[2], x0[3], c[1], s[1]);
-        turn(x1[0], x1[1], c[2], s[2]);
-        turn(x1[2], x1[3], c[3], s[3]);
+        // each packed pair is (a, b):  (a, b) c + (b, a) (-s, s)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            uint64_t& x = i < 2 ? x0[i] : x1[i - 2];
+            const uint64_t cs = c[i >> 1], ss = s[i >> 1];
+            const float ci = i & 1 ? f2_hi(cs) : f2_lo(cs), si = i & 1 ? f2_hi(ss) : f2_lo(ss);
+            const uint64_t turned = f2_pack(f2_hi(x), f2_lo(x));
+            x = f2_fma(x, f2_pack(ci, ci), f2_mul(turned, f2_pack(-si, si)));
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) turn(x0[i], x1[i], c[i], s[i]);
+        for (int i = 0; i < 2; i++) {
+            const uint64_t a = x0[i], b = x1[i];
+            x0[i] = f2_fma(a, c[i], f2_neg(f2_mul(b, s[i])));
+            x1[i] = f2_fma(b, c[i], f2_mul(a, s[i]));
+        }
     }
 }
 

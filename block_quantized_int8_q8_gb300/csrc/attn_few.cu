@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
     const long long row0 = (long long)blockIdx.x * ROWS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = W > 1 ? warp : 0;
     const long long row = W > 1 ? row0 : row0 + warp;
-    const int t = (int)(min(row, all_rows - 1) / a.heads);
+    const int t = (unsigned)min(row, all_rows - 1) / (unsigned)a.heads;
     int s = t;
     Seq q;
     if (a.sq.cu) {

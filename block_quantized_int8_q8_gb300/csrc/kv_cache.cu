@@ -14,64 +14,67 @@ namespace mmq {
 namespace {
 
 // ------------------------------------------------------------------------------------------ norm_rope
-// One group of D/8 lanes takes HEADS heads of one token (their loads are in flight together; cos and sin are read
-// once for them).  Queries first, then keys, in units of HEADS heads of one side.
+// A block takes `count` tokens; a group of D/8 lanes takes units of NR_HEADS heads of one token (their loads are in flight
+// together; cos and sin are read once for them): queries first, then keys.
 constexpr int NR_THREADS = 256;
 constexpr int NR_HEADS = 4;
 
 template <int D, typename TI, typename TO>
-__global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRopeArgs a, int count) {
     pdl_wait();
     constexpr int LANES = D / 8, GROUPS = NR_THREADS / LANES;
-    const int uq = (a.q_heads + NR_HEADS - 1) / NR_HEADS, uk = (a.k_heads + NR_HEADS - 1) / NR_HEADS;
-    const long long unit = (long long)blockIdx.x * GROUPS + threadIdx.x / LANES;
-    const long long t64 = unit / (uq + uk);
-    const int u = (int)(unit - t64 * (uq + uk));
-    const bool active = t64 < a.tokens;
-    const int t = active ? (int)t64 : 0;
+    const int uq = (a.q_heads + NR_HEADS - 1) / NR_HEADS, per = uq + (a.k_heads + NR_HEADS - 1) / NR_HEADS;
+    const int t0 = blockIdx.x * count, units = min(count, a.tokens - t0) * per;
     const int l = threadIdx.x % LANES;
-    const int pos = active && a.rot.cos ? a.positions[t] : 0;
     const Chunks ch = head_chunks(l, a.rot.half, a.rot.interleaved);
-    const bool isq = u < uq;
-    const int h0 = (isq ? u : u - uq) * NR_HEADS;
-    int here = active ? min((isq ? a.q_heads : a.k_heads) - h0, NR_HEADS) : 0;
-    const HeadRows in = isq ? a.q : a.k, out = isq ? a.q_out : a.k_out;
-    const float* weight = isq ? a.q_weight : a.k_weight;
-    const TI* src = static_cast<const TI*>(in.data) + t * in.ts + h0 * in.hs;
-    TO* dst = static_cast<TO*>(out.data) + t * out.ts + h0 * out.hs;
-    float x0[NR_HEADS][4], x1[NR_HEADS][4];
+    // groups of lanes go over the units together, so that every lane takes part in the sums
+    for (int u0 = 0; u0 < units; u0 += GROUPS) {
+        const int unit = u0 + threadIdx.x / LANES, j = min(unit / per, count - 1), u = unit - j * per, t = min(t0 + j, a.tokens - 1);
+        const bool isq = u < uq;
+        const int h0 = (isq ? u : u - uq) * NR_HEADS;
+        int here = unit < units ? min((isq ? a.q_heads : a.k_heads) - h0, NR_HEADS) : 0;
+        const int pos = a.rot.cos ? a.positions[t] : 0;
+        const HeadRows in = isq ? a.q : a.k;
+        const TI* src = static_cast<const TI*>(in.data) + t * in.ts + h0 * in.hs;
+        Raw<TI> r0[NR_HEADS] = {}, r1[NR_HEADS] = {};
 #pragma unroll
-    for (int i = 0; i < NR_HEADS; i++) {
-#pragma unroll
-        for (int e = 0; e < 4; e++) x0[i][e] = x1[i][e] = 0.f;
-        if (i < here) {
-            load4(src + i * in.hs + ch.o0, x0[i]);
-            load4(src + i * in.hs + ch.o1, x1[i]);
+        for (int i = 0; i < NR_HEADS; i++) {
+            if (i < here) {
+                r0[i] = load_raw(src + ch.o0);
+                r1[i] = load_raw(src + ch.o1);
+            }
+            src += in.hs;
         }
-    }
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.rot.cos && (pos < 0 || pos >= a.rot.positions)) {
-        here = 0;                                             // not written
-        flag_error(DEVERR_POSITION);
-    } else if (active && ch.turn) {
-        load4(a.rot.cos + (long long)pos * a.rot.half + 4 * l, c);
-        load4(a.rot.sin + (long long)pos * a.rot.half + 4 * l, s);
-    }
-    if (a.q_weight || a.k_weight) {                          // uniform: the lanes of a warp may hold both sides
-        float w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
+        Quad c, s;
+        if (a.rot.cos && (pos < 0 || pos >= a.rot.positions)) {
+            if (here > 0) flag_error(DEVERR_POSITION);
+            here = 0;                                         // not written
+        } else if (ch.turn) {
+            load4(a.rot.cos + (long long)pos * a.rot.half + 4 * l, c);
+            load4(a.rot.sin + (long long)pos * a.rot.half + 4 * l, s);
+        }
+        const float* weight = isq ? a.q_weight : a.k_weight;
+        const bool norm = a.q_weight || a.k_weight;           // uniform: the lanes of a warp may hold both sides
+        const uint64_t one = f2_pack(1.f, 1.f);
+        Quad w0 = {one, one}, w1 = {one, one};
         if (weight) {
             load4(weight + ch.o0, w0);
             load4(weight + ch.o1, w1);
         }
+        const HeadRows out = isq ? a.q_out : a.k_out;
+        TO* dst = static_cast<TO*>(out.data) + t * out.ts + h0 * out.hs;
 #pragma unroll
-        for (int i = 0; i < NR_HEADS; i++) head_norm<D>(x0[i], x1[i], w0, w1, a.eps, weight != nullptr);
-    }
-#pragma unroll
-    for (int i = 0; i < NR_HEADS; i++) {
-        if (ch.turn) head_turn(x0[i], x1[i], c, s, a.rot.interleaved);
-        if (i < here) {
-            store4(dst + i * out.hs + ch.o0, x0[i]);
-            store4(dst + i * out.hs + ch.o1, x1[i]);
+        for (int i = 0; i < NR_HEADS; i++) {
+            Quad x0, x1;
+            expand(r0[i], x0, TI());
+            expand(r1[i], x1, TI());
+            if (norm) head_norm<D>(x0, x1, w0, w1, a.eps, weight != nullptr);
+            if (i < here) {
+                if (ch.turn) head_turn(x0, x1, c, s, a.rot.interleaved);
+                store4(dst + ch.o0, x0);
+                store4(dst + ch.o1, x1);
+            }
+            dst += out.hs;
         }
     }
 }
@@ -79,32 +82,47 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
 // ------------------------------------------------------------------------------------------ append
 // One thread block per (block of B tokens, head, key or value): the rows of the block stay in registers between
 // the largest magnitude and the codes, so the new rows are read once.  Blocks of the grid past those take the
-// queries.  A sequence of n new tokens touches at most n/B + 2 blocks; slot cu[s]/B + 2s is the first of sequence s,
-// so a block finds its sequence by a search and no list is built.
-template <int D> struct AppendShape {
-    static constexpr int kThreads = D == 256 ? 256 : 128;
+// queries.  A sequence of n new tokens touches at most n/B + 2 blocks, and at most n; slot cu[s]/B + 2s, or cu[s], is the
+// first of sequence s (whichever makes fewer slots), so a block finds its sequence by a search and no list is built.
+template <int D, int B> struct AppendShape {
     static constexpr int kLanes = D / 8;                    // lanes of one row
-    static constexpr int kRows = kThreads / kLanes;         // rows of one pass: 16, 8, 8
+    // two rows a thread, within 128 to 512 threads
+    static constexpr int kWant = B * kLanes / 2;
+    static constexpr int kThreads = kWant < 128 ? 128 : (kWant > 512 ? 512 : kWant);
+    static constexpr int kRows = kThreads / kLanes;         // rows of one pass
     static constexpr int kQHeads = 4;                       // query heads of one unit of a group of lanes
     static constexpr int kQTokens = 8;                      // most tokens of a block of queries
 };
 
-// The code of x for the scale d, in the low byte: round-half-even of the rounded quotient x/d.  t = x * inv, inv within
-// 2 ulp of 1/d, lies within 4.6e-5 of the rounded quotient for |x/d| <= 127.5, and a rounding to integers only
-// changes at half-integers: more than 1e-4 away from one, t rounds to the code; nearer, the quotient is formed.  Adding
-// 1.5 * 2^23 rounds to an integer and leaves its low bits in place.
-__device__ __forceinline__ uint32_t code_byte(float x, float d, float inv) {
+// The codes of four values for the scale d: round-half-even of the rounded quotients x/d.  t = x * inv, inv within 2 ulp
+// of 1/d, lies within 4.6e-5 of the rounded quotient for |x/d| <= 127.5, and a rounding to integers only changes at
+// half-integers: more than 1e-4 away from one, t rounds to the code; where one of the four is nearer, the quotients are
+// formed.  Adding 1.5 * 2^23 rounds to an integer and leaves its low byte in place.
+__device__ __forceinline__ uint32_t codes4(const Quad& x, float d, uint64_t inv2) {
     constexpr float MAGIC = 12582912.f;
-    const float t = __fmul_rn(x, inv);
-    float y = __fadd_rn(t, MAGIC);
-    if (!(fabsf(t - __fadd_rn(y, -MAGIC)) <= 0.4999f))
-        y = __fadd_rn(fminf(fmaxf(rintf(__fdiv_rn(x, d)), -127.f), 127.f), MAGIC);
-    return __float_as_uint(y);
-}
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float d, float inv) {
-    const uint32_t lo = __byte_perm(code_byte(x[0], d, inv), code_byte(x[1], d, inv), 0x0040);
-    const uint32_t hi = __byte_perm(code_byte(x[2], d, inv), code_byte(x[3], d, inv), 0x0040);
+    const uint64_t magic = f2_pack(MAGIC, MAGIC), unmagic = f2_pack(-MAGIC, -MAGIC);
+    uint64_t y[2], off[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint64_t t = f2_mul(x[i], inv2);
+        y[i] = f2_add(t, magic);
+        off[i] = f2_add(t, f2_neg(f2_add(y[i], unmagic)));
+    }
+    const float far = fmaxf(fmaxf(fabsf(f2_lo(off[0])), fabsf(f2_hi(off[0]))),
+                            fmaxf(fabsf(f2_lo(off[1])), fabsf(f2_hi(off[1]))));
+    if (!(far <= 0.4999f)) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            y[i] = f2_pack(__fadd_rn(fminf(fmaxf(rintf(__fdiv_rn(f2_lo(x[i]), d)), -127.f), 127.f), MAGIC),
+                           __fadd_rn(fminf(fmaxf(rintf(__fdiv_rn(f2_hi(x[i]), d)), -127.f), 127.f), MAGIC));
+    }
+    const uint32_t lo = __byte_perm((uint32_t)y[0], (uint32_t)(y[0] >> 32), 0x0040);
+    const uint32_t hi = __byte_perm((uint32_t)y[1], (uint32_t)(y[1] >> 32), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
+}
+__device__ __forceinline__ float largest(const Quad& x, float m) {
+    m = fmaxf(m, fmaxf(fabsf(f2_lo(x[0])), fabsf(f2_hi(x[0]))));
+    return fmaxf(m, fmaxf(fabsf(f2_lo(x[1])), fabsf(f2_hi(x[1]))));
 }
 __device__ __forceinline__ uint32_t scale_codes4(uint32_t w, float r) {
     uint32_t o = 0;
@@ -114,14 +132,15 @@ __device__ __forceinline__ uint32_t scale_codes4(uint32_t w, float r) {
 }
 
 template <int D, int B, typename T>
-__device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int head, bool isv) {
-    using S = AppendShape<D>;
+__device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int head, bool isv, bool by_token) {
+    using S = AppendShape<D, B>;
     constexpr int NR = (B + S::kRows - 1) / S::kRows;
     int s = slot, local = 0;
     Seq q;
     if (a.sq.cu) {
-        s = find_seq<S::kThreads>(a.sq, a.c.page, slot, [](int cu, int i) { return (long long)(cu / B) + 2ll * i; }, q);
-        local = slot - (q.n0 / B + 2 * s);
+        auto first = [=](int cu, int i) { return by_token ? (long long)cu : (long long)(cu / B) + 2ll * i; };
+        s = find_seq<S::kThreads>(a.sq, a.c.page, slot, first, q);
+        local = slot - (int)first(q.n0, s);
     } else {
         q = load_seq(a.sq, s, a.c.page);
     }
@@ -147,22 +166,26 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     const float* weight = isv ? nullptr : a.k_weight;
     const int l = threadIdx.x % S::kLanes, r0 = threadIdx.x / S::kLanes;
     const Chunks ch = head_chunks(l, rotate ? a.rot.half : 0, a.rot.interleaved);
-    float x0[NR][4], x1[NR][4];
+    Raw<T> in0[NR] = {}, in1[NR] = {};
     bool fill[NR];
 #pragma unroll
     for (int i = 0; i < NR; i++) {
         const int j = r0 + i * S::kRows, pos = b0 + j;
         fill[i] = j < B && pos >= p0 && pos < q.end;
-#pragma unroll
-        for (int e = 0; e < 4; e++) x0[i][e] = x1[i][e] = 0.f;
         if (fill[i]) {
             const T* p = static_cast<const T*>(in.data) + (long long)(q.n0 + pos - p0) * in.ts + head * in.hs;
-            load4(p + ch.o0, x0[i]);
-            load4(p + ch.o1, x1[i]);
+            in0[i] = load_raw(p + ch.o0);
+            in1[i] = load_raw(p + ch.o1);
         }
     }
+    Quad x0[NR], x1[NR];
+#pragma unroll
+    for (int i = 0; i < NR; i++) {
+        expand(in0[i], x0[i], T());
+        expand(in1[i], x1[i], T());
+    }
     if (weight) {
-        float w0[4], w1[4];
+        Quad w0, w1;
         load4(weight + ch.o0, w0);
         load4(weight + ch.o1, w1);
 #pragma unroll
@@ -176,17 +199,15 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
             if (pos >= a.rot.positions) {
                 fill[i] = false;
                 if (l == 0) flag_error(DEVERR_POSITION);
-#pragma unroll
-                for (int e = 0; e < 4; e++) x0[i][e] = x1[i][e] = 0.f;
+                x0[i][0] = x0[i][1] = x1[i][0] = x1[i][1] = 0ull;
             } else if (ch.turn) {
-                float c[4], sn[4];
+                Quad c, sn;
                 load4(a.rot.cos + (long long)pos * a.rot.half + 4 * l, c);
                 load4(a.rot.sin + (long long)pos * a.rot.half + 4 * l, sn);
                 head_turn(x0[i], x1[i], c, sn, a.rot.interleaved);
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; e++) amax = fmaxf(amax, fmaxf(fabsf(x0[i][e]), fabsf(x1[i][e])));
+        amax = largest(x1[i], largest(x0[i], amax));
     }
     // block-wide largest magnitude (the bits of non-negative floats order as integers)
     __shared__ unsigned s_amax[S::kThreads / 32];
@@ -201,14 +222,15 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     const float d = fmaxf(old, need);
     if (threadIdx.x == 0 && (fresh || d != old)) *scale = d;
     const float inv = __fdividef(1.f, d);
+    const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
     for (int i = 0; i < NR; i++) {
         const int j = r0 + i * S::kRows;
         uint32_t* p0w = reinterpret_cast<uint32_t*>(codes + j * D + ch.o0);
         uint32_t* p1w = reinterpret_cast<uint32_t*>(codes + j * D + ch.o1);
         if (fill[i]) {
-            *p0w = d > 0.f ? codes4(x0[i], d, inv) : 0u;
-            *p1w = d > 0.f ? codes4(x1[i], d, inv) : 0u;
+            *p0w = d > 0.f ? codes4(x0[i], d, inv2) : 0u;
+            *p1w = d > 0.f ? codes4(x1[i], d, inv2) : 0u;
         } else if (j < B && b0 + j < p0 && d != old) {
             const float r = __fdiv_rn(old, d);
             *p0w = scale_codes4(*p0w, r);
@@ -219,9 +241,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
 
 // Queries of QTOKENS packed rows (one for a decode step, whose latency counts): positions first, then units of kQHeads
 // heads of one token.
-template <int D, typename T>
+template <int D, int B, typename T>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int count, int qot) {
-    using S = AppendShape<D>;
+    using S = AppendShape<D, B>;
     constexpr int H = S::kQHeads;
     __shared__ int s_pos[S::kQTokens];
     Seq q;
@@ -248,7 +270,7 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
     __syncthreads();
     const int per = (a.q_heads + H - 1) / H, l = threadIdx.x % S::kLanes;
     const Chunks ch = head_chunks(l, a.rot.cos ? a.rot.half : 0, a.rot.interleaved);
-    float w0[4], w1[4];
+    Quad w0, w1;
     if (a.q_weight) {
         load4(a.q_weight + ch.o0, w0);
         load4(a.q_weight + ch.o1, w1);
@@ -259,54 +281,56 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
         const int pos = u < count * per ? s_pos[j] : -1;
         const int here = pos < 0 ? 0 : min(a.q_heads - h0, H);
         const T* src = static_cast<const T*>(a.q.data) + (long long)(t0 + j) * a.q.ts + h0 * a.q.hs;
-        float x0[H][4], x1[H][4], c[4], sn[4];
+        Raw<T> r0[H] = {}, r1[H] = {};
 #pragma unroll
         for (int i = 0; i < H; i++) {
-#pragma unroll
-            for (int e = 0; e < 4; e++) x0[i][e] = x1[i][e] = 0.f;
             if (i < here) {
-                load4(src + i * a.q.hs + ch.o0, x0[i]);
-                load4(src + i * a.q.hs + ch.o1, x1[i]);
+                r0[i] = load_raw(src + ch.o0);
+                r1[i] = load_raw(src + ch.o1);
             }
+            src += a.q.hs;
         }
+        Quad c, sn;
         if (a.rot.cos && ch.turn && here > 0) {
             load4(a.rot.cos + (long long)pos * a.rot.half + 4 * l, c);
             load4(a.rot.sin + (long long)pos * a.rot.half + 4 * l, sn);
         }
-        if (a.q_weight) {
-#pragma unroll
-            for (int i = 0; i < H; i++) head_norm<D>(x0[i], x1[i], w0, w1, a.eps);
-        }
+        long long at = (long long)(t0 + j) * a.q_out.ts + h0 * a.q_out.hs;
 #pragma unroll
         for (int i = 0; i < H; i++) {
-            if (i >= here) break;
-            if (a.rot.cos && ch.turn) head_turn(x0[i], x1[i], c, sn, a.rot.interleaved);
-            const long long at = (long long)(t0 + j) * a.q_out.ts + (h0 + i) * a.q_out.hs;
-            if (qot == MMQ_F32) {
-                store4(static_cast<float*>(a.q_out.data) + at + ch.o0, x0[i]);
-                store4(static_cast<float*>(a.q_out.data) + at + ch.o1, x1[i]);
-            } else if (qot == MMQ_BF16) {
-                store4(static_cast<__nv_bfloat16*>(a.q_out.data) + at + ch.o0, x0[i]);
-                store4(static_cast<__nv_bfloat16*>(a.q_out.data) + at + ch.o1, x1[i]);
-            } else {
-                store4(static_cast<__half*>(a.q_out.data) + at + ch.o0, x0[i]);
-                store4(static_cast<__half*>(a.q_out.data) + at + ch.o1, x1[i]);
+            Quad x0, x1;
+            expand(r0[i], x0, T());
+            expand(r1[i], x1, T());
+            if (a.q_weight) head_norm<D>(x0, x1, w0, w1, a.eps);
+            if (i < here) {
+                if (a.rot.cos && ch.turn) head_turn(x0, x1, c, sn, a.rot.interleaved);
+                if (qot == MMQ_F32) {
+                    store4(static_cast<float*>(a.q_out.data) + at + ch.o0, x0);
+                    store4(static_cast<float*>(a.q_out.data) + at + ch.o1, x1);
+                } else if (qot == MMQ_BF16) {
+                    store4(static_cast<__nv_bfloat16*>(a.q_out.data) + at + ch.o0, x0);
+                    store4(static_cast<__nv_bfloat16*>(a.q_out.data) + at + ch.o1, x1);
+                } else {
+                    store4(static_cast<__half*>(a.q_out.data) + at + ch.o0, x0);
+                    store4(static_cast<__half*>(a.q_out.data) + at + ch.o1, x1);
+                }
             }
+            at += a.q_out.hs;
         }
     }
 }
 
 template <int D, int B, typename T>
-__global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const AppendArgs a, long long kv_blocks,
-                                                                          int qtokens, int qot) {
+__global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(const AppendArgs a, unsigned kv_blocks,
+                                                                          bool by_token, int qtokens, int qot) {
     pdl_wait();
-    const long long b = blockIdx.x;
+    const unsigned b = blockIdx.x;
     if (b < kv_blocks) {
-        const int slot = (int)(b / (2 * a.c.heads)), w = (int)(b - (long long)slot * 2 * a.c.heads);
+        const int slot = b / (2u * a.c.heads), w = b - slot * 2u * a.c.heads;
         const bool isv = w >= a.c.heads;
-        append_block<D, B, T>(a, slot, isv ? w - a.c.heads : w, isv);
+        append_block<D, B, T>(a, slot, isv ? w - a.c.heads : w, isv, by_token);
     } else {
-        append_queries<D, T>(a, (int)(b - kv_blocks) * qtokens, qtokens, qot);
+        append_queries<D, B, T>(a, (int)(b - kv_blocks) * qtokens, qtokens, qot);
     }
 }
 
@@ -315,22 +339,36 @@ __global__ void __launch_bounds__(AppendShape<D>::kThreads) append_kernel(const 
 // a lane turns N codes into one 16-byte store.
 constexpr int READ_THREADS = 256;
 
-__device__ __forceinline__ void store_codes(float* p, uint32_t w, float d) {
-    float x[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) x[i] = (float)(int8_t)(w >> (8 * i)) * d;
+// four codes -> f32 exactly: the byte spliced into the mantissa of 2^23 + x
+__device__ __forceinline__ void codes_f32(uint32_t w, Quad& x) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint64_t bias = f2_pack(-8388736.f, -8388736.f);    // -(2^23 + 128)
+    x[0] = f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)),
+                          __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441))), bias);
+    x[1] = f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
+                          __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), bias);
+}
+__device__ __forceinline__ void store_codes(float* p, uint32_t w, uint64_t d2) {
+    Quad x;
+    codes_f32(w, x);
+    x[0] = f2_mul(x[0], d2);
+    x[1] = f2_mul(x[1], d2);
     store4(p, x);
 }
 template <typename T>
-__device__ __forceinline__ void store_codes(T* p, uint2 w, float d) {
-    float x[8];
+__device__ __forceinline__ void store_codes(T* p, uint2 w, uint64_t d2) {
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        x[i] = (float)(int8_t)(w.x >> (8 * i)) * d;
-        x[4 + i] = (float)(int8_t)(w.y >> (8 * i)) * d;
+    for (int h = 0; h < 2; h++) {
+        Quad x;
+        codes_f32(h ? w.y : w.x, x);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            x[i] = f2_mul(x[i], d2);
+            o[2 * h + i] = pack2(f2_lo(x[i]), f2_hi(x[i]), T());
+        }
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()),
-                                              pack2(x[6], x[7], T()));
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 template <typename T> struct ReadVec { using type = uint2; static constexpr int n = 8; };
 template <> struct ReadVec<float> { using type = uint32_t; static constexpr int n = 4; };
@@ -385,22 +423,31 @@ __global__ void __launch_bounds__(READ_THREADS) read_kernel(const ReadArgs a) {
     const long long page = s_page[j];
     if (page == -2) return;
     const int off = s_off[j], blocks = a.c.page / a.c.block;
-    const long long row0 = max(page, 0ll) * a.c.heads, code0 = (long long)off * D + N * l;
-    // units: key heads, then value heads
-    const bool hk = a.k_out.data != nullptr, hv = a.v_out.data != nullptr;
-    const int first = hk ? 0 : a.c.heads, units = hv ? 2 * a.c.heads : a.c.heads;
-#pragma unroll 8
-    for (int u = first + g / S::kTokens; u < units; u += S::kGroups / S::kTokens) {
-        const bool isv = u >= a.c.heads;
-        const int head = isv ? u - a.c.heads : u;
-        V w{};
-        float d = 0.f;
-        if (page >= 0) {
-            w = *reinterpret_cast<const V*>((isv ? a.c.v : a.c.k) + (row0 + head) * a.c.page * D + code0);
-            d = (isv ? a.c.vs : a.c.ks)[(row0 + head) * blocks + off / a.c.block];
+    // one side after the other; the group's heads a fixed distance apart in each
+    constexpr int STEP = S::kGroups / S::kTokens;
+    const int h0 = g / S::kTokens;
+    const long long row = max(page, 0ll) * a.c.heads + h0;
+    const long long code_step = (long long)STEP * a.c.page * D;
+#pragma unroll
+    for (int side = 0; side < 2; side++) {
+        const HeadRows& o = side ? a.v_out : a.k_out;
+        if (o.data == nullptr) continue;
+        const int8_t* src = (side ? a.c.v : a.c.k) + (row * a.c.page + off) * D + N * l;
+        const float* scale = (side ? a.c.vs : a.c.ks) + row * blocks + off / a.c.block;
+        T* dst = static_cast<T*>(o.data) + (long long)(t0 + j) * o.ts + h0 * o.hs + N * l;
+#pragma unroll 4
+        for (int h = h0; h < a.c.heads; h += STEP) {
+            V w{};
+            float d = 0.f;
+            if (page >= 0) {
+                w = *reinterpret_cast<const V*>(src);
+                d = *scale;
+            }
+            store_codes(dst, w, f2_pack(d, d));
+            src += code_step;
+            scale += STEP * blocks;
+            dst += STEP * o.hs;
         }
-        const HeadRows& o = isv ? a.v_out : a.k_out;
-        store_codes(static_cast<T*>(o.data) + (long long)(t0 + j) * o.ts + head * o.hs + N * l, w, d);
     }
 }
 
@@ -417,32 +464,32 @@ cudaError_t with_type(mmq_dtype t, F f) {
 
 template <int D>
 cudaError_t launch_norm_rope(mmq_dtype it, mmq_dtype ot, const NormRopeArgs& a, cudaStream_t s) {
-    constexpr int GROUPS = NR_THREADS / (D / 8);
-    const long long units = (long long)a.tokens *
-                            ((a.q_heads + NR_HEADS - 1) / NR_HEADS + (a.k_heads + NR_HEADS - 1) / NR_HEADS);
-    const long long grid = (units + GROUPS - 1) / GROUPS;
-    if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    // one token a block while that leaves room for more blocks, else four
+    const int count = a.tokens <= 8 * 152 ? 1 : 4;
+    const unsigned grid = (unsigned)((a.tokens + (long long)count - 1) / count);
     return with_type(it, [&](auto ti) {
         return with_type(ot, [&](auto to) {
             using TI = decltype(ti);
             using TO = decltype(to);
-            return launch_pdl(norm_rope_kernel<D, TI, TO>, dim3((unsigned)grid), dim3(NR_THREADS), s, a);
+            return launch_pdl(norm_rope_kernel<D, TI, TO>, dim3(grid), dim3(NR_THREADS), s, a, count);
         });
     });
 }
 
 template <int D, int B>
 cudaError_t launch_append(mmq_dtype t, mmq_dtype qot, const AppendArgs& a, cudaStream_t s) {
-    using S = AppendShape<D>;
-    const long long slots = a.sq.cu ? a.sq.tokens / B + 2ll * a.sq.seqs : a.sq.seqs;
+    using S = AppendShape<D, B>;
+    const long long by_blocks = a.sq.tokens / B + 2ll * a.sq.seqs;
+    const bool by_token = !a.sq.cu || a.sq.tokens <= by_blocks;      // (without offsets: one token for each sequence)
+    const long long slots = by_token ? a.sq.tokens : by_blocks;
     const long long kv = slots * 2 * a.c.heads;
     // one token a block while that leaves SMs idle, else eight
     const int qtokens = a.sq.tokens <= 8 * 152 ? 1 : S::kQTokens;
     const long long grid = kv + (a.q_heads > 0 ? ((long long)a.sq.tokens + qtokens - 1) / qtokens : 0);
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     return with_type(t, [&](auto ti) {
-        return launch_pdl(append_kernel<D, B, decltype(ti)>, dim3((unsigned)grid), dim3(S::kThreads), s, a, kv,
-                          qtokens, (int)qot);
+        return launch_pdl(append_kernel<D, B, decltype(ti)>, dim3((unsigned)grid), dim3(S::kThreads), s, a, (unsigned)kv,
+                          by_token, qtokens, (int)qot);
     });
 }
 
