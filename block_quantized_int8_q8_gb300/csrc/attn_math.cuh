@@ -50,25 +50,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, bool bf16, float (&x)[8]
         }
     }
 }
-__device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-}
-template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-        reinterpret_cast<uint4*>(p)[i] =
-            make_uint4(pack2(x[8 * i], x[8 * i + 1], T()), pack2(x[8 * i + 2], x[8 * i + 3], T()),
-                       pack2(x[8 * i + 4], x[8 * i + 5], T()), pack2(x[8 * i + 6], x[8 * i + 7], T()));
-}
-__device__ __forceinline__ void store16_typed(void* p, long long at, const float (&x)[16], int type) {
-    if (type == MMQ_F32) store16(static_cast<float*>(p) + at, x);
-    else if (type == MMQ_BF16) store16(static_cast<__nv_bfloat16*>(p) + at, x);
-    else store16(static_cast<__half*>(p) + at, x);
-}
-
 // The part of the cache that a sequence's rows can see, in tiles of 16 tokens, and its parts of `chunk` tokens.
 struct Range {
     int tile0, tiles, parts;

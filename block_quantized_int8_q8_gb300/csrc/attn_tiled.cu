@@ -416,52 +416,55 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         const int tokrow = (row0 + min(r, rows - 1)) / a.group;                   // new token
         const int hrow = head * a.group + (row0 + min(r, rows - 1)) % a.group;
         const long long tok = q.n0 + tokrow;
-        float rs;
+        constexpr int LPR = D / 8, RPS = 32 / LPR;            // lanes on a row, rows at a time, where rows move whole
+        const int sub = lane % LPR;
+        float rs = 0.f;
         {
-            // the row to fp16, times the power of two that brings its largest magnitude to [1, 2); the sign of
-            // the scale goes into the row
-            const long long at = tok * a.q.ts + hrow * a.q.hs;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.data) + at);
-            constexpr int HOLD = D == 256 ? 8 : D / 8;        // 16-byte words of the row held between the passes
-            uint4 raw[HOLD];
-            float m = 0.f;
-#pragma unroll
-            for (int c0 = 0; c0 < D / 8; c0 += HOLD) {
-#pragma unroll
-                for (int c = 0; c < HOLD; c++) raw[c] = src[c0 + c];
-#pragma unroll
-                for (int c = 0; c < HOLD; c++) {
-                    float x[8];
-                    unpack8(raw[c], qt == MMQ_BF16, x);
-#pragma unroll
-                    for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[e]));
-                }
+            // The warp's rows come whole by asynchronous copies, D/8 lanes on a row, to where the operand belongs; each
+            // thread then turns its row into fp16 in place, times the power of two that brings the row's largest
+            // magnitude to [1, 2) (the sign of the scale goes into the row).
+            const long long mine = (tok * a.q.ts + hrow * a.q.hs) * 2;
+            const uint8_t* src = static_cast<const uint8_t*>(a.q.data) + sub * 16;
+            const uint32_t tile = sb + C::q_off + i * C::kQBytes;
+#pragma unroll 8
+            for (int s0 = 0; s0 < 32; s0 += RPS) {
+                const int at = s0 + lane / LPR;               // row of the warp
+                cp_async_16(tile + (sub / 8) * 16384 + sw128_off((warp & 3) * 32 + at, sub % 8),
+                            src + __shfl_sync(0xffffffffu, mine, at), 16);
             }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncwarp();
+            // magnitudes order as the integers that their bits are, in both 16-bit types
+            unsigned big[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 8
+            for (int c = 0; c < D / 8; c++) {
+                const uint4 v = ld_shared_u4(tile + (c / 8) * 16384 + sw128_off(r & 127, c % 8));
+                big[0] = __vmaxu2(big[0], v.x & 0x7FFF7FFFu);
+                big[1] = __vmaxu2(big[1], v.y & 0x7FFF7FFFu);
+                big[2] = __vmaxu2(big[2], v.z & 0x7FFF7FFFu);
+                big[3] = __vmaxu2(big[3], v.w & 0x7FFF7FFFu);
+            }
+            const unsigned pair = __vmaxu2(__vmaxu2(big[0], big[1]), __vmaxu2(big[2], big[3]));
+            const unsigned short top = (unsigned short)max(pair & 0xFFFFu, pair >> 16);
+            const float m = qt == MMQ_BF16 ? __uint_as_float((unsigned)top << 16) : half_bits_to_float(top);
             float up, down;
             row_scale(m, up, down);
             if (!real) up = 0.f;
             if (a.scale < 0.f) up = -up;
             rs = fabsf(a.scale) * LOG2E * down;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; c++) {
+                const uint32_t place = tile + (c / 8) * 16384 + sw128_off(r & 127, c % 8);
+                float x[8];
+                unpack8(ld_shared_u4(place), qt == MMQ_BF16, x);
+                uint32_t y[4];
 #pragma unroll
-            for (int c0 = 0; c0 < D / 8; c0 += HOLD) {
-                if (HOLD < D / 8) {
-#pragma unroll
-                    for (int c = 0; c < HOLD; c++) raw[c] = src[c0 + c];
+                for (int e = 0; e < 2; e++) {                 // dimension order 0 2 1 3
+                    y[2 * e] = pack2(x[4 * e] * up, x[4 * e + 2] * up, __half());
+                    y[2 * e + 1] = pack2(x[4 * e + 1] * up, x[4 * e + 3] * up, __half());
                 }
-#pragma unroll
-                for (int cc = 0; cc < HOLD; cc++) {
-                    const int c = c0 + cc;
-                    float x[8];
-                    unpack8(raw[cc], qt == MMQ_BF16, x);
-                    uint32_t y[4];
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {             // dimension order 0 2 1 3
-                        y[2 * e] = pack2(x[4 * e] * up, x[4 * e + 2] * up, __half());
-                        y[2 * e + 1] = pack2(x[4 * e + 1] * up, x[4 * e + 3] * up, __half());
-                    }
-                    st_shared_v4(sb + C::q_off + i * C::kQBytes + (c / 8) * 16384 + sw128_off(r & 127, c % 8), y[0],
-                                 y[1], y[2], y[3]);
-                }
+                st_shared_v4(place, y[0], y[1], y[2], y[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -587,23 +590,57 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             const long long all_rows = (long long)a.sq.tokens * a.heads, row = tok * a.heads + hrow;
             const bool part = rg.parts > 1;
             const float f = part ? 1.f : inv;
+            // through shared memory (the queries' place, whose products are complete), so that rows are stored whole:
+            // D 16-bit values or D/2 f32 values of each row at a time
+            const bool wide = part || ot == MMQ_F32;
+            const uint32_t stage = sb + C::q_off + i * C::kQBytes + (warp & 3) * (32 * D * 2);
+            const long long mine = part ? (split * all_rows + row) * D * 4
+                                        : (tok * a.out.ts + hrow * a.out.hs) * (ot == MMQ_F32 ? 4 : 2);
+            uint8_t* dst = (part ? reinterpret_cast<uint8_t*>(a.part_o) : static_cast<uint8_t*>(a.out.data)) + sub * 16;
 #pragma unroll 1
-            for (int c = 0; c < D / 16; c++) {
-                uint32_t o[16];
-                if (!none) {
-                    tmem_ld16(to + 16 * c, o);
-                    tmem_ld_wait(o);
-                }
-                float x[16];
+            for (int d0 = 0; d0 < D; d0 += wide ? D / 2 : D) {
+#pragma unroll 4
+                for (int c = 0; c < (wide ? D / 32 : D / 16); c++) {              // 16 columns
+                    uint32_t o[16];
+                    if (!none) {
+                        tmem_ld16(to + d0 + 16 * c, o);
+                        tmem_ld_wait(o);
+                    }
+                    float x[16];
 #pragma unroll
-                for (int e = 0; e < 16; e++) {                // column order 0 2 1 3 undone
-                    const int d = (e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1);
-                    x[d] = none || f == 0.f ? 0.f : __uint_as_float(o[e]) * f;
+                    for (int e = 0; e < 16; e++) {            // column order 0 2 1 3 undone
+                        const int d = (e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1);
+                        x[d] = none || f == 0.f ? 0.f : __uint_as_float(o[e]) * f;
+                    }
+                    const uint32_t at = stage + lane * (D * 2);
+                    if (wide) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            st_shared_v4(at + (((4 * c + k) ^ (lane & 7)) << 4), __float_as_uint(x[4 * k]),
+                                         __float_as_uint(x[4 * k + 1]), __float_as_uint(x[4 * k + 2]),
+                                         __float_as_uint(x[4 * k + 3]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                y[e] = ot == MMQ_BF16 ? pack2(x[8 * k + 2 * e], x[8 * k + 2 * e + 1], __nv_bfloat16())
+                                                      : pack2(x[8 * k + 2 * e], x[8 * k + 2 * e + 1], __half());
+                            st_shared_v4(at + (((2 * c + k) ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
+                        }
+                    }
                 }
-                if (real) {
-                    if (part) store16(a.part_o + (split * all_rows + row) * D + 16 * c, x);
-                    else store16_typed(a.out.data, tok * a.out.ts + hrow * a.out.hs + 16 * c, x, ot);
+                __syncwarp();
+#pragma unroll 8
+                for (int s0 = 0; s0 < 32; s0 += RPS) {
+                    const int at = s0 + lane / LPR;
+                    const long long to_row = __shfl_sync(0xffffffffu, mine, at);
+                    if ((r & ~31) + at < rows)
+                        *reinterpret_cast<uint4*>(dst + to_row + (wide ? 4 * d0 : 0)) =
+                            ld_shared_u4(stage + at * (D * 2) + ((sub ^ (at & 7)) << 4));
                 }
+                __syncwarp();
             }
             if (real) {
                 if (part) a.part_ml[split * all_rows + row] = make_float2(l == 0.f ? -INFINITY : m, l);
