@@ -67,14 +67,11 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) 
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-__device__ __forceinline__ float load_q(const void* p, long long i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-                : __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void store_out(void* p, long long i, float x, int type) {
-    if (type == MMQ_F32) static_cast<float*>(p)[i] = x;
-    else if (type == MMQ_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
-    else static_cast<__half*>(p)[i] = __float2half_rn(x);
+__device__ __forceinline__ void store_out4(void* p, long long at, const float (&x)[4], int type) {
+    const Quad v = {f2_pack(x[0], x[1]), f2_pack(x[2], x[3])};
+    if (type == MMQ_F32) store4(static_cast<float*>(p) + at, v);
+    else if (type == MMQ_BF16) store4(static_cast<__nv_bfloat16*>(p) + at, v);
+    else store4(static_cast<__half*>(p) + at, v);
 }
 
 template <int D, int NT>
@@ -84,7 +81,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     pdl_wait();
     constexpr int R = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float s_rs[R], s_m[FEW_WARPS][R], s_l[FEW_WARPS][R];
+    __shared__ float s_rs[R], s_m[FEW_WARPS][R], s_l[FEW_WARPS][R], s_max[R], s_den[R], s_inv[R], s_lse[R];
     const int split = blockIdx.x % splits, rb = blockIdx.x / splits % row_blocks;
     const int sh = blockIdx.x / splits / row_blocks, head = sh % a.c.heads, s = sh / a.c.heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -160,24 +157,36 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
 
     // queries to fp16, each row times the power of two that brings its largest magnitude to [1, 2)
     __half* sq = reinterpret_cast<__half*>(smem);
-    constexpr int PER = D / 16;
+    constexpr int PER = D / 16;                               // values of a row for each of 16 lanes
     for (int r = threadIdx.x / 16; r < R; r += FEW_THREADS / 16) {
         const int l = threadIdx.x % 16;
-        float x[PER], m = 0.f;
-        const long long at = r < rows ? (long long)(q.n0 + (r0 + r) / a.group) * a.q.ts +
-                                            (long long)(head * a.group + (r0 + r) % a.group) * a.q.hs + l * PER
-                                      : 0;
+        uint2 raw[PER / 4] = {};
+        if (r < rows) {
+            const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q.data) +
+                                                            (long long)(q.n0 + (r0 + r) / a.group) * a.q.ts +
+                                                            (long long)(head * a.group + (r0 + r) % a.group) * a.q.hs + l * PER);
 #pragma unroll
-        for (int i = 0; i < PER; i++) {
-            x[i] = r < rows ? load_q(a.q.data, at + i, qt == MMQ_BF16) : 0.f;
-            m = fmaxf(m, fabsf(x[i]));
+            for (int i = 0; i < PER / 4; i++) raw[i] = p[i];
+        }
+        float x[PER], m = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER / 4; i++) {
+            Quad v;
+            if (qt == MMQ_BF16) expand(raw[i], v, __nv_bfloat16());
+            else expand(raw[i], v, __half());
+            x[4 * i] = f2_lo(v[0]); x[4 * i + 1] = f2_hi(v[0]); x[4 * i + 2] = f2_lo(v[1]); x[4 * i + 3] = f2_hi(v[1]);
+#pragma unroll
+            for (int e = 0; e < 4; e++) m = fmaxf(m, fabsf(x[4 * i + e]));
         }
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float up, down;
         row_scale(m, up, down);
+        uint2* to = reinterpret_cast<uint2*>(sq + r * (D + 8) + l * PER);
 #pragma unroll
-        for (int i = 0; i < PER; i++) sq[r * (D + 8) + l * PER + i] = __float2half_rn(x[i] * up);
+        for (int i = 0; i < PER / 4; i++)
+            to[i] = make_uint2(pack2(x[4 * i] * up, x[4 * i + 1] * up, __half()),
+                               pack2(x[4 * i + 2] * up, x[4 * i + 3] * up, __half()));
         if (l == 0) s_rs[r] = a.scale * LOG2E * down;
     }
     __syncthreads();
@@ -329,6 +338,18 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             }
         }
     __syncthreads();                                          // also: every warp has read its queries
+    if (threadIdx.x < R) {
+        const int r = threadIdx.x;
+        float mx = s_m[0][r], den = 0.f;
+#pragma unroll
+        for (int w = 1; w < FEW_WARPS; w++) mx = fmaxf(mx, s_m[w][r]);
+#pragma unroll
+        for (int w = 0; w < FEW_WARPS; w++) den += s_l[w][r] * (s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - mx));
+        s_max[r] = mx;
+        s_den[r] = den;
+        s_inv[r] = den == 0.f ? 0.f : 1.f / den;
+        s_lse[r] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
+    }
     float* so = reinterpret_cast<float*>(smem + FewSmem<D, NT>::kRing);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
@@ -345,26 +366,29 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                 *reinterpret_cast<float2*>(row + 16 * c) = make_float2(o[c][nt][e] * f, o[c][nt][2 + e] * f);
         }
     __syncthreads();
+    // four values of a row at a time; the rows' statistics by the first threads
     const long long all_rows = (long long)a.sq.tokens * a.heads;
-    for (int i = threadIdx.x; i < rows * D; i += FEW_THREADS) {
-        const int r = i / D, d = i - r * D;
-        float mx = s_m[0][r], den = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 1; w < FEW_WARPS; w++) mx = fmaxf(mx, s_m[w][r]);
+    const bool whole = rg.parts == 1;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += FEW_THREADS) {
+        const int r = i / (D / 4), d = 4 * (i % (D / 4));
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < FEW_WARPS; w++) {
-            den += s_l[w][r] * (s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - mx));
-            acc += so[(w * R + r) * kSumPitch<D> + d];
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * R + r) * kSumPitch<D> + d);
+            acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
         }
         const long long tok = q.n0 + (r0 + r) / a.group;
         const int h = head * a.group + (r0 + r) % a.group;
-        if (rg.parts == 1) {
-            store_out(a.out.data, tok * a.out.ts + h * a.out.hs + d, den == 0.f ? 0.f : acc / den, ot);
-            if (d == 0 && a.lse) a.lse[tok * a.heads + h] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
+        if (whole) {
+            const float f = s_inv[r];
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[e] = f == 0.f ? 0.f : acc[e] * f;
+            store_out4(a.out.data, tok * a.out.ts + h * a.out.hs + d, acc, ot);
+            if (d == 0 && a.lse) a.lse[tok * a.heads + h] = s_lse[r];
         } else {
             const long long row = split * all_rows + tok * a.heads + h;
-            a.part_o[row * D + d] = acc;
-            if (d == 0) a.part_ml[row] = make_float2(mx, den);
+            *reinterpret_cast<float4*>(a.part_o + row * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (d == 0) a.part_ml[row] = make_float2(s_max[r], s_den[r]);
         }
     }
 }
@@ -452,9 +476,21 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
         }
     }
     const int h = (int)(row - (long long)t * a.heads);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const long long at = (long long)t * a.out.ts + h * a.out.hs + lane * PER;
+    if constexpr (PER == 2) {
+        const float x0 = inv == 0.f ? 0.f : acc[0] * inv, x1 = inv == 0.f ? 0.f : acc[1] * inv;
+        if (ot == MMQ_F32) *reinterpret_cast<float2*>(static_cast<float*>(a.out.data) + at) = make_float2(x0, x1);
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out.data) + at) =
+            ot == MMQ_BF16 ? pack2(x0, x1, __nv_bfloat16()) : pack2(x0, x1, __half());
+    } else {
 #pragma unroll
-    for (int e = 0; e < PER; e++)
-        store_out(a.out.data, (long long)t * a.out.ts + h * a.out.hs + lane * PER + e, den == 0.f ? 0.f : acc[e] / den, ot);
+        for (int e = 0; e < PER; e += 4) {
+            const float x[4] = {inv == 0.f ? 0.f : acc[e] * inv, inv == 0.f ? 0.f : acc[e + 1] * inv,
+                                inv == 0.f ? 0.f : acc[e + 2] * inv, inv == 0.f ? 0.f : acc[e + 3] * inv};
+            store_out4(a.out.data, at + e, x, ot);
+        }
+    }
     if (lane == 0 && a.lse) a.lse[row] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
 }
 
