@@ -8,7 +8,7 @@
 // to the largest term; O and l are f32.
 //
 // Bound by reading the cache.  Each warp walks tiles of 16 tokens of its own: asynchronous 16-byte copies into a ring in
-// shared memory, two to five tiles ahead, then 16-byte reads straight into tensor-core fragments.  The product
+// shared memory, two steps ahead, then 16-byte reads straight into tensor-core fragments.  The product
 // S^T = K Q^T has 16 tokens as rows and 8 query rows as columns, so a group of up to 8 query heads wastes nothing,
 // and O^T = V^T P^T takes P^T from S^T by a transposing register move.  Which head dimension a fragment element means
 // is free as long as both operands agree, so lanes read contiguous bytes: K rows as quarters of 64 bytes, V through
@@ -44,11 +44,12 @@ template <int D> constexpr int kSumPitch = D + 4;
 // Shared memory: fp16 queries, the warps' rings, and over these at the end the warps' sums.
 template <int D, int NT> struct FewSmem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kStages = D == 64 ? 6 : 3;                                  // 12 KB a warp (head_dim 256: 24)
+    static constexpr int kStep = D == 64 ? 2 : 1;                                    // tiles of 16 tokens taken at once
+    static constexpr int kStages = 3;                                                // 12 KB a warp (head_dim 256: 24)
     static constexpr int kTile = 16 * D;                                             // bytes of a tile's K or V
     static constexpr int kScale = kRows * (D + 8) * 2;
-    static constexpr int kRing = kScale + FEW_WARPS * kStages * 16;
-    static constexpr int kBytes = kRing + FEW_WARPS * kStages * 2 * kTile;
+    static constexpr int kRing = kScale + FEW_WARPS * kStages * kStep * 16;
+    static constexpr int kBytes = kRing + FEW_WARPS * kStages * kStep * 2 * kTile;
     static_assert(FEW_WARPS * kRows * kSumPitch<D> * 4 <= kBytes - kRing, "the sums fit over the rings");
 };
 
@@ -79,7 +80,8 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                                                           int qt, int ot) {
     pdl_trigger();
     pdl_wait();
-    constexpr int R = 8 * NT;
+    using M = FewSmem<D, NT>;
+    constexpr int R = 8 * NT, U = M::kStep, ST = M::kStages;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_rs[R], s_m[FEW_WARPS][R], s_l[FEW_WARPS][R], s_max[R], s_den[R], s_inv[R], s_lse[R];
     const int split = blockIdx.x % splits, rb = blockIdx.x / splits % row_blocks;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     // the warp's first 32 tiles are read together with it (within the row of the table; used only if in the range).
     int early = -1;
     if (a.window == 0) {
-        const int page = (split * (chunk / 16) + warp + FEW_WARPS * lane) * 16 / a.c.page;
+        const int page = (split * (chunk / 16) + (warp + FEW_WARPS * (lane / U)) * U + lane % U) * 16 / a.c.page;
         if (page < a.sq.stride) early = a.sq.table[s * a.sq.stride + page];
     }
     const Seq q = load_seq(a.sq, s, a.c.page);
@@ -105,15 +107,16 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     int t_begin = rg.tile0 + split * (chunk / 16), t_end = rg.tile0 + min(rg.tiles, (split + 1) * (chunk / 16));
     if (a.causal) t_end = min(t_end, (min(end, first + i1 + 1) + 15) / 16);
     if (a.window > 0) t_begin = max(t_begin, (first + i0 - a.window + 1) / 16);
-    // this warp's tiles: t_begin + warp, + 4, ...; lane i looks up the place and the scales of the i-th of the next 32
+    // this warp's steps of U tiles: the first at t_begin + U warp, the next 4U on; lane i looks up the place and the scales
+    // of the i-th of the warp's next 32 tiles
     const int blocks = a.c.page / a.c.block;
-    const int tiles = max((t_end - t_begin - warp + FEW_WARPS - 1) / FEW_WARPS, 0);
+    const int steps = max((t_end - t_begin - U * warp + U * FEW_WARPS - 1) / (U * FEW_WARPS), 0);
     long long src = 0;                                        // first code of the tile
     float ks = 0.f, lv = -INFINITY, iv = 0.f;                 // (no place: the tile's terms vanish)
     auto lookup = [&](int n0) {
-        const int tok = (t_begin + warp + FEW_WARPS * (n0 + lane)) * 16;
+        const int tile = t_begin + (warp + FEW_WARPS * ((n0 + lane) / U)) * U + (n0 + lane) % U, tok = tile * 16;
         src = 0, ks = 0.f, lv = -INFINITY, iv = 0.f;
-        if (n0 + lane < tiles) {
+        if (tile < t_end) {
             const int page = tok / a.c.page, off = tok - page * a.c.page;
             const int pg = n0 == 0 && a.window == 0 ? early : a.sq.table[s * a.sq.stride + page];
             if ((unsigned)pg < (unsigned long long)a.c.pages) {
@@ -129,31 +132,32 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             }
         }
     };
-    using M = FewSmem<D, NT>;
-    constexpr int ST = M::kStages;
-    float4* ring_scale = reinterpret_cast<float4*>(smem + M::kScale) + warp * ST;
-    uint8_t* ring = smem + M::kRing + warp * (ST * 2 * M::kTile);
-    // copies of tile x: lane -> chunk lane % (D/16) of rows lane / (D/16) + ...
-    constexpr int CHUNKS = D / 16, PASS = 32 / CHUNKS > 0 ? 32 / CHUNKS : 1;          // rows of one pass
+    float4* ring_scale = reinterpret_cast<float4*>(smem + M::kScale) + warp * (ST * U);
+    uint8_t* ring = smem + M::kRing + warp * (ST * U * 2 * M::kTile);
+    // copies of a step's tiles: lane -> chunk lane % (D/16) of rows lane / (D/16) + ...
+    constexpr int CHUNKS = D / 16, PASS = 32 / CHUNKS;        // rows of one pass
     const int cr = lane / CHUNKS, cc = lane % CHUNKS;
-    auto fetch = [&](int x) {
-        if (x < tiles) {
-            const int i = x & 31, slot = x % ST;
-            if (i == 0 && x > 0) lookup(x);
-            const long long at = __shfl_sync(0xffffffffu, src, i) + lane * 16;
-            if (lane == i) ring_scale[slot] = make_float4(ks, lv, iv, 0.f);
-            const uint32_t to = smem_u32(ring + slot * 2 * M::kTile);
+    auto fetch = [&](int n) {
+        if (n < steps) {
 #pragma unroll
-            for (int r = 0; r < 16; r += PASS) {
-                cp_async_16(to + k_at<D>(r + cr, cc), a.c.k + at + r * D, 16);
-                cp_async_16(to + M::kTile + v_at<D>(r + cr, cc), a.c.v + at + r * D, 16);
+            for (int u = 0; u < U; u++) {
+                const int x = n * U + u, i = x & 31, slot = n % ST * U + u;
+                if (i == 0 && x > 0) lookup(x);
+                const long long at = __shfl_sync(0xffffffffu, src, i) + lane * 16;
+                if (lane == i) ring_scale[slot] = make_float4(ks, lv, iv, 0.f);
+                const uint32_t to = smem_u32(ring + slot * 2 * M::kTile);
+#pragma unroll
+                for (int r = 0; r < 16; r += PASS) {
+                    cp_async_16(to + k_at<D>(r + cr, cc), a.c.k + at + r * D, 16);
+                    cp_async_16(to + M::kTile + v_at<D>(r + cr, cc), a.c.v + at + r * D, 16);
+                }
             }
         }
         cp_async_commit();
     };
     lookup(0);
 #pragma unroll
-    for (int x = 0; x < ST - 1; x++) fetch(x);               // on their way while the queries convert
+    for (int n = 0; n < ST - 1; n++) fetch(n);               // on their way while the queries convert
 
     // queries to fp16, each row times the power of two that brings its largest magnitude to [1, 2)
     __half* sq = reinterpret_cast<__half*>(smem);
@@ -223,60 +227,67 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
 #pragma unroll
             for (int e = 0; e < 4; e++) o[i][nt][e] = 0.f;
 
-    for (int n = 0; n < tiles; n++) {
-        const int slot = n % ST, tok = (t_begin + warp + FEW_WARPS * n) * 16;
+    for (int n = 0; n < steps; n++) {
+        const int tok = (t_begin + (warp + FEW_WARPS * n) * U) * 16;
         cp_async_wait<ST - 2>();
-        __syncwarp();                                         // every lane's copies of tile n are here, tile n-1 is read
+        __syncwarp();                                         // every lane's copies of step n are here, step n-1 is read
         fetch(n + ST - 1);
-        const uint32_t kv = smem_u32(ring + slot * 2 * M::kTile);
-        const float4 b = ring_scale[slot];
-        const float ksc = b.x, lvc = b.y, ivc = b.z;
-        float sc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) sc[nt][e] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 64; c++) {
-            const uint4 ka = ld_shared_u4(kv + k_at<D>(g, 4 * c + t)), kb = ld_shared_u4(kv + k_at<D>(g + 8, 4 * c + t));
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-            for (int w = 0; w < 4; w++) {
-                uint32_t a0, a1, a2, a3;
-                codes_even_odd(wa[w], a0, a2);
-                codes_even_odd(wb[w], a1, a3);
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    const uint2 f = QREG ? qf[QREG ? nt : 0][QREG ? 4 * c + w : 0] : q_frag(nt, 4 * c + w);
-                    mma16816(sc[nt], a0, a1, a2, a3, f.x, f.y);
-                }
-            }
-        }
-        const bool masked = tok + 15 > lim_all || tok < low_all;
+        const uint32_t kv = smem_u32(ring + n % ST * U * 2 * M::kTile);
+        const float4* scales = ring_scale + n % ST * U;
+        float sc[U][NT][4], ivc[U];
+        const bool masked = tok + 16 * U - 1 > lim_all || tok < low_all;
         bool grow = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+        for (int u = 0; u < U; u++) {
+            const uint32_t kt = kv + u * 2 * M::kTile;
+            const float4 b = scales[u];
+            ivc[u] = b.z;
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float f = rs[nt][e] * ksc;
-                sc[nt][e] = fmaf(sc[nt][e], f, lvc);
-                sc[nt][2 + e] = fmaf(sc[nt][2 + e], f, lvc);
-                if (masked) {
-                    const int at = (r0 + min(8 * nt + 2 * t + e, rows - 1)) / a.group;       // new token of the row
-                    const int lim = a.causal ? min(first + at, end - 1) : end - 1;
-                    const int low = a.window > 0 ? first + at - a.window + 1 : 0;
-                    if (tok + g > lim || tok + g < low) sc[nt][e] = -INFINITY;
-                    if (tok + g + 8 > lim || tok + g + 8 < low) sc[nt][2 + e] = -INFINITY;
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sc[u][nt][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; c++) {
+                const uint4 ka = ld_shared_u4(kt + k_at<D>(g, 4 * c + t)), kb = ld_shared_u4(kt + k_at<D>(g + 8, 4 * c + t));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_even_odd(wa[w], a0, a2);
+                    codes_even_odd(wb[w], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        const uint2 f = QREG ? qf[QREG ? nt : 0][QREG ? 4 * c + w : 0] : q_frag(nt, 4 * c + w);
+                        mma16816(sc[u][nt], a0, a1, a2, a3, f.x, f.y);
+                    }
                 }
-                grow |= fmaxf(sc[nt][e], sc[nt][2 + e]) > m[nt][e] + LAZY;
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float f = rs[nt][e] * b.x;
+                    sc[u][nt][e] = fmaf(sc[u][nt][e], f, b.y);
+                    sc[u][nt][2 + e] = fmaf(sc[u][nt][2 + e], f, b.y);
+                    if (masked) {
+                        const int at = (r0 + min(8 * nt + 2 * t + e, rows - 1)) / a.group;   // new token of the row
+                        const int lim = a.causal ? min(first + at, end - 1) : end - 1;
+                        const int low = a.window > 0 ? first + at - a.window + 1 : 0, j = tok + 16 * u + g;
+                        if (j > lim || j < low) sc[u][nt][e] = -INFINITY;
+                        if (j + 8 > lim || j + 8 < low) sc[u][nt][2 + e] = -INFINITY;
+                    }
+                    grow |= fmaxf(sc[u][nt][e], sc[u][nt][2 + e]) > m[nt][e] + LAZY;
+                }
+        }
         // the reference of a row (one for the lanes that share its column) is raised when a term passes it by 2^8
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    float top = fmaxf(sc[nt][e], sc[nt][2 + e]);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < U; u++) top = fmaxf(top, fmaxf(sc[u][nt][e], sc[u][nt][2 + e]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -291,33 +302,37 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                     }
                 }
         }
-        uint32_t pf[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            float p[4];
+        for (int u = 0; u < U; u++) {
+            uint32_t pf[NT][2];
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float mu = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-                p[e] = ex2(sc[nt][e] - mu);
-                p[2 + e] = ex2(sc[nt][2 + e] - mu);
-                l[nt][e] = fmaf(p[e] + p[2 + e], ivc, l[nt][e]);
+            for (int nt = 0; nt < NT; nt++) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float mu = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                    p[e] = ex2(sc[u][nt][e] - mu);
+                    p[2 + e] = ex2(sc[u][nt][2 + e] - mu);
+                    l[nt][e] = fmaf(p[e] + p[2 + e], ivc[u], l[nt][e]);
+                }
+                pf[nt][0] = transpose8(pack2(p[0], p[1], __half()));
+                pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
             }
-            pf[nt][0] = transpose8(pack2(p[0], p[1], __half()));
-            pf[nt][1] = transpose8(pack2(p[2], p[3], __half()));
-        }
-        // O^T += V^T P^T: a transposed read brings dimensions 2g, 2g+1 of 16-byte chunk c for tokens 2t, 2t+1 (and + 8);
-        // fragment rows g, g+8 of product c are dimensions 16c + 2g and + 1
+            // O^T += V^T P^T: a transposed read brings dimensions 2g, 2g+1 of 16-byte chunk c for tokens 2t, 2t+1 (and
+            // + 8); fragment rows g, g+8 of product c are dimensions 16c + 2g and + 1
+            const uint32_t vt = kv + (2 * u + 1) * M::kTile;
 #pragma unroll
-        for (int c = 0; c < D / 16; c += 2) {
-            uint32_t vw[4];
-            ldmatrix_trans(kv + M::kTile + v_at<D>(lane & 15, c + (lane >> 4)), vw);
+            for (int c = 0; c < D / 16; c += 2) {
+                uint32_t vw[4];
+                ldmatrix_trans(vt + v_at<D>(lane & 15, c + (lane >> 4)), vw);
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                uint32_t a0, a1, a2, a3;
-                codes_even_odd(vw[2 * h], a0, a1);
-                codes_even_odd(vw[2 * h + 1], a2, a3);
+                for (int h = 0; h < 2; h++) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_even_odd(vw[2 * h], a0, a1);
+                    codes_even_odd(vw[2 * h + 1], a2, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) mma16816(o[c + h][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    for (int nt = 0; nt < NT; nt++) mma16816(o[c + h][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                }
             }
         }
     }
