@@ -78,8 +78,8 @@ __device__ __forceinline__ void store_out4(void* p, long long at, const float (&
 template <int D, int NT>
 __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(const AttnArgs a, int chunk, int splits, int row_blocks,
                                                           int qt, int ot) {
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();                                            // after the wait: the join reads its inputs before its own
     using M = FewSmem<D, NT>;
     constexpr int R = 8 * NT, U = M::kStep, ST = M::kStages;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -413,7 +413,6 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
 constexpr int JOIN_THREADS = 128;
 template <int D, int W>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, int chunk, int ot) {
-    pdl_wait();
     constexpr int ROWS = JOIN_THREADS / 32 / W, PER = D / 32;
     __shared__ float s_acc[W > 1 ? W : 1][W > 1 ? D : 1], s_den[W];
     const long long all_rows = (long long)a.sq.tokens * a.heads;
@@ -421,6 +420,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = W > 1 ? warp : 0;
     const long long row = W > 1 ? row0 : row0 + warp;
     const int t = (unsigned)min(row, all_rows - 1) / (unsigned)a.heads;
+    // Lengths and offsets were complete before the attention kernel let this launch begin (its own wait comes first), so
+    // they are read while that kernel still runs; its sums only after the wait below.
     int s = t;
     Seq q;
     if (a.sq.cu) {
@@ -432,9 +433,29 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
     } else {
         q = load_seq(a.sq, s, a.c.page);
     }
-    if (row >= all_rows || t < q.n0 || t >= q.n0 + min(q.n, a.max_tokens)) return;           // W > 1: the whole block
+    const bool mine = row < all_rows && t >= q.n0 && t < q.n0 + min(q.n, a.max_tokens);
     const int parts = visible_range(a, q, chunk).parts;
-    if (parts == 1) return;
+    pdl_wait();
+    if (!mine || parts == 1) return;                          // W > 1: the whole block
+    // eight parts' sums in flight, the first eight before their weights are known
+    float x[8][PER];
+    auto fetch = [&](int p) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float* po = a.part_o + (min(p + W * i, parts - 1) * all_rows + row) * D + lane * PER;
+            if constexpr (PER == 2) {
+                const float2 v = *reinterpret_cast<const float2*>(po);
+                x[i][0] = v.x; x[i][1] = v.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < PER; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(po + e);
+                    x[i][e] = v.x; x[i][e + 1] = v.y; x[i][e + 2] = v.z; x[i][e + 3] = v.w;
+                }
+            }
+        }
+    };
+    fetch(w);
     float mx = -INFINITY;
     for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, a.part_ml[p * all_rows + row].x);
 #pragma unroll
@@ -443,37 +464,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttnArgs a, in
 #pragma unroll
     for (int i = 0; i < PER; i++) acc[i] = 0.f;
     for (int p0 = w; p0 < parts; p0 += 32 * W) {              // lane i: weight of part p0 + W i
-        const int mine = p0 + W * lane;
+        const int its = p0 + W * lane;
         float f = 0.f;
-        if (mine < parts) {
-            const float2 ml = a.part_ml[mine * all_rows + row];
+        if (its < parts) {
+            const float2 ml = a.part_ml[its * all_rows + row];
             f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
             den += ml.y * f;
         }
         const int here = min((parts - p0 + W - 1) / W, 32);
-        for (int i0 = 0; i0 < here; i0 += 8) {                // eight parts' loads in flight
-            float x[8][PER], fi[8];
+        for (int i0 = 0; i0 < here; i0 += 8) {
+            if (p0 > w || i0 > 0) fetch(p0 + W * i0);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                fi[i] = __shfl_sync(0xffffffffu, f, i0 + i);  // 0 past the last part
-                const long long part = min(p0 + W * (i0 + i), parts - 1);
-                const float* po = a.part_o + (part * all_rows + row) * D + lane * PER;
-                if constexpr (PER == 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(po);
-                    x[i][0] = v.x; x[i][1] = v.y;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < PER; e += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(po + e);
-                        x[i][e] = v.x; x[i][e + 1] = v.y; x[i][e + 2] = v.z; x[i][e + 3] = v.w;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i++)
+                const float fi = __shfl_sync(0xffffffffu, f, i0 + i);             // 0 past the last part
 #pragma unroll
                 for (int e = 0; e < PER; e++)                 // a part that saw nothing wrote no sums
-                    acc[e] = fmaf(fi[i] == 0.f ? 0.f : x[i][e], fi[i], acc[e]);
+                    acc[e] = fmaf(fi == 0.f ? 0.f : x[i][e], fi, acc[e]);
+            }
         }
     }
     den = lane_sum<32>(den);

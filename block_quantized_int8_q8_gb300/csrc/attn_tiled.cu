@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                                                              int ot) {
     using C = Tiled<D>;
     constexpr int KT = C::kTokens, NQ = C::kQTiles, ROWS = 128 * NQ;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();                                            // after the wait: the join reads its inputs before its own
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
