@@ -93,7 +93,7 @@ struct AttnPlan {
     size_t part_o, part_ml, total;     // workspace offsets and size
 };
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                        long long max_kv);
+                        long long max_kv, long long window);
 cudaError_t run_attention_few(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,
                               cudaStream_t s);
 cudaError_t run_attention_tiled(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,

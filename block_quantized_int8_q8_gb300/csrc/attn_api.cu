@@ -84,40 +84,48 @@ namespace mmq {
 // The cache range is cut in chunks where the row blocks alone would not fill the GPU.
 //   few rows: all thread blocks do equal work on equal lengths, so the chunks are cut to make one wave; ragged
 //     lengths even out from 2048 tokens down.
-//   tiled: one thread block fits on an SM, and its start and end cost about as much as six tiles, so a cut only
-//     pays where it turns idle SMs busy: as many parts as fit beside each other.  (128 blocks of 250 tiles each: 423 us
-//     whole, 455 us in two parts, 464 us in seven.)
+//   tiled: one thread block fits on an SM, and its start and end cost about as much as five tiles.  B < 152 of them leave
+//     SMs idle, so every range of T tokens is cut at c = B (T + 640) / 152: the B whole parts take an SM each, and the
+//     last, shorter ones go one after the other to the SMs left over, all done at about the same time.  (128 blocks of
+//     32 k tokens: 425 us whole, 455 us in two equal parts, 464 us in seven.)  No cut for a rest below ten tiles.
+// A window shortens the range that a sequence's rows see together; the parts stay within what max_kv alone would give,
+// so that the workspace does not depend on it.
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                        long long max_kv) {
+                        long long max_kv, long long window) {
     AttnPlan p{};
     constexpr long long SMS = 152;
     const long long rows = max_tokens * (heads / kv_heads);
     p.few = rows <= 16;
-    const long long pairs = (long long)seqs * kv_heads;
-    long long chunk;
-    if (p.few) {
-        const long long want = (few_blocks(dim, rows <= 8 ? 1 : 2) * SMS + pairs - 1) / pairs;
-        chunk = (max_kv + want - 1) / want;
-        chunk = (chunk + 63) / 64 * 64;
-        chunk = chunk < 128 ? 128 : (chunk > 2048 ? 2048 : chunk);
-    } else {
-        const int block = dim == 256 ? 128 : 256;
-        const long long blocks = pairs * ((rows + block - 1) / block);
-        const long long parts = blocks < SMS ? SMS / blocks : 1;
-        chunk = ((max_kv + parts - 1) / parts + 127) / 128 * 128;
-        if (chunk < 512) chunk = 512;
+    const long long pairs = (long long)seqs * kv_heads, granule = p.few ? 64 : 128;
+    auto cut = [&](long long range) {                         // tokens of a part
+        if (p.few) {
+            const long long want = (few_blocks(dim, rows <= 8 ? 1 : 2) * SMS + pairs - 1) / pairs;
+            const long long chunk = ((range + want - 1) / want + granule - 1) / granule * granule;
+            return chunk < 128 ? 128ll : (chunk > 2048 ? 2048ll : chunk);
+        }
+        const long long block = dim == 256 ? 128 : 256, blocks = pairs * ((rows + block - 1) / block);
+        const long long whole = (range + granule - 1) / granule * granule;
+        const long long chunk = blocks < SMS ? (blocks * (range + 640) / SMS + granule - 1) / granule * granule : whole;
+        return chunk + 1280 > range ? (whole > 512 ? whole : 512ll) : (chunk < 512 ? 512ll : chunk);
+    };
+    auto parts = [](long long range, long long chunk) { return range > chunk ? (range + chunk - 1) / chunk : 1; };
+    long long chunk = cut(max_kv);
+    const long long most = parts(max_kv, chunk);
+    p.splits = (int)most;
+    const long long seen = max_tokens + window + 30;          // in whole tiles of 16
+    if (window > 0 && seen < max_kv) {
+        chunk = cut(seen);
+        while (parts(seen, chunk) > most) chunk += granule;
+        p.splits = (int)parts(seen, chunk);
     }
     p.chunk = (int)chunk;
-    // a window or an unaligned start can shift the range by one tile
-    p.splits = (int)((max_kv + 16 + chunk - 1) / chunk);
-    if (p.splits < 1) p.splits = 1;
     size_t off = 0;
     if (p.splits > 1) {
-        const size_t rows = (size_t)tokens * heads * p.splits;
+        const size_t all = (size_t)tokens * heads * p.splits;
         p.part_ml = off;
-        off += (rows * sizeof(float2) + 255) & ~size_t(255);
+        off += (all * sizeof(float2) + 255) & ~size_t(255);
         p.part_o = off;
-        off += (rows * dim * sizeof(float) + 255) & ~size_t(255);
+        off += (all * dim * sizeof(float) + 255) & ~size_t(255);
     }
     p.total = off;
     return p;
@@ -217,7 +225,7 @@ size_t mmq_attention_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, 
         max_tokens <= 0 || max_kv_len < 0 || tokens > kMaxDim || tokens * n_heads > kMaxDim)
         return 0;
     if (max_tokens > tokens) max_tokens = tokens;
-    return attention_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len).total;
+    return attention_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len, 0).total;
 }
 
 mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs,
@@ -238,8 +246,10 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
     if (!aligned16(lse)) return MMQ_ERR_ALIGN;
     if (max_tokens > tokens) max_tokens = tokens;
     const AttnPlan p = attention_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens,
-                                      max_kv_len);
-    if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return MMQ_ERR_WORKSPACE;
+                                      max_kv_len, window);
+    const size_t need = mmq_attention_workspace_bytes(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs,
+                                                      max_tokens, max_kv_len);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MMQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
     AttnArgs a{};
     a.q = rows_of(q);

@@ -157,10 +157,10 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // the last rows of a causal prompt see most of the cache: they go first
-    const int per = a.sq.seqs * a.c.heads * splits;
-    const int qb = q_blocks - 1 - (int)(blockIdx.x / per), rest = blockIdx.x % per;
-    const int split = rest % splits, head = rest / splits % a.c.heads, s = rest / splits / a.c.heads;
+    // Long pieces first: a range's whole parts before its last one, and the last rows of a causal prompt, which see most
+    // of the cache, before the others.
+    const int per = a.sq.seqs * a.c.heads, piece = blockIdx.x / per, sh = blockIdx.x % per;
+    const int split = piece / q_blocks, qb = q_blocks - 1 - piece % q_blocks, head = sh % a.c.heads, s = sh / a.c.heads;
     const Seq q = load_seq(a.sq, s, a.c.page);
     const int n = min(q.n, a.max_tokens), row0 = qb * ROWS, rows = min(n * a.group - row0, ROWS);
     if (rows <= 0) return;                                    // uniform, nothing set up yet
