@@ -173,3 +173,23 @@ def test_workspace_sizes(lib):
     assert size(1, 32, 7, 128, 1, 1, 100000) == 0
     assert size(1, 32, 8, 96, 1, 1, 100000) == 0
     assert size(1, 32, 8, 128, 0, 1, 100000) == 0
+
+
+def test_binding_refuses_what_it_cannot_pass(lib):
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(2, 3, 64), torch.zeros(64)
+    codes, scale = torch.zeros(4, 2, 32, 64, dtype=torch.int8), torch.zeros(4, 2, 2)
+    for call in (lambda: api.qk_norm_rope(None, None), lambda: api.qk_norm_rope(x, None), lambda: api.qk_norm_rope(x, None, w),
+                 lambda: api.KVCache(codes, codes, scale, scale), lambda: api.KVCache(codes, codes, scale, scale[:2]),
+                 lambda: api.KVCache(codes.float(), codes, scale, scale), lambda: api.KVCache(1, 2, 3, 4)):
+        with pytest.raises(api.MMQError):
+            call()
+    with pytest.raises(api.MMQError):                          # an output of another shape
+        api.qk_norm_rope(x, None, q_out=x[:1])
+
+
+def test_missing_binding_raises(monkeypatch, tmp_path):
+    monkeypatch.setattr(api, "_bind", None)
+    monkeypatch.setattr(_build, "BIND_LIB", str(tmp_path / "none.so"))
+    with pytest.raises(api.MMQError):
+        api._binding()
