@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                     grow |= fmaxf(sc[u][nt][e], sc[u][nt][2 + e]) > m[nt][e] + LAZY;
                 }
         }
-        // the reference of a row (one for the lanes that share its column) is raised when a term passes it by 2^8
+        // the reference of a row (one for the lanes that share its column) is raised when a term passes it by 2^12
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)

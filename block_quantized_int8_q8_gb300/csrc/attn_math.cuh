@@ -7,7 +7,7 @@ namespace mmq {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float SCALE_FLOOR = 0x1p-64f;      // stands for a zero value scale (all codes zero) in log2 and 1/x
-constexpr float LAZY = 8.f;                  // the running maximum may trail by 2^8 before sums are rescaled
+constexpr float LAZY = 12.f;                 // the reference may trail a term by 2^12 (fp16 holds 2^15) before sums are rescaled
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -6,16 +6,24 @@
 // Bound by the tensor cores and the exponentials.  One thread block takes 256 rows (two tiles of 128; head_dim 256:
 // one) of one sequence and key/value head, rows = (new token, query head of the group), and walks the cache in tiles
 // of 128 tokens (head_dim 256: 64):
-//   * seven converter warps read the codes in units of 16 tokens (each within one page), turn them into fp16 exactly
-//     and store them with the 128-byte swizzle.  K is the K-major operand of S, V the MN-major operand of O, so both
-//     have the same layout [token][64 dimensions of 128 bytes] and one routine makes them.  Within each four
-//     dimensions the order is 0 2 1 3 (two codes of a word convert at once); Q is stored in that order too, and the
-//     output undoes it.  They also publish the units' block scales.
+//   * seven converter warps read the codes in units of 32 tokens (two groups of 16, each within one page), turn them into
+//     fp16 exactly and store them with the 128-byte swizzle.  K is the K-major operand of S, V the MN-major operand of
+//     O, so both have the same layout [token][64 dimensions of 128 bytes] and one routine makes them.  Within each
+//     four dimensions the order is 0 2 1 3 (two codes of a word convert at once); Q is stored in that order too, and
+//     the output undoes it.  They also publish the groups' block scales.
 //   * one warp issues the products, S_i = Q_i K^T into TMEM and O_i += P_i V with P_i from TMEM.  The two row
 //     tiles alternate: while the softmax of one runs, the other's products do.
 //   * four softmax warps for each row tile, one thread a row: the row of S in registers, its maximum, the
 //     exponentials, P as fp16 over the columns of S (in halves, so that the product can start on the first).  O is
-//     rescaled only when the maximum grows by more than 2^8, which happens a few times in a row's life.
+//     rescaled only when the maximum grows by more than 2^12, which happens a few times in a row's life.  These warps
+//     also bring the queries in and the outputs out, as whole rows through shared memory.
+// What it measures (GB300; 1909 TFLOP/s is the card's dense fp16 rate): 2048 tokens of 16 heads after 30000 cached ones,
+// 392 us, 1.33 PFLOP/s; prompts of up to 4096 tokens of 32 heads, 311 us, 1.02 PFLOP/s.  A tile of 128 tokens takes a
+// block 3300 cycles: 1700 to 2000 of products (their operands take 1500 cycles of shared memory reads, the converted
+// codes 500 of writes), the rest is the chain S -> maximum -> exponentials -> P, which two row tiles hide in part.
+// Variants measured slower: two threads a row (chunk 492 -> 625 us), the reference checked after the exponentials
+// instead of a maximum first (492 -> 525), each half of P on its own maximum (394 -> 413), P in one piece (394 -> 399),
+// three or six converter warps (691, 413), parts and rests of equal length.
 #include "attn_device.cuh"
 #include "attn_math.cuh"
 #include "internal.h"
@@ -393,13 +401,13 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                     np ^= 1u << buf;
                     if (!ok) break;
                 }
+                if (i == NQ - 1) release(x + 1);
                 if (NQ == 2 && more && active(i, j + 1)) {
                     tc_fence_after();
                     product_s(i, j + 1);
                 }
             }
             if (!ok) break;
-            release(x + 1);
             if (more) release(x + 2);
         }
         if (elect_one()) umma_commit(bar.done());
