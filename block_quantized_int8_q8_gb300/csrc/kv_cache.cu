@@ -1,11 +1,17 @@
 // kv_cache.cu -- the operators that write and read the 8-bit paged key/value cache, and the head norm with the
-// position rotation.  All of them move each value once and are bound by memory bandwidth, or by launch latency for
-// a decode step.
+// position rotation.
 //
 //   norm_rope  y = rotate(x / sqrt(mean x^2 + eps) * w), heads of D values
 //   append     the same on the way into the cache, then per block of B tokens and head
 //              s' = max(s, amax/127), code = round-half-even(x / s'); codes already there times s/s'
 //   read       scale * code
+//
+// All of them move each value once.  Long calls are bound by memory bandwidth and by the instructions around each value
+// (hence packed arithmetic, 16-byte or paired 8-byte accesses, no 64-bit divisions), short ones by the chain of dependent
+// loads: sequence, page, rows.  GB300, each call over inputs larger than the last one left in the cache:
+//   norm_rope  8191 tokens of 40 heads of 128, bf16: 30 us, 5.7 TB/s; 4 tokens: 2.5 us
+//   append     6500 tokens of 32 query and 8 key/value heads, bf16: 37 us; 64 single tokens, f32: 6 us
+//   read       131072 tokens of 8 heads to bf16: 132 us, 6.1 TB/s
 #include "attn_device.cuh"
 #include "internal.h"
 
@@ -337,8 +343,6 @@ __global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(con
 // ------------------------------------------------------------------------------------------ read
 // One thread block per 8 packed rows (4 of the widest f32 heads); a group of lanes keeps one row and goes over its heads,
 // a lane turns N codes into one 16-byte store.
-constexpr int READ_THREADS = 256;
-
 // four codes -> f32 exactly: the byte spliced into the mantissa of 2^23 + x
 __device__ __forceinline__ void codes_f32(uint32_t w, Quad& x) {
     const uint32_t u = w ^ 0x80808080u;
@@ -373,15 +377,15 @@ __device__ __forceinline__ void store_codes(T* p, uint2 w, uint64_t d2) {
 template <typename T> struct ReadVec { using type = uint2; static constexpr int n = 8; };
 template <> struct ReadVec<float> { using type = uint32_t; static constexpr int n = 4; };
 
-template <int D, typename T> struct ReadShape {
-    static constexpr int kLanes = D / ReadVec<T>::n, kGroups = READ_THREADS / kLanes;
+template <int D, typename T, int THREADS> struct ReadShape {
+    static constexpr int kLanes = D / ReadVec<T>::n, kGroups = THREADS / kLanes;
     static constexpr int kTokens = kGroups < 8 ? kGroups : 8;
 };
 
-template <int D, typename T>
-__global__ void __launch_bounds__(READ_THREADS) read_kernel(const ReadArgs a) {
+template <int D, typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS) read_kernel(const ReadArgs a) {
     pdl_wait();
-    using S = ReadShape<D, T>;
+    using S = ReadShape<D, T, THREADS>;
     constexpr int N = ReadVec<T>::n;
     using V = typename ReadVec<T>::type;
     __shared__ long long s_page[S::kTokens];
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(READ_THREADS) read_kernel(const ReadArgs a) {
     const int t0 = blockIdx.x * S::kTokens;
     int s = t0;
     Seq q;
-    if (a.sq.cu) s = find_seq<READ_THREADS>(a.sq, a.c.page, t0, [](int cu, int) { return (long long)cu; }, q);
+    if (a.sq.cu) s = find_seq<THREADS>(a.sq, a.c.page, t0, [](int cu, int) { return (long long)cu; }, q);
     if (threadIdx.x < S::kTokens) {
         const int t = t0 + threadIdx.x;
         long long page = -2;                                 // past the rows
@@ -503,12 +507,19 @@ cudaError_t launch_append_block(mmq_dtype t, mmq_dtype qot, const AppendArgs& a,
     return cudaErrorInvalidValue;
 }
 
+template <int D, typename T, int THREADS>
+cudaError_t launch_read_threads(const ReadArgs& a, cudaStream_t s) {
+    constexpr int tokens = ReadShape<D, T, THREADS>::kTokens;
+    const unsigned grid = (unsigned)((a.sq.tokens + tokens - 1) / tokens);
+    return launch_pdl(read_kernel<D, T, THREADS>, dim3(grid), dim3(THREADS), s, a);
+}
+// Many rows: smaller blocks, whose starts overlap other blocks' copies; few: more lanes on a row (131072 rows: 132 us
+// with 128 threads, 154 with 256; an append of 6500 rows with their read: 52 us with 128, 49 with 256).
 template <int D>
 cudaError_t launch_read(mmq_dtype t, const ReadArgs& a, cudaStream_t s) {
     return with_type(t, [&](auto ti) {
-        constexpr int tokens = ReadShape<D, decltype(ti)>::kTokens;
-        const unsigned grid = (unsigned)((a.sq.tokens + tokens - 1) / tokens);
-        return launch_pdl(read_kernel<D, decltype(ti)>, dim3(grid), dim3(READ_THREADS), s, a);
+        using T = decltype(ti);
+        return a.sq.tokens > 32768 ? launch_read_threads<D, T, 128>(a, s) : launch_read_threads<D, T, 256>(a, s);
     });
 }
 
