@@ -103,7 +103,9 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
             const long long chunk = ((range + want - 1) / want + granule - 1) / granule * granule;
             return chunk < 128 ? 128ll : (chunk > 2048 ? 2048ll : chunk);
         }
-        const long long block = dim == 256 ? 128 : 256, blocks = pairs * ((rows + block - 1) / block);
+        const long long block = dim == 256 ? 128 : 256, group = heads / kv_heads;
+        const long long packed = tokens * group / block + seqs, each = seqs * ((rows + block - 1) / block);
+        const long long blocks = kv_heads * (packed < each ? packed : each);
         const long long whole = (range + granule - 1) / granule * granule;
         const long long chunk = blocks < SMS ? (blocks * (range + 640) / SMS + granule - 1) / granule * granule : whole;
         return chunk + 1280 > range ? (whole > 512 ? whole : 512ll) : (chunk < 512 ? 512ll : chunk);

@@ -150,7 +150,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     } else {
         q = load_seq(a.sq, s, a.c.page);
     }
-    if (q.n == 0) return;
+    if (q.n == 0 || local < 0) return;
     const int p0 = q.len - q.n;                              // position of the first new token
     if (threadIdx.x == 0 && local == 0 && (p0 < 0 || q.end < q.len)) flag_error(DEVERR_LENGTH);
     const int b0 = (max(p0, 0) / B + local) * B;             // first position of this block

@@ -579,3 +579,13 @@ def test_steps_in_a_graph():
     want, _, vmax = ref_attention(q.cpu(), cache, table, [40] * n_seq, [1] * n_seq, D ** -0.5, True, 0)
     assert_close(out, want, torch.full_like(want, vmax * (2.0 ** -11 + 2.0 ** -16)))
     assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_prompt_among_single_tokens(D):
+    """One prompt and many single tokens in a batch, in every order: rows of many sequences in one launch."""
+    n = [1, 1, 300, 1, 0, 1, 17, 1, 1, 1] + [1] * 30
+    lens = [90, 1, 300, 33, 5, 64, 40, 128, 700, 16] + [20 + i for i in range(30)]
+    check_attention(lens, n, 8, 2, D, 64, 16)
+    check_attention(lens[::-1], n[::-1], 6, 1, D, 32, 32, window=50)
