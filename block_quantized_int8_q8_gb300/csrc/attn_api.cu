@@ -83,7 +83,11 @@ namespace mmq {
 // Few rows (new tokens x query heads of a key/value head <= 16) run on the few-row kernel, more on the tiled one.
 // The cache range is cut in chunks where the row blocks alone would not fill the GPU.
 //   few rows: all thread blocks do equal work on equal lengths, so the chunks are cut to make one wave; ragged
-//     lengths even out from 2048 tokens down.
+//     lengths even out from 2048 tokens down.  Several sequences whose pairs with a head fill less than half of a wave
+//     leave a second wave nearly empty at that size and take 1024 (heads of 128, 8 key/value heads, ragged: 8 and 16
+//     sequences of up to 20 k tokens 48.5 -> 44.6 and 74.8 -> 68.5 us).  More pairs make many waves anyway, and smaller
+//     parts only add starts and joins (200 of up to 2000 tokens: 78 -> 83 us; 64 of up to 8192 at head_dim 64 and 256:
+//     59 -> 62 and 183 -> 195).
 //   tiled: one thread block fits on an SM, and its start and end cost about as much as five tiles.  B < 152 of them leave
 //     SMs idle, so every range of T tokens is cut at c = B (T + 640) / 152: the B whole parts take an SM each, and the
 //     last, shorter ones go one after the other to the SMs left over, all done at about the same time.  (128 blocks of
@@ -99,9 +103,10 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
     const long long pairs = (long long)seqs * kv_heads, granule = p.few ? 64 : 128;
     auto cut = [&](long long range) {                         // tokens of a part
         if (p.few) {
-            const long long want = (few_blocks(dim, rows <= 8 ? 1 : 2) * SMS + pairs - 1) / pairs;
+            const long long slots = few_blocks(dim, rows <= 8 ? 1 : 2) * SMS, want = (slots + pairs - 1) / pairs;
             const long long chunk = ((range + want - 1) / want + granule - 1) / granule * granule;
-            return chunk < 128 ? 128ll : (chunk > 2048 ? 2048ll : chunk);
+            const long long most = seqs > 1 && 2 * pairs <= slots ? 1024 : 2048;
+            return chunk < 128 ? 128ll : (chunk > most ? most : chunk);
         }
         const long long block = dim == 256 ? 128 : 256, group = heads / kv_heads;
         const long long packed = tokens * group / block + seqs, each = seqs * ((rows + block - 1) / block);

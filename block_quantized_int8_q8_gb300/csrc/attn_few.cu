@@ -19,7 +19,8 @@
 // GB300, heads of 128, 32 query and 8 key/value heads: 64 sequences of up to 8192 tokens 101 us (5.4 TB/s of cache), of
 // which the join takes 6; one sequence of 131 k tokens 54 us (5.0 TB/s), the join 5; one of 77 tokens 4.6 us.  With the
 // tiles loaded straight into registers a tile ahead the first two took 114 and 59 us; with V through byte shuffles 105 and
-// 60; chunks of 1024 or 4096 tokens instead of 2048 for the batch: 100 and 113 us.
+// 60; chunks of 1024 or 4096 tokens instead of 2048 for the batch: 100 and 113 us; parts joined through the shared memory of
+// a cluster instead of by a second launch: 107 (its blocks hold their places until the last has finished).
 #include "attn_device.cuh"
 #include "attn_math.cuh"
 #include "internal.h"

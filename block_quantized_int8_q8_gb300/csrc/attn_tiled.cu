@@ -23,7 +23,8 @@
 // codes 500 of writes), the rest is the chain S -> maximum -> exponentials -> P, which two row tiles hide in part.
 // Variants measured slower: two threads a row (chunk 492 -> 625 us), the reference checked after the exponentials
 // instead of a maximum first (492 -> 525), each half of P on its own maximum (394 -> 413), P in one piece (394 -> 399),
-// three or six converter warps (691, 413), parts and rests of equal length.
+// three or six converter warps (691, 413), parts and rests of equal length, S in halves of 64 tokens with the first made
+// ahead over columns already read (393 -> 483: the queries are read from shared memory twice).
 #include "attn_device.cuh"
 #include "attn_math.cuh"
 #include "internal.h"
