@@ -525,6 +525,17 @@ def test_attention_flags_lengths_and_pages(n):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,n,Hq,H", [([9001, 300], [1, 1], 4, 1),                  # 71 parts of 128
+                                         ([5000, 77, 4999], [3, 1, 4], 4, 1),          # 40 parts, several rows
+                                         ([20011, 1025, 1024, 30], [1] * 4, 8, 8),     # parts of 1024
+                                         ([700, 33, 385, 384] * 10, [1] * 40, 64, 8)])  # more rows than resident blocks
+def test_attention_joins(lens, n, Hq, H, D):
+    """Every form of the join: few rows of many parts, of a few, and many rows; sequences of one part among them."""
+    check_attention(lens, n, Hq, H, D, 64, 16)
+
+
+@gpu
 @pytest.mark.parametrize("n", [1, 33])
 def test_attention_offsets_past_32_bits(n):
     """A cache whose codes take more than 2^32 bytes, with the sequence in its last pages."""
