@@ -10,7 +10,7 @@
 // (hence packed arithmetic, 16-byte or paired 8-byte accesses, no 64-bit divisions), short ones by the chain of dependent
 // loads: sequence, page, rows.  GB300, each call over inputs larger than the last one left in the cache:
 //   norm_rope  8191 tokens of 40 heads of 128, bf16: 30 us, 5.7 TB/s; 4 tokens: 2.5 us
-//   append     6500 tokens of 32 query and 8 key/value heads, bf16: 37 us; 64 single tokens, f32: 6 us
+//   append     6500 tokens of 32 query and 8 key/value heads, bf16: 34 us; 64 single tokens, f32: 6 us
 //   read       131072 tokens of 8 heads to bf16: 132 us, 6.1 TB/s
 #include "attn_device.cuh"
 #include "internal.h"
@@ -87,9 +87,11 @@ __global__ void __launch_bounds__(NR_THREADS, 4) norm_rope_kernel(const NormRope
 
 // ------------------------------------------------------------------------------------------ append
 // One thread block per (block of B tokens, head, key or value): the rows of the block stay in registers between
-// the largest magnitude and the codes, so the new rows are read once.  Blocks of the grid past those take the
-// queries.  A sequence of n new tokens touches at most n/B + 2 blocks, and at most n; slot cu[s]/B + 2s, or cu[s], is the
-// first of sequence s (whichever makes fewer slots), so a block finds its sequence by a search and no list is built.
+// the largest magnitude and the codes, so the new rows are read once.  Other blocks take the queries; the two kinds are
+// spread evenly over the grid, since one waits for memory more and the other works more (6500 tokens: 37 us with the
+// queries last, 34 mixed).  A sequence of n new tokens touches at most n/B + 2 blocks, and at most n; slot
+// cu[s]/B + 2s, or cu[s], is the first of sequence s (whichever makes fewer slots), so a block finds its sequence by a
+// search and no list is built.
 template <int D, int B> struct AppendShape {
     static constexpr int kLanes = D / 8;                    // lanes of one row
     // two rows a thread, within 128 to 512 threads
@@ -327,16 +329,17 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
 }
 
 template <int D, int B, typename T>
-__global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(const AppendArgs a, unsigned kv_blocks,
+__global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(const AppendArgs a, unsigned query_share,
                                                                           bool by_token, int qtokens, int qot) {
     pdl_wait();
-    const unsigned b = blockIdx.x;
-    if (b < kv_blocks) {
+    // block b is the q-th of the queries' where q grows at b, else one of the cache's
+    const unsigned q = __umulhi(blockIdx.x, query_share), b = blockIdx.x - q;
+    if (__umulhi(blockIdx.x + 1, query_share) == q) {
         const int slot = b / (2u * a.c.heads), w = b - slot * 2u * a.c.heads;
         const bool isv = w >= a.c.heads;
         append_block<D, B, T>(a, slot, isv ? w - a.c.heads : w, isv, by_token);
     } else {
-        append_queries<D, B, T>(a, (int)(b - kv_blocks) * qtokens, qtokens, qot);
+        append_queries<D, B, T>(a, (int)q * qtokens, qtokens, qot);
     }
 }
 
@@ -491,8 +494,10 @@ cudaError_t launch_append(mmq_dtype t, mmq_dtype qot, const AppendArgs& a, cudaS
     const int qtokens = a.sq.tokens <= 8 * 152 ? 1 : S::kQTokens;
     const long long grid = kv + (a.q_heads > 0 ? ((long long)a.sq.tokens + qtokens - 1) / qtokens : 0);
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    // the queries' blocks for every 2^32 of the grid, rounded up: the last block's number comes out exactly
+    const unsigned share = (unsigned)((((grid - kv) << 32) + grid - 1) / grid);
     return with_type(t, [&](auto ti) {
-        return launch_pdl(append_kernel<D, B, decltype(ti)>, dim3((unsigned)grid), dim3(S::kThreads), s, a, (unsigned)kv,
+        return launch_pdl(append_kernel<D, B, decltype(ti)>, dim3((unsigned)grid), dim3(S::kThreads), s, a, share,
                           by_token, qtokens, (int)qot);
     });
 }
