@@ -18,7 +18,7 @@
 //     rescaled only when the maximum grows by more than 2^12, which happens a few times in a row's life.  These warps
 //     also bring the queries in and the outputs out, as whole rows through shared memory.
 // What it measures (GB300; 1909 TFLOP/s is the card's dense fp16 rate): 2048 tokens of 16 heads after 30000 cached ones,
-// 385 us, 1.35 PFLOP/s; prompts of up to 4096 tokens of 32 heads, 311 us, 1.02 PFLOP/s.  A tile of 128 tokens takes a
+// 386 us, 1.34 PFLOP/s; prompts of up to 4096 tokens of 32 heads, 304 us, 1.04 PFLOP/s.  A tile of 128 tokens takes a
 // block 3300 cycles: 1700 to 2000 of products (their operands take 1500 cycles of shared memory reads, the converted
 // codes 500 of writes), the rest is the chain S -> maximum -> exponentials -> P, which two row tiles hide in part.
 // Variants measured slower: two threads a row (chunk 492 -> 625 us), the reference checked after the exponentials
@@ -221,6 +221,24 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc_off + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc_off);
     float4* scales = reinterpret_cast<float4*>(smem + C::sc_off);
+    // The softmax warps' rows of queries come whole by asynchronous copies, D/8 lanes on a row, to where the operand
+    // belongs, while the block is set up (prompts: 309 us with the copies after it, 303).
+    constexpr int LPR = D / 8, RPS = 32 / LPR;                // lanes on a row, rows at a time
+    const int sub = lane % LPR;
+    if (warp < 4 * NQ) {
+        const int r = min(warp * 32 + lane, rows - 1);
+        const long long mine = ((long long)(q.n0 + (row0 + r) / a.group) * a.q.ts +
+                                (long long)(head * a.group + (row0 + r) % a.group) * a.q.hs) * 2;
+        const uint8_t* src = static_cast<const uint8_t*>(a.q.data) + sub * 16;
+        const uint32_t tile = sb + C::q_off + (warp >> 2) * C::kQBytes;
+#pragma unroll 8
+        for (int s0 = 0; s0 < 32; s0 += RPS) {
+            const int at = s0 + lane / LPR;                   // row of the warp
+            cp_async_16(tile + (sub / 8) * 16384 + sw128_off((warp & 3) * 32 + at, sub % 8),
+                        src + __shfl_sync(0xffffffffu, mine, at), 16);
+        }
+        cp_async_commit();
+    }
     if (warp == T_MMA) {
         if (lane == 0) {
             for (int i = 0; i < C::kStages; i++) {
@@ -439,23 +457,11 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         const int tokrow = (row0 + min(r, rows - 1)) / a.group;                   // new token
         const int hrow = head * a.group + (row0 + min(r, rows - 1)) % a.group;
         const long long tok = q.n0 + tokrow;
-        constexpr int LPR = D / 8, RPS = 32 / LPR;            // lanes on a row, rows at a time, where rows move whole
-        const int sub = lane % LPR;
         float rs = 0.f;
         {
-            // The warp's rows come whole by asynchronous copies, D/8 lanes on a row, to where the operand belongs; each
-            // thread then turns its row into fp16 in place, times the power of two that brings the row's largest
+            // Each thread turns its row into fp16 in place, times the power of two that brings the row's largest
             // magnitude to [1, 2) (the sign of the scale goes into the row).
-            const long long mine = (tok * a.q.ts + hrow * a.q.hs) * 2;
-            const uint8_t* src = static_cast<const uint8_t*>(a.q.data) + sub * 16;
             const uint32_t tile = sb + C::q_off + i * C::kQBytes;
-#pragma unroll 8
-            for (int s0 = 0; s0 < 32; s0 += RPS) {
-                const int at = s0 + lane / LPR;               // row of the warp
-                cp_async_16(tile + (sub / 8) * 16384 + sw128_off((warp & 3) * 32 + at, sub % 8),
-                            src + __shfl_sync(0xffffffffu, mine, at), 16);
-            }
-            cp_async_commit();
             cp_async_wait<0>();
             __syncwarp();
             // magnitudes order as the integers that their bits are, in both 16-bit types
