@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The roles stand inside the branch that sets their share of registers (not indented further): set in a branch before
+    // theirs, the compiler keeps to the launch's 128 and spills 4 KB a thread.
     if (warp >= T_CONV0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     if (warp != T_MMA) {
