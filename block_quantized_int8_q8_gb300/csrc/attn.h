@@ -90,6 +90,7 @@ constexpr int few_blocks(int dim, int nt) { return dim == 256 ? 2 : (nt == 2 ? 3
 struct AttnPlan {
     bool few;                  // the few-row kernel, else the tiled one
     int chunk, splits;
+    int window;                // 0 where the asked one hides nothing: what the kernels are given
     size_t part_o, part_ml, total;     // workspace offsets and size
 };
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,

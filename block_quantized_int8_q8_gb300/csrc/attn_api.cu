@@ -93,7 +93,8 @@ namespace mmq {
 //     last, shorter ones go one after the other to the SMs left over, all done at about the same time.  (128 blocks of
 //     32 k tokens: 425 us whole, 455 us in two equal parts, 464 us in seven.)  No cut for a rest below ten tiles.
 // A window shortens the range that a sequence's rows see together; the parts stay within what max_kv alone would give,
-// so that the workspace does not depend on it.
+// so that the workspace does not depend on it.  One that no sequence outgrows hides nothing and is none: the largest
+// values of its type, a common way to ask for none, take no part in any sum.
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
                         long long max_kv, long long window) {
     AttnPlan p{};
@@ -119,8 +120,9 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
     long long chunk = cut(max_kv);
     const long long most = parts(max_kv, chunk);
     p.splits = (int)most;
-    const long long seen = max_tokens + window + 30;          // in whole tiles of 16
-    if (window > 0 && seen < max_kv) {
+    p.window = window < max_kv ? (int)window : 0;
+    const long long seen = max_tokens + p.window + 30;        // in whole tiles of 16
+    if (p.window > 0 && seen < max_kv) {
         chunk = cut(seen);
         while (parts(seen, chunk) > most) chunk += granule;
         p.splits = (int)parts(seen, chunk);
@@ -269,7 +271,7 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
     a.max_kv = (int)max_kv_len;
     a.scale = scale;
     a.causal = causal != 0;
-    a.window = window > max_kv_len + max_tokens ? 0 : (int)window;
+    a.window = p.window;
     a.lse = lse;
     if (p.total > 0) {
         a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_ml);

@@ -343,7 +343,8 @@ mmq_status mmq_kv_read(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64
  * lse    : f32 [tokens][n_heads], the log of the softmax denominator (natural log, with the scores' scale), or
  *          null.
  * Row i of a sequence's n new tokens sees positions j < kv_len; with causal set, j <= kv_len - n + i; with
- * window > 0 (causal only) j > kv_len - n + i - window too.  A row that sees nothing gets 0 and lse = -inf.
+ * window > 0 (causal only) j > kv_len - n + i - window too (max_kv_len or more hides nothing).  A row that sees
+ * nothing gets 0 and lse = -inf.
  * max_tokens, max_kv_len : upper bounds of a sequence's new tokens and of kv_lens; they size the launch.
  * workspace : mmq_attention_workspace_bytes(...) bytes for the same sizes (0: may be null), 16-byte aligned; its
  *          contents on entry do not matter.
