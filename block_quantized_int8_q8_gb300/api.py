@@ -297,6 +297,7 @@ class KVCache:
 
 
 def _handle(stream) -> int | None:
+    # outputs and workspaces of a call come from its stream's memory, as under torch.cuda.stream(stream)
     return None if stream is None else stream.cuda_stream
 
 

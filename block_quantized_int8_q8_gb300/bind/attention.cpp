@@ -7,6 +7,8 @@
 #include <Python.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -134,10 +136,21 @@ at::Tensor output(const at::Tensor& x, PyObject* out, PyObject* dtype, const cha
     return o;
 }
 
-mmq_stream_t stream_of(PyObject* o) {
-    if (o == Py_None) return reinterpret_cast<mmq_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
-    return reinterpret_cast<mmq_stream_t>((uintptr_t)integer(o));
-}
+// The call's stream, a handle or None for the current one.  A given stream is the current one while this object lives, so
+// that outputs and workspace come from its memory: what the allocator takes back from another stream may still be
+// in use there, and a workspace given back when the call returns would be handed out there while the kernels use it.
+class OnStream {
+    c10::cuda::OptionalCUDAStreamGuard guard;
+public:
+    explicit OnStream(PyObject* o) {
+        if (o == Py_None) return;
+        const auto handle = reinterpret_cast<cudaStream_t>((uintptr_t)integer(o));
+        guard.reset_stream(c10::cuda::getStreamFromExternal(handle, c10::cuda::current_device()));
+    }
+    operator mmq_stream_t() const {
+        return reinterpret_cast<mmq_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
+    }
+};
 
 void check(mmq_status st, const char* what) {
     if (st == MMQ_OK) return;
@@ -155,6 +168,7 @@ PyObject* none() { Py_RETURN_NONE; }
 // q, k, positions, cos, sin, q_weight, k_weight, eps, interleaved, q_out, k_out, dtype, stream
 PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
     need(n, 13);
+    const OnStream stream(a[12]);
     const at::Tensor *q = tensor_or_none(a[0], "q"), *k = tensor_or_none(a[1], "k");
     const at::Tensor* x = q ? q : k;
     if (!x) refuse("qk_norm_rope", "neither q nor k given");
@@ -171,7 +185,7 @@ PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
     const void* pos = plain(tensor_or_none(a[2], "positions"), at::kInt, tokens, "positions");
     check(mmq_qk_norm_rope(q ? &hq : nullptr, q ? (int)q->size(1) : 0, vector(a[5], dim, "q_weight"), q ? &hqo : nullptr,
                            k ? &hk : nullptr, k ? (int)k->size(1) : 0, vector(a[6], dim, "k_weight"), k ? &hko : nullptr,
-                           tokens, (int)dim, static_cast<const int32_t*>(pos), rot, real(a[7]), stream_of(a[12])),
+                           tokens, (int)dim, static_cast<const int32_t*>(pos), rot, real(a[7]), stream),
           "mmq_qk_norm_rope");
     PyObject* p = q ? THPVariable_Wrap(std::move(qo)) : none();
     PyObject* s = k ? THPVariable_Wrap(std::move(ko)) : none();
@@ -184,6 +198,7 @@ PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
 // cache, k, v, page_table, kv_lens, cu_tokens, cos, sin, interleaved, k_weight, eps, q, q_weight, q_out, q_dtype, stream
 PyObject* kv_append(PyObject* const* a, Py_ssize_t n) {
     need(n, 16);
+    const OnStream stream(a[15]);
     const mmq_kv_cache* c = cache_of(a[0]);
     const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
     const at::Tensor* q = tensor_or_none(a[11], "q");
@@ -203,7 +218,7 @@ PyObject* kv_append(PyObject* const* a, Py_ssize_t n) {
     const mmq_rotary* rot = rotary(a[6], a[7], a[8], &r);
     check(mmq_kv_append(c, &sq, tokens, &hk, &hv, vector(a[9], dim, "k_weight"), q ? &hq : nullptr,
                         q ? (int)q->size(1) : 0, vector(a[12], dim, "q_weight"), q ? &hqo : nullptr, rot, real(a[10]),
-                        stream_of(a[15])),
+                        stream),
           "mmq_kv_append");
     return q ? THPVariable_Wrap(std::move(qo)) : none();
 }
@@ -211,6 +226,7 @@ PyObject* kv_append(PyObject* const* a, Py_ssize_t n) {
 // cache, device tensor, page_table, kv_lens, tokens, cu_tokens, dtype, stream
 PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
     need(n, 8);
+    const OnStream stream(a[7]);
     const mmq_kv_cache* c = cache_of(a[0]);
     const long long tokens = integer(a[4]);
     if (tokens < 0) refuse("kv_read", "tokens is negative");
@@ -218,7 +234,7 @@ PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
     at::Tensor k = at::empty({tokens, c->kv_heads, c->head_dim}, options), v = at::empty(k.sizes(), options);
     const mmq_heads hk = heads(k, "k"), hv = heads(v, "v");
     const mmq_kv_seqs sq = sequences(a[2], a[3], a[5]);
-    check(mmq_kv_read(c, &sq, tokens, &hk, &hv, stream_of(a[7])), "mmq_kv_read");
+    check(mmq_kv_read(c, &sq, tokens, &hk, &hv, stream), "mmq_kv_read");
     PyObject *p = THPVariable_Wrap(std::move(k)), *s = THPVariable_Wrap(std::move(v));
     PyObject* both = PyTuple_Pack(2, p, s);
     Py_XDECREF(p);
@@ -230,6 +246,7 @@ PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
 // workspace, stream
 PyObject* attention(PyObject* const* a, Py_ssize_t n) {
     need(n, 15);
+    const OnStream stream(a[14]);
     const at::Tensor& q = tensor(a[0], "q");
     const mmq_kv_cache* c = cache_of(a[1]);
     const mmq_heads hq = heads(q, "q");
@@ -254,7 +271,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
     }
     check(mmq_attention(&hq, (int)h, c, &sq, tokens, max_tokens, max_kv, scale, truth(a[8]), integer(a[9]), &ho,
                         lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                        ws.defined() ? ws.data_ptr() : nullptr, size, stream_of(a[14])),
+                        ws.defined() ? ws.data_ptr() : nullptr, size, stream),
           "mmq_attention");
     if (!lse.defined()) return THPVariable_Wrap(std::move(out));
     PyObject *p = THPVariable_Wrap(std::move(out)), *s = THPVariable_Wrap(std::move(lse));

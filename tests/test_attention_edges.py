@@ -19,3 +19,72 @@ def test_windows_that_hide_nothing(n):
     want = check_attention(lens, n, 4, 1, 128, 64, 16)
     for window in (9001, 1 << 31, sys.maxsize):
         assert torch.equal(check_attention(lens, n, 4, 1, 128, 64, 16, window=window), want)
+
+
+def busy(stream):
+    """Keep the stream from what is queued next for some 10 ms."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 70])
+def test_workspace_stays_with_the_call_s_stream(n):
+    """Neither output nor workspace given, another stream that is busy: memory taken and filled at once on the current
+    stream is not the call's."""
+    cache, table = make_cache(torch.Generator().manual_seed(n), [9001], 1, 128, 64, 16)
+    q = torch.randn(n, 4, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    kv, cu, tb = torch.tensor([9001], dtype=torch.int32, device="cuda"), offsets([n]).cuda(), table.cuda()
+    want, wlse = api.attention(q, cache, tb, kv, 9001, cu, n, return_lse=True)
+    size = api.attention_workspace_bytes(n, 4, 1, 128, 1, n, 9001)
+    assert size > 0
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        api.attention(q, cache, tb, kv, 9001, cu, n, stream=st)          # both streams have memory of these sizes
+        junk = [torch.full((size // 4,), float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        busy(st)
+        out, lse = api.attention(q, cache, tb, kv, 9001, cu, n, return_lse=True, stream=st)
+        junk = [torch.full((size // 4,), float("nan"), device="cuda") for _ in range(4)]
+        assert not st.query()                                 # the call has not run yet
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wlse) and all(j.isnan().all() for j in junk)
+
+
+@gpu
+def test_outputs_take_no_memory_that_another_stream_still_reads():
+    g = torch.Generator().manual_seed(3)
+    cache, table = make_cache(g, [64], 2, 64, 64, 16)
+    tb, kv, cu = table.cuda(), torch.tensor([64], dtype=torch.int32, device="cuda"), offsets([64]).cuda()
+    x = torch.randn(64, 2, 64, generator=g).cuda()
+    w = torch.ones(64, device="cuda")
+    q = x.bfloat16()
+    calls = {
+        "norm": lambda st: api.qk_norm_rope(x, None, q_weight=w, stream=st)[0],
+        "append": lambda st: api.kv_append(cache, x, x, tb, kv, cu, q=x, q_weight=w, stream=st),
+        "read": lambda st: api.kv_read(cache, tb, kv, 64, cu, torch.float32, stream=st)[0],
+        "attention": lambda st: api.attention(q, cache, tb, kv, 64, cu, 64, out_dtype=torch.float32, stream=st),
+    }
+    for name, call in calls.items():
+        st, mine = torch.cuda.Stream(), torch.cuda.current_stream()
+        torch.cuda.synchronize()
+        call(st)                                              # the stream has memory of this size
+        torch.cuda.synchronize()
+        held = [torch.full_like(x, float(i)) for i in range(8)]
+        copies = [torch.empty_like(x) for _ in held]
+        torch.cuda.synchronize()
+        busy(mine)
+        for h, c in zip(held, copies):
+            c.copy_(h)                                        # queued behind the wait
+        held = h = None                                       # given back while still to be read
+        outs = [call(st) for _ in range(4)]
+        st.synchronize()
+        assert not mine.query(), name
+        mine.synchronize()
+        for i, c in enumerate(copies):
+            assert (c == i).all(), name
+        want = call(None)
+        for o in outs:
+            assert torch.equal(o, want), name
