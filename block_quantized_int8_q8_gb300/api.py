@@ -5,6 +5,9 @@ Every function forwards device pointers, sizes and the current CUDA stream to th
 include/mmq.h; all arithmetic runs in the library's sm_103a kernels.  PyTorch is used only for device
 memory and streams.  If the library is missing or fails to load, every call raises: there is no CPU
 fallback.
+
+stream=: the stream to launch on (default: the current one).  Outputs and workspaces that a call makes come from
+that stream's memory, as under torch.cuda.stream(stream); inputs have to be complete for it.
 """
 from __future__ import annotations
 
@@ -110,6 +113,14 @@ def _stream(stream) -> int:
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    # from the memory of the stream that writes it: the current stream may hand out again, or still read, its own
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     if t is None:
         return None
@@ -184,7 +195,7 @@ def quantize_q8_1(x: torch.Tensor, out: torch.Tensor | None = None, stream=None)
     """x f32 [M, K] on the GPU -> q8_1 byte buffer (mmq_quantize_q8_1)."""
     M, K = x.shape
     if out is None:
-        out = torch.empty(q8_1_bytes(M, K), dtype=torch.uint8, device=x.device)
+        out = _empty(q8_1_bytes(M, K), torch.uint8, x.device, stream)
     _check(load().mmq_quantize_q8_1(_ptr(x), M, K, _ptr(out), _stream(stream)), "mmq_quantize_q8_1")
     return out
 
@@ -193,7 +204,7 @@ def gemm(wtype: int, W: torch.Tensor, Xq: torch.Tensor, M: int, N: int, K: int, 
          stream=None) -> torch.Tensor:
     """Dense MMQ product (mmq_gemm): f32 [M, N] (bf16 for W8A8)."""
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16 if wtype == W8A8 else torch.float32, device=W.device)
+        out = _empty((M, N), torch.bfloat16 if wtype == W8A8 else torch.float32, W.device, stream)
     _check(load().mmq_gemm(wtype, _ptr(W), _ptr(Xq), _ptr(out), M, N, K, _stream(stream)), "mmq_gemm")
     return out
 
@@ -202,7 +213,7 @@ def gemm_debug_partials(wtype: int, W: torch.Tensor, Xq: torch.Tensor, M: int, N
                         stream=None) -> torch.Tensor:
     """Exact per-group int32 dots (mmq_gemm_debug_partials): [M, N, K/G]."""
     G = 16 if wtype == IQ1_M else 32
-    out = torch.empty((M, N, K // G), dtype=torch.int32, device=W.device)
+    out = _empty((M, N, K // G), torch.int32, W.device, stream)
     _check(load().mmq_gemm_debug_partials(wtype, _ptr(W), _ptr(Xq), _ptr(out), M, N, K, _stream(stream)),
            "mmq_gemm_debug_partials")
     return out
@@ -211,7 +222,7 @@ def gemm_debug_partials(wtype: int, W: torch.Tensor, Xq: torch.Tensor, M: int, N
 def gemm_debug_block_sums(wtype: int, W: torch.Tensor, Xq: torch.Tensor, M: int, N: int, K: int,
                           stream=None) -> torch.Tensor:
     """The TMA-fed kernel's exact 32-k block accumulators (mmq_gemm_debug_block_sums): int32 [M, N, K/32]."""
-    out = torch.empty((M, N, K // 32), dtype=torch.int32, device=W.device)
+    out = _empty((M, N, K // 32), torch.int32, W.device, stream)
     _check(load().mmq_gemm_debug_block_sums(wtype, _ptr(W), _ptr(Xq), _ptr(out), M, N, K, _stream(stream)),
            "mmq_gemm_debug_block_sums")
     return out
@@ -223,10 +234,10 @@ def gemm_id(wtype: int, W: torch.Tensor, n_experts: int, Xq: torch.Tensor, ids: 
     """MoE MUL_MAT_ID (mmq_gemm_id): f32 [M, slots, N]."""
     slots = ids.shape[1]
     if out is None:
-        out = torch.empty((M, slots, N), dtype=torch.float32, device=W.device)
+        out = _empty((M, slots, N), torch.float32, W.device, stream)
     need = gemm_id_workspace_bytes(M, K, slots, n_experts)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=W.device)
+        workspace = _empty(max(need, 16), torch.uint8, W.device, stream)
     _check(load().mmq_gemm_id(wtype, _ptr(W), n_experts, _ptr(Xq), _ptr(ids), slots, _ptr(out), M, N, K,
                               _ptr(workspace), workspace.numel(), _stream(stream)), "mmq_gemm_id")
     return out
@@ -238,7 +249,7 @@ def gemm_id_noalloc(wtype: int, W: torch.Tensor, n_experts: int, Xq: torch.Tenso
     library's static device scratch array, for callers that cannot allocate device memory."""
     slots = ids.shape[1]
     if out is None:
-        out = torch.empty((M, slots, N), dtype=torch.float32, device=W.device)
+        out = _empty((M, slots, N), torch.float32, W.device, stream)
     _check(load().mmq_gemm_id_noalloc(wtype, _ptr(W), n_experts, _ptr(Xq), _ptr(ids), slots, _ptr(out), M, N, K,
                                       _stream(stream)), "mmq_gemm_id_noalloc")
     return out
@@ -253,9 +264,10 @@ def read_device_errors(stream=None) -> int:
 
 def selftest_bounded_wait(device="cuda", stream=None) -> list[int]:
     """mmq_selftest_bounded_wait: [completed, abort_flag] of the polling and of the sleeping wait."""
-    res = torch.full((4,), -1, dtype=torch.int32, device=device)
-    _check(load().mmq_selftest_bounded_wait(_ptr(res), _stream(stream)), "mmq_selftest_bounded_wait")
-    return res.cpu().tolist()
+    with torch.cuda.stream(stream):
+        res = torch.full((4,), -1, dtype=torch.int32, device=device)
+        _check(load().mmq_selftest_bounded_wait(_ptr(res), _stream(stream)), "mmq_selftest_bounded_wait")
+        return res.cpu().tolist()
 
 
 # ------------------------------------------------------------------------------- attention over the 8-bit cache
@@ -297,7 +309,6 @@ class KVCache:
 
 
 def _handle(stream) -> int | None:
-    # outputs and workspaces of a call come from its stream's memory, as under torch.cuda.stream(stream)
     return None if stream is None else stream.cuda_stream
 
 
