@@ -618,6 +618,9 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         }
         if (ok) {
             const bool none = span[i].e <= span[i].s;         // no tile: O was never written
+            // nor has a product shown that the row tile's other warps are done with the queries' place, which the outputs
+            // go through: they meet first
+            if (none) asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long all_rows = (long long)a.sq.tokens * a.heads, row = tok * a.heads + hrow;
             const bool part = rg.parts > 1;

@@ -88,3 +88,23 @@ def test_outputs_take_no_memory_that_another_stream_still_reads():
         want = call(None)
         for o in outs:
             assert torch.equal(o, want), name
+
+
+@gpu
+@pytest.mark.parametrize("D,group", [(64, 1), (128, 4), (256, 2)])
+@pytest.mark.parametrize("ot", [torch.bfloat16, torch.float32])
+def test_prompt_rows_without_any_position_are_zeros(D, group, ot):
+    """Many blocks of rows for which there is no cache tile: their outputs leave while other rows' queries still come in
+    from far apart."""
+    n, seqs, heads = 256 // group + 5, 64, 4
+    cache = api.KVCache.empty(4, heads // group, D, 64, 16)
+    wide = torch.randn(seqs * n, 64, D, device="cuda", generator=torch.Generator("cuda").manual_seed(D)).bfloat16() + 3
+    q = wide[:, ::16]                                         # heads far apart in memory
+    table = torch.zeros(seqs, 1, dtype=torch.int32, device="cuda")
+    kv = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+    cu = offsets([n] * seqs).cuda()
+    for _ in range(10):
+        out = torch.full((seqs * n, heads, D), 5.0, dtype=ot, device="cuda")
+        _, lse = api.attention(q, cache, table, kv, 64, cu, n, out=out, return_lse=True)
+        assert (out == 0).all() and torch.isneginf(lse).all()
+    assert api.read_device_errors() == 0
