@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                     grow |= fmaxf(sc[u][nt][e], sc[u][nt][2 + e]) > m[nt][e] + LAZY;
                 }
         }
-        // the reference of a row (one for the lanes that share its column) is raised when a term passes it by 2^12
+        // the reference of a row (one for the lanes that share its column) is raised when a term passes it by 2^LAZY
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float mn = fmaxf(m[nt][e], top);
+                    const float mn = fmaxf(m[nt][e], top - HEAD);
                     const float f = mn == -INFINITY ? 1.f : ex2(m[nt][e] - mn);
                     m[nt][e] = mn;
                     l[nt][e] *= f;

@@ -349,9 +349,12 @@ mmq_status mmq_kv_read(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64
  * workspace : mmq_attention_workspace_bytes(...) bytes for the same sizes (0: may be null), 16-byte aligned; its
  *          contents on entry do not matter.
  * Arithmetic: cache codes and queries enter the tensor cores as fp16 (codes exactly; a query row is scaled by a
- * power of two first, so bf16's range fits), probabilities as fp16 relative to the row's largest term; scores,
- * statistics and sums are f32.  f32 outputs thus carry the probabilities' 2^-11 relative rounding.  Results do not
- * depend on the order in which blocks of the launch run.
+ * power of two first, so bf16's range fits: its values are exact down to 2^-14 of the row's largest and rounded to
+ * 2^-25 of it below), probabilities as fp16 (2^-11 relative, or 2^-32 of the row's largest term where that is more);
+ * scores, statistics and sums are f32.  f32 outputs thus carry the probabilities' rounding; and where values of one
+ * sign add up over a long range, that of the tensor cores' accumulators, which are truncated after every 16 tokens by
+ * up to 2^-22 of what they hold: 2^-11 in all, since no sum runs over more than 32768 tokens.  Results do not depend
+ * on the order in which blocks of the launch run.
  */
 size_t mmq_attention_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
                                      int64_t max_tokens, int64_t max_kv_len);

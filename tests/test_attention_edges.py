@@ -1,10 +1,11 @@
 """Attention and its cache at the edges of their arguments and inputs (tolerances as in test_attention_ops.py)."""
+import math
 import sys
 
 import pytest
 import torch
 
-from test_attention_ops import check_attention, make_cache, offsets
+from test_attention_ops import assert_close, check_attention, make_cache, offsets
 
 from block_quantized_int8_q8_gb300 import api
 
@@ -107,4 +108,37 @@ def test_prompt_rows_without_any_position_are_zeros(D, group, ot):
         out = torch.full((seqs * n, heads, D), 5.0, dtype=ot, device="cuda")
         _, lse = api.attention(q, cache, table, kv, 64, cu, n, out=out, return_lse=True)
         assert (out == 0).all() and torch.isneginf(lse).all()
+    assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("where", [0, 20000, 40003])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 20])
+def test_one_strong_position_over_a_long_cache_of_weak_ones(n, D, where):
+    """One position 2^16 to 2^34 above 40003 others of equal score and opposite value: together these weigh 2^-1 to 2^-19
+    of it, and keep that share.  Each keeps fp16's bits or is rounded to 2^-36 of the strong one, 2^-20 for all of them, so
+    the tolerance stays.  There are as many sequences as leave the cache of prompts in one piece."""
+    L, seqs, B = 40004, 160, 16
+    pages = -(-L // 64)
+    cache = api.KVCache.empty(pages, 1, D, 64, B)
+    cache.k.zero_()
+    cache.v.fill_(-127)
+    cache.k_scale.fill_(1 / 127)
+    cache.v_scale.fill_(1 / 127)
+    cache.k[where // 64, 0, where % 64, 0] = 127
+    cache.v[where // 64, 0, where % 64] = 127
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(seqs, pages).contiguous()
+    kv = torch.full((seqs,), L, dtype=torch.int32, device="cuda")
+    q = torch.zeros(seqs * n, 1, D, dtype=torch.float16)
+    q[:, 0, 0] = torch.linspace(16, 34, seqs * n).half()      # powers of two: scale ln 2
+    scale = math.log(2)
+    out, lse = api.attention(q.cuda(), cache, table, kv, L, offsets([n] * seqs).cuda(), n, scale=scale, causal=False,
+                             out_dtype=torch.float32, return_lse=True)
+    unit = float(torch.tensor(1 / 127, dtype=torch.float32))
+    s = q[:, 0, 0].double() * 127 * unit * float(torch.tensor(scale, dtype=torch.float32))
+    w = (L - 1) * torch.exp(-s)
+    want = (127 * unit * (1 - w) / (1 + w))[:, None, None].expand(-1, 1, D)
+    assert_close(out, want, torch.full_like(want, 2.0 ** -11 + 2.0 ** -16))
+    assert_close(lse, (s + torch.log1p(w))[:, None], (2.0 ** -18 + 2.0 ** -20 * s)[:, None])
     assert api.read_device_errors() == 0
