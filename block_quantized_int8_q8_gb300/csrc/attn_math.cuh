@@ -8,12 +8,13 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float SCALE_FLOOR = 0x1p-64f;      // stands for a zero value scale (all codes zero) in log2 and 1/x
 // A row's probabilities are 2^(t - m) with m, the reference, 2^HEAD below the largest term when it is set; a term may pass it
-// by 2^LAZY (fp16 ends just below 2^16) before the sums are rescaled.  Terms down to 2^-(HEAD + 14) of the largest then
+// by 2^LAZY before the sums are rescaled (fp16 ends just below 2^16: the rest is for the rounding of t, half a binary order
+// where it is near 2^24).  Terms down to 2^-(HEAD + 14) of the largest then
 // keep fp16's 11 bits and smaller ones are rounded to 2^-(HEAD + 25) of it, so that a long cache of weak terms beside
 // a strong one is not lost: l sums the terms unrounded, and with HEAD 0 the 2^-25 of each made 5e-3 of the output at 131 k
-// tokens.  What HEAD takes from the slack costs rescales: prompts 306 us with a slack of 12, 308 with 9, 321 with 4.
+// tokens.  What HEAD takes from the slack costs rescales: prompts 306 us with a slack of 12, 308 with 8, 321 with 4.
 constexpr float HEAD = 7.f;
-constexpr float LAZY = 15.875f;
+constexpr float LAZY = 15.f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

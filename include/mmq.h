@@ -353,8 +353,9 @@ mmq_status mmq_kv_read(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64
  * 2^-25 of it below), probabilities as fp16 (2^-11 relative, or 2^-32 of the row's largest term where that is more);
  * scores, statistics and sums are f32.  f32 outputs thus carry the probabilities' rounding; and where values of one
  * sign add up over a long range, that of the tensor cores' accumulators, which are truncated after every 16 tokens by
- * up to 2^-22 of what they hold: 2^-11 in all, since no sum runs over more than 32768 tokens.  Results do not depend
- * on the order in which blocks of the launch run.
+ * up to 2^-22 of what they hold: 2^-11 in all, since no sum runs over more than 32768 tokens.  Scores may reach 2^23
+ * in magnitude (f32 then tells them apart by whole binary orders of weight); larger ones are not supported.  Results
+ * do not depend on the order in which blocks of the launch run.
  */
 size_t mmq_attention_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
                                      int64_t max_tokens, int64_t max_kv_len);

@@ -142,3 +142,34 @@ def test_one_strong_position_over_a_long_cache_of_weak_ones(n, D, where):
     assert_close(out, want, torch.full_like(want, 2.0 ** -11 + 2.0 ** -16))
     assert_close(lse, (s + torch.log1p(w))[:, None], (2.0 ** -18 + 2.0 ** -20 * s)[:, None])
     assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("base", [-8e6, -2e6, 1e6, 2e6, 4e6, 8e6])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 40])
+def test_scores_of_large_magnitude(n, D, base):
+    """Scores of up to 2^23 in magnitude, where f32 steps by up to a binary order: equal ones average, and ones that differ
+    by up to 2^20 weigh whatever f32 leaves of their differences, within the largest value."""
+    L, seqs = 1500, 64
+    g = torch.Generator().manual_seed(int(abs(base)) + D)
+    cache, table = make_cache(g, [L], 1, D, 64, 16)
+    cache.k_scale.fill_(1 / 64)
+    cache.v_scale.fill_(1 / 64)
+    cache.k[..., 0] = 64
+    table = table.repeat(seqs, 1).cuda()
+    kv, cu = torch.full((seqs,), L, dtype=torch.int32, device="cuda"), offsets([n] * seqs).cuda()
+    ref = cache.v.double().cpu()[table[0, :-(-L // 64)].long().cpu()][:, 0].reshape(-1, D)[:L] / 64
+    vmax = float(ref.abs().max())
+    q = torch.zeros(seqs * n, 2, D, dtype=torch.bfloat16)
+    q[..., 0] = base
+    out, lse = api.attention(q.cuda(), cache, table, kv, L, cu, n, scale=1.0, causal=False, out_dtype=torch.float32,
+                             return_lse=True)
+    want = ref.mean(0).expand(seqs * n, 2, D)
+    assert_close(out, want, torch.full_like(want, vmax * (2.0 ** -11 + 2.0 ** -16)))
+    s = q[..., 0].double() + math.log(L)
+    assert_close(lse, s, 2.0 ** -18 + 2.0 ** -20 * s.abs())
+    q[..., 1:] = torch.randn(seqs * n, 2, D - 1, generator=g) * 2
+    out = api.attention(q.cuda(), cache, table, kv, L, cu, n, scale=1.0, causal=False, out_dtype=torch.float32)
+    assert torch.isfinite(out).all() and float(out.abs().max()) <= vmax * (1 + 2.0 ** -10)
+    assert api.read_device_errors() == 0
