@@ -289,14 +289,24 @@ def _binding():
 
 class KVCache:
     """One layer's 8-bit paged cache (mmq_kv_cache): int8 codes k, v [pages, kv_heads, page_size, head_dim] and f32
-    scales k_scale, v_scale [pages, kv_heads, page_size / block].  Holds the given tensors; nothing is copied."""
+    scales k_scale, v_scale [pages, kv_heads, page_size / block].  Holds the given tensors for good (the calls use
+    their addresses as they are now); nothing is copied."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim", "block", "_packed")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        self._packed, self.pages, self.kv_heads, self.page_size, self.head_dim, self.block = \
-            (_bind or _binding()).make_cache(k, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        packed, *sizes = (_bind or _binding()).make_cache(k, v, k_scale, v_scale)
+        for name, value in zip(self.__slots__, (k, v, k_scale, v_scale, *sizes, packed)):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KVCache.{name} cannot be set: make another cache")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"KVCache.{name} cannot be deleted")
+
+    def __reduce__(self):                                     # a copy is a cache of the (copied) tensors
+        return type(self), (self.k, self.v, self.k_scale, self.v_scale)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 16, device="cuda"):

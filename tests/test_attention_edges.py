@@ -1,4 +1,5 @@
 """Attention and its cache at the edges of their arguments and inputs (tolerances as in test_attention_ops.py)."""
+import copy
 import math
 import sys
 
@@ -173,3 +174,16 @@ def test_scores_of_large_magnitude(n, D, base):
     out = api.attention(q.cuda(), cache, table, kv, L, cu, n, scale=1.0, causal=False, out_dtype=torch.float32)
     assert torch.isfinite(out).all() and float(out.abs().max()) <= vmax * (1 + 2.0 ** -10)
     assert api.read_device_errors() == 0
+
+
+@gpu
+def test_copies_of_a_cache():
+    cache, table = make_cache(torch.Generator().manual_seed(1), [64], 1, 64, 64, 16)
+    kv, cu, tb = torch.tensor([64], dtype=torch.int32, device="cuda"), offsets([64]).cuda(), table.cuda()
+    shallow, deep = copy.copy(cache), copy.deepcopy(cache)
+    assert shallow.k is cache.k and deep.k.data_ptr() != cache.k.data_ptr()
+    before = api.kv_read(cache, tb, kv, 64, cu)
+    x = torch.full((64, 1, 64), 9.0, device="cuda")
+    api.kv_append(cache, x, x, tb, kv, cu)
+    for c, want in ((shallow, api.kv_read(cache, tb, kv, 64, cu)), (deep, before)):
+        assert all(torch.equal(a, b) for a, b in zip(api.kv_read(c, tb, kv, 64, cu), want))
