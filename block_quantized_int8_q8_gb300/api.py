@@ -311,6 +311,8 @@ class KVCache:
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 16, device="cuda"):
         """A cache of unwritten pages (nothing has to be initialised)."""
+        if block <= 0 or page_size % block:
+            raise MMQError(f"KVCache: page_size {page_size} is not a multiple of block {block}")
         shape = (pages, kv_heads, page_size, head_dim)
         codes = [torch.empty(shape, dtype=torch.int8, device=device) for _ in range(2)]
         scales = [torch.empty((pages, kv_heads, page_size // block), dtype=torch.float32, device=device)
