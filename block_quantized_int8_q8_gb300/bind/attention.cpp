@@ -72,12 +72,20 @@ at::ScalarType scalar_or(PyObject* o, at::ScalarType otherwise) {
     return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
+// The kernels run on the current device; its memory is theirs alone.
+thread_local int t_device;                 // during a call: the current device, -1 until it is asked for
+void on_device(int device, const char* what) {
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    if (device != t_device) refuse(what, "is not on the current device");
+}
+
 // [tokens][heads][head_dim], the last dimension contiguous
 mmq_heads heads(const at::Tensor& t, const char* what) {
     mmq_heads h;
     if (!t.is_cuda() || t.dim() != 3 || !dtype_of(t.scalar_type(), &h.dtype))
         refuse(what, "expected a CUDA tensor [tokens, heads, head_dim] of f32, bf16 or f16");
     if (t.stride(2) != 1) refuse(what, "the last dimension must be contiguous");
+    on_device(t.get_device(), what);
     h.data = t.data_ptr();
     h.token_stride = t.stride(0);
     h.head_stride = t.stride(1);
@@ -88,6 +96,7 @@ void* plain(const at::Tensor* t, at::ScalarType type, long long n, const char* w
     if (t->scalar_type() != type) refuse(what, type == at::kInt ? "expected int32" : "expected float32");
     if (!t->is_cuda() || !t->is_contiguous()) refuse(what, "expected a contiguous CUDA tensor");
     if (n >= 0 && t->numel() != n) refuse(what, "has the wrong number of values");
+    on_device(t->get_device(), what);
     return t->data_ptr();
 }
 const float* vector(PyObject* o, long long n, const char* what) {
@@ -108,9 +117,15 @@ const mmq_rotary* rotary(PyObject* cos, PyObject* sin, PyObject* interleaved, mm
     return r;
 }
 
+struct PackedCache {
+    mmq_kv_cache c;
+    int32_t device;
+};
 const mmq_kv_cache* cache_of(PyObject* o) {
-    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(mmq_kv_cache)) refuse("cache", "expected a KVCache");
-    return reinterpret_cast<const mmq_kv_cache*>(PyBytes_AS_STRING(o));
+    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(PackedCache)) refuse("cache", "expected a KVCache");
+    const auto* p = reinterpret_cast<const PackedCache*>(PyBytes_AS_STRING(o));
+    on_device(p->device, "cache");
+    return &p->c;
 }
 
 mmq_kv_seqs sequences(PyObject* table, PyObject* lens, PyObject* cu) {
@@ -267,6 +282,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
     } else {
         ws = tensor(a[13], "workspace");
         if (!ws.is_cuda() || !ws.is_contiguous()) refuse("workspace", "expected a contiguous CUDA tensor");
+        on_device(ws.get_device(), "workspace");
         size = (size_t)ws.nbytes();
     }
     check(mmq_attention(&hq, (int)h, c, &sq, tokens, max_tokens, max_kv, scale, truth(a[8]), integer(a[9]), &ho,
@@ -281,7 +297,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
     return both;
 }
 
-// k, v, k_scale, v_scale -> (packed mmq_kv_cache, pages, kv_heads, page_size, head_dim, block)
+// k, v, k_scale, v_scale -> (packed cache, pages, kv_heads, page_size, head_dim, block)
 PyObject* make_cache(PyObject* const* a, Py_ssize_t n) {
     need(n, 4);
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &ks = tensor(a[2], "k_scale"), &vs = tensor(a[3], "v_scale");
@@ -291,9 +307,12 @@ PyObject* make_cache(PyObject* const* a, Py_ssize_t n) {
         ks.size(0) != k.size(0) || ks.size(1) != k.size(1) || ks.size(2) <= 0 || k.size(2) % ks.size(2))
         refuse("KVCache", "the scales are f32 tensors [pages, kv_heads, page_size / block]");
     for (const at::Tensor* t : {&k, &v, &ks, &vs})
-        if (!t->is_cuda() || !t->is_contiguous()) refuse("KVCache", "expected contiguous CUDA tensors");
+        if (!t->is_cuda() || !t->is_contiguous() || t->get_device() != k.get_device())
+            refuse("KVCache", "expected contiguous CUDA tensors on one device");
     if (k.size(1) > INT32_MAX || k.size(2) > INT32_MAX || k.size(3) > INT32_MAX) refuse("KVCache", "too large");
-    mmq_kv_cache c{};
+    PackedCache p{};
+    p.device = (int32_t)k.get_device();
+    mmq_kv_cache& c = p.c;
     c.k = static_cast<int8_t*>(k.data_ptr());
     c.v = static_cast<int8_t*>(v.data_ptr());
     c.k_scale = static_cast<float*>(ks.data_ptr());
@@ -303,12 +322,13 @@ PyObject* make_cache(PyObject* const* a, Py_ssize_t n) {
     c.page_size = (int32_t)k.size(2);
     c.head_dim = (int32_t)k.size(3);
     c.block = (int32_t)(k.size(2) / ks.size(2));
-    return Py_BuildValue("(y#Liiii)", reinterpret_cast<const char*>(&c), (Py_ssize_t)sizeof(c), (long long)c.pages,
+    return Py_BuildValue("(y#Liiii)", reinterpret_cast<const char*>(&p), (Py_ssize_t)sizeof(p), (long long)c.pages,
                          (int)c.kv_heads, (int)c.page_size, (int)c.head_dim, (int)c.block);
 }
 
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    t_device = -1;
     try {
         return F(args, n);
     } catch (const PyRaised&) {

@@ -1,12 +1,13 @@
 """Attention and its cache at the edges of their arguments and inputs (tolerances as in test_attention_ops.py)."""
 import copy
 import math
+import struct
 import sys
 
 import pytest
 import torch
 
-from test_attention_ops import assert_close, check_attention, make_cache, offsets
+from test_attention_ops import assert_close, check_attention, make_cache, offsets, rotary_tables
 
 from block_quantized_int8_q8_gb300 import api
 
@@ -187,3 +188,42 @@ def test_copies_of_a_cache():
     api.kv_append(cache, x, x, tb, kv, cu)
     for c, want in ((shallow, api.kv_read(cache, tb, kv, 64, cu)), (deep, before)):
         assert all(torch.equal(a, b) for a, b in zip(api.kv_read(c, tb, kv, 64, cu), want))
+
+
+@gpu
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Tensors that claim to lie on the next device (without memory) in each place of each call."""
+    from torch._subclasses import fake_tensor
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    monkeypatch.setattr(fake_tensor, "init_gpu_context", lambda device: None)      # there need not be such a device
+    far = torch.cuda.current_device() + 1
+    mode = FakeTensorMode()
+
+    def there(t):
+        with mode:
+            return torch.empty(t.shape, dtype=t.dtype, device=f"cuda:{far}")
+
+    cache, table = make_cache(torch.Generator().manual_seed(1), [64], 2, 64, 64, 16)
+    x = torch.randn(64, 2, 64, device="cuda")
+    cos, sin = (t.cuda() for t in rotary_tables(64, 64))
+    w, pos = torch.ones(64, device="cuda"), torch.arange(64, dtype=torch.int32, device="cuda")
+    tb, kv, cu = table.cuda(), torch.tensor([64], dtype=torch.int32, device="cuda"), offsets([64]).cuda()
+    ws = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    calls = (
+        (api.qk_norm_rope, dict(q=x, k=x, positions=pos, cos=cos, sin=sin, q_weight=w, k_weight=w, q_out=x, k_out=x)),
+        (api.kv_append, dict(cache=cache, k=x, v=x, page_table=tb, kv_lens=kv, cu_tokens=cu, cos=cos, sin=sin,
+                             k_weight=w, q=x, q_weight=w, q_out=x.clone())),
+        (api.kv_read, dict(cache=cache, page_table=tb, kv_lens=kv, tokens=64, cu_tokens=cu)),
+        (api.attention, dict(q=x.half(), cache=cache, page_table=tb, kv_lens=kv, max_kv_len=64, cu_tokens=cu,
+                             max_tokens=64, out=x.clone(), workspace=ws)),
+    )
+    elsewhere = copy.copy(cache)
+    object.__setattr__(elsewhere, "_packed", cache._packed[:-8] + struct.pack("=ii", far, 0))
+    for call, given in calls:
+        call(**given)
+        for name, value in given.items():
+            if name == "cache" or torch.is_tensor(value):
+                with pytest.raises(api.MMQError, match="device"):
+                    call(**{**given, name: elsewhere if name == "cache" else there(value)})
+    assert api.read_device_errors() == 0
