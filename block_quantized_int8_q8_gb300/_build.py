@@ -35,15 +35,39 @@ def _deps():
         [os.path.join(ROOT, "include", "mmq.h")]
 
 
+def _newer(lib, deps) -> bool:
+    return os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, _deps()) and _newer(PEAKS_LIB, [PEAKS_SRC, os.path.join(ROOT, "include", "mmq_peaks.h")])
+
+
+def _torch_version() -> str | None:
+    """What a binding is compiled against (its C++ interface changes with the version), None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        return f"{spec.origin}\n{sys.version}\n{f.read()}"
+
+
+def _stamp() -> str:
+    return os.path.join(OBJDIR, "bind_attention.torch")
+
+
+def _binding_up_to_date() -> bool:
+    version = _torch_version()
+    if version is None:
+        return True                                           # nothing could load one
+    if not _newer(BIND_LIB, [BIND_SRC, os.path.join(ROOT, "include", "mmq.h")]) or not os.path.exists(_stamp()):
+        return False
+    with open(_stamp()) as f:
+        return f.read() == version
+
+
 def up_to_date() -> bool:
-    for lib, deps in ((LIB, _deps()), (PEAKS_LIB, [PEAKS_SRC, os.path.join(ROOT, "include", "mmq_peaks.h")]),
-                      (BIND_LIB, [BIND_SRC, os.path.join(ROOT, "include", "mmq.h")])):
-        if not os.path.exists(lib):
-            return False
-        t = os.path.getmtime(lib)
-        if any(os.path.getmtime(d) > t for d in deps):
-            return False
-    return True
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def _run(cmd, what):
@@ -64,8 +88,21 @@ def _bind_object():
     return obj, os.path.join(torch_dir, "lib")
 
 
+def _link_binding(obj, torch_lib):
+    tmp = BIND_LIB + f".tmp{os.getpid()}"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-lc10_cuda", f"-L{LIBDIR}", "-lmmq_gb300", "-Wl,-rpath,$ORIGIN"], "link of the binding failed")
+    os.replace(tmp, BIND_LIB)
+    with open(_stamp(), "w") as f:
+        f.write(_torch_version())
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    """Both libraries, then the binding: the C library needs neither torch nor Python's headers, and is there where
+    compiling the binding fails (which raises) or there is no torch to bind to."""
+    library = force or not _library_up_to_date()
+    binding = _torch_version() is not None and (force or not _binding_up_to_date())
+    if not library and not binding:
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -75,31 +112,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [NVCC, *ARCH, *CFLAGS, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
+        _run(cmd, f"nvcc failed for {src}")
         return obj
 
+    def link(objs, lib):
+        tmp = lib + f".tmp{os.getpid()}"
+        _run([NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"], "link failed")
+        os.replace(tmp, lib)
+
     with ThreadPoolExecutor(max_workers=max(4, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_bind_object)
-        objs = list(ex.map(compile_one, sources() + [PEAKS_SRC]))
-        bind_obj, torch_lib = bind.result()
-    peaks_obj = objs.pop()
-    tmp = PEAKS_LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, peaks_obj, "-lcudart"], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, PEAKS_LIB)
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BIND_LIB + f".tmp{os.getpid()}"
-    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bind_obj, f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
-          "-lc10", "-lc10_cuda", f"-L{LIBDIR}", "-lmmq_gb300", "-Wl,-rpath,$ORIGIN"], "link of the binding failed")
-    os.replace(tmp, BIND_LIB)
+        bind = ex.submit(_bind_object) if binding else None
+        if library:
+            *objs, peaks_obj = ex.map(compile_one, sources() + [PEAKS_SRC])
+            link([peaks_obj], PEAKS_LIB)
+            link(objs, LIB)
+    if bind:
+        _link_binding(*bind.result())
     return LIB
 
 
