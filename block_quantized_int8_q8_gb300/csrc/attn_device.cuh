@@ -89,6 +89,10 @@ struct Seq {
     int len;                   // cached tokens as stated
     int end;                   // tokens the page table can hold, at most len
 };
+// Offsets run from 0 to the number of tokens and do not fall: true where sequence s breaks that.
+__device__ __forceinline__ bool odd_offsets(const SeqArgs& a, int s, int n0, int n1) {
+    return n1 < n0 || (s == 0 && n0 != 0) || (s == a.seqs - 1 && n1 != a.tokens);
+}
 __device__ __forceinline__ Seq make_seq(const SeqArgs& a, int page, int n0, int n1, int len) {
     Seq q;
     q.n0 = max(n0, 0);
@@ -104,7 +108,7 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs& a, int s, int page) {
 
 // The largest s with key(cu[s], s) <= x, for a non-decreasing key with key of 0 <= x, and that sequence; every thread of
 // the block takes part.  Up to THREADS sequences in one round of loads, which brings the sequence's figures too; more by
-// a THREADS-fold narrowing.
+// a THREADS-fold narrowing.  The grid's first block looks over all offsets on the way.
 template <int THREADS, typename Key>
 __device__ __forceinline__ int find_seq(const SeqArgs& a, int page, long long x, Key key, Seq& q) {
     __shared__ int s_seq[3];
@@ -115,6 +119,7 @@ __device__ __forceinline__ int find_seq(const SeqArgs& a, int page, long long x,
             c0 = a.cu[i];
             c1 = a.cu[i + 1];
             len = a.lens[i];
+            if (blockIdx.x == 0 && odd_offsets(a, i, c0, c1)) flag_error(DEVERR_LENGTH);
         }
         const int s = max(__syncthreads_count(i < a.seqs && key(c0, i) <= x) - 1, 0);
         if (i == s) {
@@ -126,6 +131,9 @@ __device__ __forceinline__ int find_seq(const SeqArgs& a, int page, long long x,
         q = make_seq(a, page, s_seq[0], s_seq[1], s_seq[2]);
         return s;
     }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.seqs; i += THREADS)
+            if (odd_offsets(a, i, a.cu[i], a.cu[i + 1])) flag_error(DEVERR_LENGTH);
     int lo = 0, len = a.seqs;
     while (len > 1) {
         const int step = (len + THREADS - 1) / THREADS, at = (int)threadIdx.x * step;

@@ -102,10 +102,12 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     }
     const Seq q = load_seq(a.sq, s, a.c.page);
     const int n = min(q.n, a.max_tokens), r0 = rb * R, rows = min(n * a.group - r0, R);
+    if (split == 0 && head == 0 && rb == 0 && threadIdx.x == 0) {
+        const bool odd = a.sq.cu && odd_offsets(a.sq, s, a.sq.cu[s], a.sq.cu[s + 1]);
+        if (odd || (rows > 0 && (q.n > n || min(q.end, a.max_kv) < q.len))) flag_error(DEVERR_LENGTH);
+    }
     if (rows <= 0) return;
     const Range rg = visible_range(a, q, chunk);
-    if (split == 0 && head == 0 && rb == 0 && threadIdx.x == 0 && (q.n > n || min(q.end, a.max_kv) < q.len))
-        flag_error(DEVERR_LENGTH);
     if (split >= rg.parts) return;
     const int first = q.len - q.n, end = min(q.end, a.max_kv);
     const int i0 = r0 / a.group, i1 = (r0 + rows - 1) / a.group;      // new tokens of the first and the last row

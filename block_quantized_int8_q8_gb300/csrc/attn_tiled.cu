@@ -184,6 +184,9 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         head = sh % a.c.heads;
         s = sh / a.c.heads;
         q = load_seq(a.sq, s, a.c.page);
+        if (split == 0 && head == 0 && qb == 0 && threadIdx.x == 0 && a.sq.cu &&
+            odd_offsets(a.sq, s, a.sq.cu[s], a.sq.cu[s + 1]))
+            flag_error(DEVERR_LENGTH);
     }
     const int n = min(q.n, a.max_tokens), row0 = qb * ROWS, rows = min(n * a.group - row0, ROWS);
     if (rows <= 0 || qb < 0) return;                          // uniform, nothing set up yet

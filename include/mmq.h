@@ -106,8 +106,9 @@ typedef enum {
 #define MMQ_DEVERR_DUP_EXPERT  4u  /* a token listed the same expert twice */
 #define MMQ_DEVERR_PAGE        8u  /* a page table entry in use was outside the cache; its rows were skipped */
 #define MMQ_DEVERR_POSITION   16u  /* a position was outside the rotation table; that token was skipped */
-#define MMQ_DEVERR_LENGTH     32u  /* a sequence was longer than its page table or the stated maximum, or
-                                      its length or token offsets were inconsistent; the excess was skipped */
+#define MMQ_DEVERR_LENGTH     32u  /* a sequence was longer than its page table or the stated maximum, or (append, read)
+                                      shorter than its new tokens, or the token offsets fell or did not run from 0
+                                      to the number of tokens; what does not fit was skipped */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mmq_status_string(mmq_status s);
@@ -289,8 +290,9 @@ typedef struct {
 
 /* The sequences of a batch.  Sequence s has kv_lens[s] cached tokens, its new ones included; position p of it
  * lies in page page_table[s*table_stride + p/page_size].  Its new tokens are packed rows cu_tokens[s] ..
- * cu_tokens[s+1]-1 (cu_tokens int32 [seqs+1]; null: one token for each sequence) and are its last positions.
- * Page table entries past a sequence's length are not used. */
+ * cu_tokens[s+1]-1 (cu_tokens int32 [seqs+1] from 0 to the number of tokens; null: one token for each sequence) and
+ * are its last positions.  Page table entries past a sequence's length are not used.  Rows that no sequence covers, or
+ * past the stated maximum, are left unwritten (mmq_kv_read: zeros). */
 typedef struct {
     const int32_t* page_table;
     int64_t table_stride;          /* entries in a row of the table */
