@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import os
 
 import torch
@@ -292,18 +293,15 @@ class KVCache:
     scales k_scale, v_scale [pages, kv_heads, page_size / block].  Holds the given tensors for good (the calls use
     their addresses as they are now); nothing is copied."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim", "block", "_packed")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_pages", "_kv_heads", "_page_size", "_head_dim", "_block", "_packed")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        packed, *sizes = (_bind or _binding()).make_cache(k, v, k_scale, v_scale)
-        for name, value in zip(self.__slots__, (k, v, k_scale, v_scale, *sizes, packed)):
-            object.__setattr__(self, name, value)
+        self._packed, self._pages, self._kv_heads, self._page_size, self._head_dim, self._block = \
+            (_bind or _binding()).make_cache(k, v, k_scale, v_scale)
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
 
-    def __setattr__(self, name, value):
-        raise AttributeError(f"KVCache.{name} cannot be set: make another cache")
-
-    def __delattr__(self, name):
-        raise AttributeError(f"KVCache.{name} cannot be deleted")
+    k, v, k_scale, v_scale, pages, kv_heads, page_size, head_dim, block = \
+        (property(operator.attrgetter(name)) for name in __slots__[:-1])
 
     def __reduce__(self):                                     # a copy is a cache of the (copied) tensors
         return type(self), (self.k, self.v, self.k_scale, self.v_scale)
@@ -350,7 +348,7 @@ def kv_read(cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, tok
             cu_tokens: torch.Tensor | None = None, dtype=torch.bfloat16, stream=None):
     """The last cu_tokens[s+1] - cu_tokens[s] cached tokens of each sequence, `tokens` in all, as rows (k, v)
     [tokens, kv_heads, head_dim] of `dtype` (mmq_kv_read)."""
-    return (_bind or _binding()).kv_read(cache._packed, cache.k, page_table, kv_lens, tokens, cu_tokens, dtype,
+    return (_bind or _binding()).kv_read(cache._packed, cache._k, page_table, kv_lens, tokens, cu_tokens, dtype,
                                          _handle(stream))
 
 
