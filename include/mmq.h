@@ -322,7 +322,7 @@ mmq_status mmq_qk_norm_rope(const mmq_heads* q, int q_heads, const float* q_weig
  * Quantization, for each block of tokens and head that gets new tokens:
  *   s' = max(s, amax/127) with amax over the block's new values and s the block's scale (0 if the block's first
  *   token is among the new ones; quotients below 2^-63 count as 0); codes already there become
- *   round-half-even(code * (s/s')), new ones round-half-even(x/s') clamped to [-127, 127].
+ *   round-half-even(code * (s/s')), new ones round-half-even(x/s') clamped to [-127, 127], quotients and product in f32.
  * Inputs must be finite.  Two sequences may share pages only if neither appends to a shared block.
  */
 mmq_status mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const mmq_heads* k,
