@@ -80,10 +80,12 @@ struct AttnArgs {
     float scale;
     int causal, window;        // window 0: none
     float* lse;
-    // split along the cache: partial sums of rows [split][row] (row = token * heads + head)
+    // split along the cache, or a part longer than kChain: sums of rows [split][row] (row = token * heads + head)
     float* part_o;             // [splits][rows][dim], not divided by the denominator
     float2* part_ml;           // [splits][rows]: running maximum (log2) and denominator
 };
+// Most tokens that the tiled kernel sums in one go.
+constexpr int kChain = 32768;
 // Thread blocks of the few-row kernel that fit on an SM (its launch bound), for head_dim and 8 or 16 rows.
 constexpr int few_blocks(int dim, int nt) { return dim == 256 ? 2 : (nt == 2 ? 3 : 4); }
 // How a problem is split along the cache: chunk tokens per part, and the parts of the longest sequence.

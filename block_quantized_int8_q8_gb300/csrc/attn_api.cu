@@ -92,15 +92,14 @@ namespace mmq {
 //     SMs idle, so every range of T tokens is cut at c = B (T + 640) / 152: the B whole parts take an SM each, and the
 //     last, shorter ones go one after the other to the SMs left over, all done at about the same time.  (128 blocks of
 //     32 k tokens: 425 us whole, 455 us in two equal parts, 464 us in seven.)  No cut for a rest below ten tiles.
-//     Nor is a part longer than CHAIN tokens: the tensor cores' f32 accumulators are truncated after every 16 tokens,
-//     always to the same side, by up to 2^-22 of what they hold.  131072 tokens in one piece make 2^-9 of it, CHAIN 2^-11.
+//     A part of more than kChain tokens needs its rows' places in the workspace even where it is the only one.
 // A window shortens the range that a sequence's rows see together; the parts stay within what max_kv alone would give,
 // so that the workspace does not depend on it.  One that no sequence outgrows hides nothing and is none: the largest
 // values of its type, a common way to ask for none, take no part in any sum.
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
                         long long max_kv, long long window) {
     AttnPlan p{};
-    constexpr long long SMS = 152, CHAIN = 32768;
+    constexpr long long SMS = 152;
     const long long rows = max_tokens * (heads / kv_heads);
     p.few = rows <= 16;
     const long long pairs = (long long)seqs * kv_heads, granule = p.few ? 64 : 128;
@@ -115,9 +114,8 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
         const long long packed = tokens * group / block + seqs, each = seqs * ((rows + block - 1) / block);
         const long long blocks = kv_heads * (packed < each ? packed : each);
         const long long whole = (range + granule - 1) / granule * granule;
-        long long chunk = blocks < SMS ? (blocks * (range + 640) / SMS + granule - 1) / granule * granule : whole;
-        if (chunk + 1280 > range) chunk = whole;
-        return chunk < 512 ? 512ll : (chunk > CHAIN ? CHAIN : chunk);
+        const long long chunk = blocks < SMS ? (blocks * (range + 640) / SMS + granule - 1) / granule * granule : whole;
+        return chunk + 1280 > range ? (whole > 512 ? whole : 512ll) : (chunk < 512 ? 512ll : chunk);
     };
     auto parts = [](long long range, long long chunk) { return range > chunk ? (range + chunk - 1) / chunk : 1; };
     long long chunk = cut(max_kv);
@@ -132,7 +130,7 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
     }
     p.chunk = (int)chunk;
     size_t off = 0;
-    if (p.splits > 1) {
+    if (p.splits > 1 || (!p.few && chunk > kChain)) {
         const size_t all = (size_t)tokens * heads * p.splits;
         p.part_ml = off;
         off += (all * sizeof(float2) + 255) & ~size_t(255);

@@ -156,7 +156,8 @@ struct TileSpan {
 };
 
 // PACKED: row blocks numbered through the packed rows instead of for every sequence the most that one has.
-template <int D, bool PACKED>
+// LONG: parts may be longer than kChain tokens, after which the sums are put aside.
+template <int D, bool PACKED, bool LONG>
 __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, int chunk, int slots, int qt, int ot) {
     using C = Tiled<D>;
     constexpr int KT = C::kTokens, NQ = C::kQTiles, ROWS = 128 * NQ;
@@ -514,6 +515,15 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         const int k_lo = a.window > 0 ? (max(first + rz / a.group - a.window + 1 - b0, 0) + KT - 1) / KT : 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + C::kOCol + i * D;
+        // Tiles summed in one go, and the row's place for such sums (worked out where it is needed: the rows are hidden from
+        // the compiler, which would keep it in registers throughout).
+        constexpr int CHAIN = kChain / KT;
+        auto place = [&]() {
+            int at = min(r, rows - 1);
+            asm volatile("" : "+r"(at));
+            return (long long)split * a.sq.tokens * a.heads + (q.n0 + (row0 + at) / a.group) * (long long)a.heads +
+                   head * a.group + (row0 + at) % a.group;
+        };
         float m = -INFINITY, l = 0.f, lost = 0.f;
         uint32_t ns = 0;                                      // phase of each buffer's S
         bool ok = true;
@@ -527,6 +537,46 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             }
             ns ^= 1u << buf;
             tc_fence_after();
+            if (LONG && k % CHAIN == 0 && k > k_s) {
+                // The accumulators are truncated after every 16 tokens, always to the same side: by up to 2^-22 of what they
+                // hold, 2^-9 after 131 k tokens.  So every kChain tokens O goes to the row's place in the workspace, with
+                // its l and reference, and starts from zero.  All products so far are complete: S came after them (or the
+                // last one is waited for).
+                if (NQ == 1) {
+                    if (!mbar_wait(bar.pvdone(), (k - k_s - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                const long long at = place();
+                float2 was = make_float2(-INFINITY, 0.f);
+                if (real && k - CHAIN > k_s) was = a.part_ml[at];
+                const float f = was.x == -INFINITY ? 0.f : ex2(was.x - m);
+#pragma unroll 1
+                for (int c = 0; c < D / 16; c++) {
+                    uint32_t o[16];
+                    tmem_ld16(to + 16 * c, o);
+                    tmem_ld_wait(o);
+                    if (real) {
+                        float4* aside = reinterpret_cast<float4*>(a.part_o + at * D + 16 * c);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (f != 0.f) v = aside[e];
+                            aside[e] = make_float4(fmaf(v.x, f, __uint_as_float(o[4 * e])),
+                                                   fmaf(v.y, f, __uint_as_float(o[4 * e + 1])),
+                                                   fmaf(v.z, f, __uint_as_float(o[4 * e + 2])),
+                                                   fmaf(v.w, f, __uint_as_float(o[4 * e + 3])));
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e++) o[e] = 0u;
+                    tmem_st16(to + 16 * c, o);
+                }
+                if (real) a.part_ml[at] = make_float2(m, fmaf(was.y, f, l));
+                l = lost = 0.f;
+            }
             const float4* sc = scales + slot * C::kBlocks;
             const bool masked = k < k_lo || k >= k_hi;
             float x[KT];                                      // the row of S
@@ -615,7 +665,7 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.pready(buf, h));
             }
-            // One rounding a tile: 2^-24 of l to the same side, 256 times a part at most (with one for every 16 tokens, lse
+            // One rounding a tile: 2^-24 of l to the same side, at most 256 times before l is put aside (with one for every 16 tokens, lse
             // was off by 4e-4 after 131 k tokens); the shorter tiles of head_dim 256 carry on what was rounded away.  All of
             // them doing so costs 0.5 %.
             if constexpr (KT < 128) {
@@ -630,6 +680,26 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         if (ok && span[i].e > span[i].s) {
             ok = mbar_wait(bar.odone(i), 0, abort_flag);
             tc_fence_after();
+        }
+        if (LONG && ok && (k_e - 1) / CHAIN * CHAIN > k_s) {  // what was put aside, on the last reference
+            const long long at = place();
+            float2 was = make_float2(-INFINITY, 0.f);
+            if (real) was = a.part_ml[at];
+            const float f = was.x == -INFINITY ? 0.f : ex2(was.x - m);
+            l = fmaf(was.y, f, l);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; c++) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * c, o);
+                tmem_ld_wait(o);
+                if (f != 0.f) {
+                    const float* aside = a.part_o + at * D + 16 * c;
+#pragma unroll
+                    for (int e = 0; e < 16; e++) o[e] = __float_as_uint(fmaf(aside[e], f, __uint_as_float(o[e])));
+                }
+                tmem_st16(to + 16 * c, o);
+            }
+            tmem_st_wait();
         }
         if (ok) {
             const bool none = span[i].e <= span[i].s;         // no tile: O was never written
@@ -707,12 +777,12 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     if (warp == T_MMA) tmem_dealloc(tmem, C::kCols);
 }
 
-template <int D, bool PACKED>
+template <int D, bool PACKED, bool LONG>
 cudaError_t launch_tiled(long long slots, long long blocks, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a,
                          const AttnPlan& p, cudaStream_t s) {
     const long long grid = blocks * a.c.heads * p.splits;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    auto kern = tiled_kernel<D, PACKED>;
+    auto kern = tiled_kernel<D, PACKED, LONG>;
     static bool configured[64] = {};
     bool& done = device_flag(configured);
     if (!done) {
@@ -733,8 +803,12 @@ cudaError_t launch_tiled_rows(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, con
     constexpr int ROWS = 128 * Tiled<D>::kQTiles;
     const long long each = ((long long)a.max_tokens * a.group + ROWS - 1) / ROWS, all = each * a.sq.seqs;
     const long long packed = (long long)a.sq.tokens * a.group / ROWS + a.sq.seqs;
-    if (a.sq.cu && all > 2 * packed) return launch_tiled<D, true>(packed, packed, qt, ot, a, p, s);
-    return launch_tiled<D, false>(each, all, qt, ot, a, p, s);
+    // Parts that no sum has to be put aside in have a kernel without that code: prompts 306 us, 313 with it.
+    const bool by_rows = a.sq.cu && all > 2 * packed, longer = p.chunk > kChain;
+    const long long slots = by_rows ? packed : each, blocks = by_rows ? packed : all;
+    auto launch = by_rows ? (longer ? launch_tiled<D, true, true> : launch_tiled<D, true, false>)
+                          : (longer ? launch_tiled<D, false, true> : launch_tiled<D, false, false>);
+    return launch(slots, blocks, qt, ot, a, p, s);
 }
 
 }  // namespace

@@ -227,3 +227,40 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                 with pytest.raises(api.MMQError, match="device"):
                     call(**{**given, name: elsewhere if name == "cache" else there(value)})
     assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("L,seqs,causal", [(70001, 160, False), (100003, 100, True), (70001, 40, True)])
+def test_sums_put_aside_over_long_caches(L, seqs, causal, D):
+    """Prompts over caches so long that sums are put aside once or twice, in one piece and in parts that are joined; the
+    largest scores early for some rows and late for others."""
+    n, pages = 18, -(-L // 64)
+    g = torch.Generator("cuda").manual_seed(D + seqs)
+    cache = api.KVCache.empty(pages, 1, D, 64, 16)
+    for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        c.copy_((torch.randn(c.shape, device="cuda", generator=g) * 40).round().clamp(-127, 127))
+        s.uniform_(0.001, 0.02, generator=g)
+    tilt = torch.linspace(-100, 100, pages * 64, device="cuda").view(pages, 1, 64)
+    cache.k[..., 0] = tilt.round().to(torch.int8)
+    cache.k_scale.fill_(0.01)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(seqs, pages).contiguous()
+    kv, cu = torch.full((seqs,), L, dtype=torch.int32, device="cuda"), offsets([n] * seqs).cuda()
+    q = torch.randn(seqs * n, 1, D, device="cuda", generator=g)
+    q[:, 0, 0] = torch.linspace(-150, 150, seqs * n, device="cuda")[torch.randperm(seqs * n, device="cuda", generator=g)]
+    q = q.bfloat16()
+    out, lse = api.attention(q, cache, table, kv, L, cu, n, scale=D ** -0.5, causal=causal, out_dtype=torch.float32,
+                             return_lse=True)
+    one, cu1 = kv[:1].clone(), offsets([L]).cuda()
+    k, v = (t[:, 0].double() for t in api.kv_read(cache, table[:1].clone(), one, L, cu1, torch.float32))
+    place = torch.arange(L - n, L, device="cuda").repeat(seqs)
+    for a in range(0, seqs * n, 300):
+        s = q[a:a + 300, 0].double() @ k.T * D ** -0.5
+        if causal:
+            s.masked_fill_(torch.arange(L, device="cuda") > place[a:a + 300, None], -math.inf)
+        want = torch.softmax(s, -1) @ v
+        wlse = torch.logsumexp(s, -1).cpu()
+        # scores reach 2^7 here, four times those that 2^-16 is stated for
+        assert_close(out[a:a + 300, 0], want.cpu(), torch.full_like(want.cpu(), float(v.abs().max()) * (2.0 ** -11 + 2.0 ** -14)))
+        assert_close(lse[a:a + 300, 0], wlse, 2.0 ** -18 + 2.0 ** -20 * wlse.abs())
+    assert api.read_device_errors() == 0

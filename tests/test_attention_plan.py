@@ -59,9 +59,10 @@ def test_parts_fit_the_launch_and_the_workspace(plan):
                              int(2 ** rng.uniform(0, 18))])
         p, whole = (plan(tokens, heads, kv, dim, seqs, most, max_kv, w) for w in (window, 0))
         assert p.total <= whole.total and p.chunk > 0 and p.chunk % 16 == 0
-        assert (p.total == 0) == (p.splits == 1)
-        assert p.chunk <= (2048 if p.few else 32768)          # what a sum of the tensor cores may run over
-        if p.splits > 1:
+        # a sum of the tensor cores runs over 32768 tokens at most: longer parts put it aside in the workspace
+        assert p.chunk <= 2048 if p.few else (p.total > 0) == (p.splits > 1 or p.chunk > 32768)
+        assert p.total > 0 or p.splits == 1
+        if p.total > 0:
             rows = tokens * heads * p.splits
             assert p.part_o >= rows * 8 and p.total - p.part_o >= rows * dim * 4
         for length, n, causal in itertools.product({0, 1, max_kv - 1, max_kv, max_kv + 7, rng.randint(0, max_kv)},
