@@ -42,11 +42,6 @@ long long integer(PyObject* o) {
     if (v == -1 && PyErr_Occurred()) throw PyRaised();
     return v;
 }
-int int32(PyObject* o, const char* what) {
-    const long long v = integer(o);
-    if (v < INT32_MIN || v > INT32_MAX) refuse(what, "out of range");
-    return (int)v;
-}
 float real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw PyRaised();

@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kJoinThreads<W>) join_kernel(const AttnArgs a,
             for (int i = 0; i < 8; i++) {
                 const float fi = __shfl_sync(0xffffffffu, f, i0 + i);             // 0 past the last part
 #pragma unroll
-                for (int e = 0; e < PER; e++)                 // a part that saw nothing wrote no sums
+                for (int e = 0; e < PER; e++)                 // weight 0: past the last part, or nothing seen
                     acc[e] = fmaf(fi == 0.f ? 0.f : x[i][e], fi, acc[e]);
             }
         }

@@ -11,7 +11,7 @@ constexpr float SCALE_FLOOR = 0x1p-64f;      // stands for a zero value scale (a
 // by 2^LAZY before the sums are rescaled (fp16 ends just below 2^16: the rest is for the rounding of t, half a binary order
 // where it is near 2^24).  Terms down to 2^-(HEAD + 14) of the largest then
 // keep fp16's 11 bits and smaller ones are rounded to 2^-(HEAD + 25) of it, so that a long cache of weak terms beside
-// a strong one is not lost: l sums the terms unrounded, and with HEAD 0 the 2^-25 of each made 5e-3 of the output at 131 k
+// a strong one is not lost: l sums the terms unrounded, and with HEAD 0 the 2^-25 of each made 4e-3 of the output at 131 k
 // tokens.  What HEAD takes from the slack costs rescales: prompts 306 us with a slack of 12, 308 with 8, 321 with 4.
 constexpr float HEAD = 7.f;
 constexpr float LAZY = 15.f;

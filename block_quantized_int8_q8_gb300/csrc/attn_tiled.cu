@@ -18,7 +18,7 @@
 //     rescaled only when the maximum outgrows its slack (LAZY), which happens a few times in a row's life.  These warps
 //     also bring the queries in and the outputs out, as whole rows through shared memory.
 // What it measures (GB300; 1909 TFLOP/s is the card's dense fp16 rate): 2048 tokens of 16 heads after 30000 cached ones,
-// 386 us, 1.34 PFLOP/s; prompts of up to 4096 tokens of 32 heads, 304 us, 1.04 PFLOP/s.  A tile of 128 tokens takes a
+// 389 us, 1.34 PFLOP/s; prompts of up to 4096 tokens of 32 heads, 308 us, 1.03 PFLOP/s.  A tile of 128 tokens takes a
 // block 3300 cycles: 1700 to 2000 of products (their operands take 1500 cycles of shared memory reads, the converted
 // codes 500 of writes), the rest is the chain S -> maximum -> exponentials -> P, which two row tiles hide in part.
 // Variants measured slower: two threads a row (chunk 492 -> 625 us), the reference checked after the exponentials

@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(con
 }
 
 // ------------------------------------------------------------------------------------------ read
-// One thread block per 8 packed rows (4 of the widest f32 heads); a group of lanes keeps one row and goes over its heads,
-// a lane turns N codes into one 16-byte store.
+// One thread block per 8 packed rows, or as many as it has groups of lanes (f32 heads of 256: 4, with 128 threads 2); a group
+// keeps one row and goes over its heads, a lane turns N codes into one 16-byte store.
 // four codes -> f32 exactly: the byte spliced into the mantissa of 2^23 + x
 __device__ __forceinline__ void codes_f32(uint32_t w, Quad& x) {
     const uint32_t u = w ^ 0x80808080u;

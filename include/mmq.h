@@ -318,7 +318,9 @@ mmq_status mmq_qk_norm_rope(const mmq_heads* q, int q_heads, const float* q_weig
  * mmq_kv_append -- write the batch's new keys and values to the cache, normed and rotated on the way.
  * k, v: [tokens][kv_heads][head_dim], one type.  Keys are normed where k_weight is given and rotated where
  * rotary is, at their position in the sequence; all in f32, and the f32 result is quantized.  Where q is given,
- * the queries [tokens][q_heads][head_dim] (k's type) are normed and rotated to q_out in the same launch.
+ * the queries [tokens][q_heads][head_dim] (k's type) are normed and rotated to q_out in the same launch; rows of a
+ * position below 0 or outside the rotation table are left unwritten there (MMQ_DEVERR_LENGTH, MMQ_DEVERR_POSITION),
+ * and keys of such positions are not stored.
  * Quantization, for each block of tokens and head that gets new tokens:
  *   s' = max(s, amax/127) with amax over the block's new values and s the block's scale (0 if the block's first
  *   token is among the new ones; quotients below 2^-63 count as 0); codes already there become
