@@ -229,13 +229,10 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     assert api.read_device_errors() == 0
 
 
-@gpu
-@pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("L,seqs,causal", [(70001, 160, False), (100003, 100, True), (70001, 40, True)])
-def test_sums_put_aside_over_long_caches(L, seqs, causal, D):
-    """Prompts over caches so long that sums are put aside once or twice, in one piece and in parts that are joined; the
-    largest scores early for some rows and late for others."""
-    n, pages = 18, -(-L // 64)
+def check_long_caches(L, n, causal, D):
+    """Sequences of n[i] new tokens over one cache of L tokens that they share, the largest scores early for some rows and
+    late for others."""
+    seqs, total, pages = len(n), sum(n), -(-L // 64)
     g = torch.Generator("cuda").manual_seed(D + seqs)
     cache = api.KVCache.empty(pages, 1, D, 64, 16)
     for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
@@ -245,22 +242,38 @@ def test_sums_put_aside_over_long_caches(L, seqs, causal, D):
     cache.k[..., 0] = tilt.round().to(torch.int8)
     cache.k_scale.fill_(0.01)
     table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(seqs, pages).contiguous()
-    kv, cu = torch.full((seqs,), L, dtype=torch.int32, device="cuda"), offsets([n] * seqs).cuda()
-    q = torch.randn(seqs * n, 1, D, device="cuda", generator=g)
-    q[:, 0, 0] = torch.linspace(-150, 150, seqs * n, device="cuda")[torch.randperm(seqs * n, device="cuda", generator=g)]
+    kv, cu = torch.full((seqs,), L, dtype=torch.int32, device="cuda"), offsets(n).cuda()
+    q = torch.randn(total, 1, D, device="cuda", generator=g)
+    q[:, 0, 0] = torch.linspace(-150, 150, total, device="cuda")[torch.randperm(total, device="cuda", generator=g)]
     q = q.bfloat16()
-    out, lse = api.attention(q, cache, table, kv, L, cu, n, scale=D ** -0.5, causal=causal, out_dtype=torch.float32,
+    out, lse = api.attention(q, cache, table, kv, L, cu, max(n), scale=D ** -0.5, causal=causal, out_dtype=torch.float32,
                              return_lse=True)
     one, cu1 = kv[:1].clone(), offsets([L]).cuda()
     k, v = (t[:, 0].double() for t in api.kv_read(cache, table[:1].clone(), one, L, cu1, torch.float32))
-    place = torch.arange(L - n, L, device="cuda").repeat(seqs)
-    for a in range(0, seqs * n, 300):
+    place = torch.cat([torch.arange(L - m, L, device="cuda") for m in n])
+    for a in range(0, total, 300):
         s = q[a:a + 300, 0].double() @ k.T * D ** -0.5
         if causal:
             s.masked_fill_(torch.arange(L, device="cuda") > place[a:a + 300, None], -math.inf)
-        want = torch.softmax(s, -1) @ v
+        want = (torch.softmax(s, -1) @ v).cpu()
         wlse = torch.logsumexp(s, -1).cpu()
         # scores reach 2^7 here, four times those that 2^-16 is stated for
-        assert_close(out[a:a + 300, 0], want.cpu(), torch.full_like(want.cpu(), float(v.abs().max()) * (2.0 ** -11 + 2.0 ** -14)))
+        assert_close(out[a:a + 300, 0], want, torch.full_like(want, float(v.abs().max()) * (2.0 ** -11 + 2.0 ** -14)))
         assert_close(lse[a:a + 300, 0], wlse, 2.0 ** -18 + 2.0 ** -20 * wlse.abs())
     assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("L,seqs,causal", [(70001, 160, False), (100003, 100, True), (70001, 40, True)])
+def test_sums_put_aside_over_long_caches(L, seqs, causal, D):
+    """Prompts over caches so long that sums are put aside once or twice, in one piece and in parts that are joined."""
+    check_long_caches(L, [18] * seqs, causal, D)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_sums_put_aside_in_a_mixed_batch(causal, D):
+    """Rows numbered through the batch: a prompt, single tokens and empty sequences over a cache of three such sums."""
+    check_long_caches(100003, [1, 0] * 60 + [700] + [1, 2, 0] * 40, causal, D)
