@@ -23,7 +23,7 @@ from . import _build
 
 Q8_0, Q4_0, Q4_K, IQ1_M, W8A8, Q6_K = 0, 1, 2, 3, 4, 5
 DEVERR_TIMEOUT, DEVERR_EXPERT_ID, DEVERR_DUP_EXPERT = 1, 2, 4
-DEVERR_PAGE, DEVERR_POSITION, DEVERR_LENGTH = 8, 16, 32
+DEVERR_PAGE, DEVERR_POSITION, DEVERR_LENGTH, DEVERR_DRAFT = 8, 16, 32, 64
 
 #: every symbol include/mmq.h declares
 EXPORTS = ("mmq_status_string", "mmq_last_cuda_error", "mmq_q8_1_bytes", "mmq_weight_bytes", "mmq_w8a8_act_bytes", "mmq_quantize_q8_1",
@@ -92,7 +92,14 @@ def load():
     lib.mmq_attention_workspace_bytes.argtypes = [I64, I, I, I, I, I64, I64]
     lib.mmq_attention_workspace_bytes.restype = SZ
     lib.mmq_attention.argtypes = [P, I, P, P, I64, I64, I64, F, I, I64, P, P, P, SZ, P]
-    for f in (lib.mmq_qk_norm_rope, lib.mmq_kv_append, lib.mmq_kv_read, lib.mmq_attention):
+    lib.mmq_draft_masks.argtypes = [P, P, I, I64, I64, P, P, I, P]
+    lib.mmq_kv_append_tree.argtypes = [P, P, P, I64, P, P, P, P, I, P, P, P, F, P]
+    lib.mmq_attention_tree_workspace_bytes.argtypes = [I64, I, I, I, I, I64, I64]
+    lib.mmq_attention_tree_workspace_bytes.restype = SZ
+    lib.mmq_attention_tree.argtypes = [P, I, P, P, P, I64, I64, I64, F, I64, P, P, P, SZ, P]
+    lib.mmq_kv_keep.argtypes = [P, P, I64, P, I64, P, P]
+    for f in (lib.mmq_qk_norm_rope, lib.mmq_kv_append, lib.mmq_kv_read, lib.mmq_attention, lib.mmq_draft_masks,
+              lib.mmq_kv_append_tree, lib.mmq_attention_tree, lib.mmq_kv_keep):
         f.restype = I
     _lib = lib
     return lib
@@ -336,12 +343,14 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torc
               cu_tokens: torch.Tensor | None = None, cos: torch.Tensor | None = None, sin: torch.Tensor | None = None,
               interleaved: bool = False, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
               q: torch.Tensor | None = None, q_weight: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
-              q_dtype=None, stream=None):
+              q_dtype=None, stream=None, tree: "DraftTree | None" = None):
     """Quantize the new keys and values [tokens, kv_heads, head_dim] into the paged cache, normed and rotated on
     the way (mmq_kv_append).  kv_lens: cached tokens of each sequence, the new ones included.  Returns q_out (the
-    queries normed and rotated in the same launch) where q is given."""
+    queries normed and rotated in the same launch) where q is given.  With a tree of drafted tokens, keys and queries
+    turn at the position of their depth and are stored in row order (mmq_kv_append_tree)."""
+    depths, masks = _of_tree(tree)
     return (_bind or _binding()).kv_append(cache._packed, k, v, page_table, kv_lens, cu_tokens, cos, sin, interleaved,
-                                           k_weight, eps, q, q_weight, q_out, q_dtype, _handle(stream))
+                                           k_weight, eps, q, q_weight, q_out, q_dtype, _handle(stream), depths, masks)
 
 
 def kv_read(cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, tokens: int,
@@ -360,10 +369,55 @@ def attention_workspace_bytes(tokens: int, heads: int, kv_heads: int, head_dim: 
 def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
               max_kv_len: int | None = None, cu_tokens: torch.Tensor | None = None, max_tokens: int | None = None,
               scale: float | None = None, causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
-              out_dtype=None, return_lse: bool = False, workspace: torch.Tensor | None = None, stream=None):
+              out_dtype=None, return_lse: bool = False, workspace: torch.Tensor | None = None, stream=None,
+              tree: "DraftTree | None" = None):
     """softmax(scale q k^T) v over the 8-bit paged cache (mmq_attention): out [tokens, heads, head_dim], or
     (out, lse f32 [tokens, heads]).  max_kv_len and max_tokens bound a sequence's length and new tokens (default:
-    what the page table holds; 1 without cu_tokens, else all tokens); scale defaults to head_dim ** -0.5."""
+    what the page table holds; 1 without cu_tokens, else all tokens); scale defaults to head_dim ** -0.5.  With a tree of
+    drafted tokens, a new token sees the cached ones before them all and, of the new, its ancestors and itself
+    (mmq_attention_tree)."""
+    depths, masks = _of_tree(tree)
     return (_bind or _binding()).attention(q, cache._packed, page_table, kv_lens, max_kv_len, cu_tokens, max_tokens,
                                            scale, causal, window, out, out_dtype, return_lse, workspace,
-                                           _handle(stream))
+                                           _handle(stream), depths, masks)
+
+
+# ------------------------------------------------------------------------------- a tree of drafted tokens
+class DraftTree:
+    """What the new tokens of a batch see of each other (mmq_draft_tree): depths int32 [tokens], the number of a token's
+    ancestors, and masks int32 [tokens, words], bit j % 32 of word j / 32 set where it sees token j of its sequence.
+    draft_tree() makes one from the tokens' parents, once for all layers."""
+
+    __slots__ = ("depths", "masks")
+
+    def __init__(self, depths: torch.Tensor, masks: torch.Tensor):
+        self.depths, self.masks = depths, masks
+
+
+def _of_tree(tree):
+    if tree is None:
+        return None, None
+    if not isinstance(tree, DraftTree):
+        raise MMQError("tree: expected a DraftTree")
+    return tree.depths, tree.masks
+
+
+def draft_tree(parents: torch.Tensor, cu_tokens: torch.Tensor | None = None, max_tokens: int | None = None,
+               stream=None) -> DraftTree:
+    """The tree (or trees) of each sequence's new tokens (mmq_draft_masks).  parents int32 [tokens]: the token that each
+    one continues, counted within its sequence and before it, or -1 for the cached text.  max_tokens bounds a sequence's
+    new tokens (default: 1 without cu_tokens, else all tokens), at most 1024."""
+    return DraftTree(*(_bind or _binding()).draft_masks(parents, cu_tokens, max_tokens, _handle(stream)))
+
+
+def attention_tree_workspace_bytes(tokens: int, heads: int, kv_heads: int, head_dim: int, seqs: int, max_tokens: int,
+                                   max_kv_len: int) -> int:
+    return int(load().mmq_attention_tree_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len))
+
+
+def kv_keep(cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, tokens: int, kept: torch.Tensor,
+            counts: torch.Tensor, cu_tokens: torch.Tensor | None = None, stream=None) -> None:
+    """Of each sequence's new tokens (`tokens` in all, the last of kv_lens), keep those of the rows kept[s, :counts[s]], which
+    ascend, and move them up behind the cached text (mmq_kv_keep).  kept int32 [sequences, rows], counts int32
+    [sequences].  The new lengths are kv_lens minus the new tokens plus counts."""
+    (_bind or _binding()).kv_keep(cache._packed, page_table, kv_lens, tokens, kept, counts, cu_tokens, _handle(stream))

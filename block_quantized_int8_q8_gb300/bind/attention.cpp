@@ -205,9 +205,22 @@ PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
     return both;
 }
 
-// cache, k, v, page_table, kv_lens, cu_tokens, cos, sin, interleaved, k_weight, eps, q, q_weight, q_out, q_dtype, stream
+// The tree of `tokens` packed tokens, or null where none is given.
+const mmq_draft_tree* draft_tree(PyObject* depths, PyObject* masks, long long tokens, mmq_draft_tree* t) {
+    const at::Tensor *d = tensor_or_none(depths, "depths"), *m = tensor_or_none(masks, "masks");
+    if (!d && !m) return nullptr;
+    if (!d || !m || m->dim() != 2 || m->size(0) != tokens || m->size(1) > INT32_MAX)
+        refuse("tree", "expected int32 depths [tokens] and masks [tokens, words]");
+    t->depths = static_cast<const int32_t*>(plain(d, at::kInt, tokens, "depths"));
+    t->masks = static_cast<const uint32_t*>(plain(m, at::kInt, -1, "masks"));
+    t->mask_words = (int32_t)m->size(1);
+    return t;
+}
+
+// cache, k, v, page_table, kv_lens, cu_tokens, cos, sin, interleaved, k_weight, eps, q, q_weight, q_out, q_dtype, stream,
+// depths, masks
 PyObject* kv_append(PyObject* const* a, Py_ssize_t n) {
-    need(n, 16);
+    need(n, 18);
     const OnStream stream(a[15]);
     const mmq_kv_cache* c = cache_of(a[0]);
     const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
@@ -226,10 +239,18 @@ PyObject* kv_append(PyObject* const* a, Py_ssize_t n) {
     const mmq_kv_seqs sq = sequences(a[3], a[4], a[5]);
     mmq_rotary r;
     const mmq_rotary* rot = rotary(a[6], a[7], a[8], &r);
-    check(mmq_kv_append(c, &sq, tokens, &hk, &hv, vector(a[9], dim, "k_weight"), q ? &hq : nullptr,
-                        q ? (int)q->size(1) : 0, vector(a[12], dim, "q_weight"), q ? &hqo : nullptr, rot, real(a[10]),
-                        stream),
-          "mmq_kv_append");
+    mmq_draft_tree d;
+    const mmq_draft_tree* tree = draft_tree(a[16], a[17], tokens, &d);
+    const float *wk = vector(a[9], dim, "k_weight"), *wq = vector(a[12], dim, "q_weight"), eps = real(a[10]);
+    const int q_heads = q ? (int)q->size(1) : 0;
+    if (tree)
+        check(mmq_kv_append_tree(c, &sq, tree, tokens, &hk, &hv, wk, q ? &hq : nullptr, q_heads, wq, q ? &hqo : nullptr,
+                                 rot, eps, stream),
+              "mmq_kv_append_tree");
+    else
+        check(mmq_kv_append(c, &sq, tokens, &hk, &hv, wk, q ? &hq : nullptr, q_heads, wq, q ? &hqo : nullptr, rot, eps,
+                            stream),
+              "mmq_kv_append");
     return q ? THPVariable_Wrap(std::move(qo)) : none();
 }
 
@@ -253,9 +274,9 @@ PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, cache, page_table, kv_lens, max_kv_len, cu_tokens, max_tokens, scale, causal, window, out, out_dtype, return_lse,
-// workspace, stream
+// workspace, stream, depths, masks
 PyObject* attention(PyObject* const* a, Py_ssize_t n) {
-    need(n, 15);
+    need(n, 17);
     const OnStream stream(a[14]);
     const at::Tensor& q = tensor(a[0], "q");
     const mmq_kv_cache* c = cache_of(a[1]);
@@ -267,12 +288,16 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
     const long long max_kv = a[4] == Py_None ? sq.table_stride * c->page_size : integer(a[4]);
     const long long max_tokens = a[6] == Py_None ? (sq.cu_tokens ? tokens : 1) : integer(a[6]);
     const float scale = a[7] == Py_None ? 1.f / std::sqrt((float)dim) : real(a[7]);
+    mmq_draft_tree d;
+    const mmq_draft_tree* tree = draft_tree(a[15], a[16], tokens, &d);
+    if (tree && !truth(a[8])) refuse("attention", "a tree's tokens see their ancestors: causal is true");
     at::Tensor out = output(q, a[10], a[11], "out"), lse, ws;
     const mmq_heads ho = heads(out, "out");
     if (truth(a[12])) lse = at::empty({tokens, h}, q.options().dtype(at::kFloat));
     size_t size = 0;
     if (a[13] == Py_None) {
-        size = mmq_attention_workspace_bytes(tokens, (int)h, c->kv_heads, (int)dim, sq.seqs, max_tokens, max_kv);
+        size = (tree ? mmq_attention_tree_workspace_bytes : mmq_attention_workspace_bytes)(
+            tokens, (int)h, c->kv_heads, (int)dim, sq.seqs, max_tokens, max_kv);
         if (size) ws = at::empty({(long long)size}, q.options().dtype(at::kByte));
     } else {
         ws = tensor(a[13], "workspace");
@@ -280,16 +305,64 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
         on_device(ws.get_device(), "workspace");
         size = (size_t)ws.nbytes();
     }
-    check(mmq_attention(&hq, (int)h, c, &sq, tokens, max_tokens, max_kv, scale, truth(a[8]), integer(a[9]), &ho,
-                        lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                        ws.defined() ? ws.data_ptr() : nullptr, size, stream),
-          "mmq_attention");
+    float* lse_at = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+    void* ws_at = ws.defined() ? ws.data_ptr() : nullptr;
+    if (tree)
+        check(mmq_attention_tree(&hq, (int)h, c, &sq, tree, tokens, max_tokens, max_kv, scale, integer(a[9]), &ho, lse_at,
+                                 ws_at, size, stream),
+              "mmq_attention_tree");
+    else
+        check(mmq_attention(&hq, (int)h, c, &sq, tokens, max_tokens, max_kv, scale, truth(a[8]), integer(a[9]), &ho, lse_at,
+                            ws_at, size, stream),
+              "mmq_attention");
     if (!lse.defined()) return THPVariable_Wrap(std::move(out));
     PyObject *p = THPVariable_Wrap(std::move(out)), *s = THPVariable_Wrap(std::move(lse));
     PyObject* both = PyTuple_Pack(2, p, s);
     Py_XDECREF(p);
     Py_XDECREF(s);
     return both;
+}
+
+// parents, cu_tokens, max_tokens, stream -> (depths, masks)
+PyObject* draft_masks(PyObject* const* a, Py_ssize_t n) {
+    need(n, 4);
+    const OnStream stream(a[3]);
+    const at::Tensor& parents = tensor(a[0], "parents");
+    const at::Tensor* cu = tensor_or_none(a[1], "cu_tokens");
+    if (parents.dim() != 1) refuse("parents", "expected int32 [tokens]");
+    const auto* p = static_cast<const int32_t*>(plain(&parents, at::kInt, -1, "parents"));
+    const auto* c = static_cast<const int32_t*>(plain(cu, at::kInt, -1, "cu_tokens"));
+    const long long tokens = parents.size(0), seqs = cu ? cu->numel() - 1 : tokens;
+    if (seqs < 0 || seqs > INT32_MAX) refuse("cu_tokens", "expected int32 [sequences + 1]");
+    long long most = a[2] == Py_None ? (cu ? tokens : 1) : integer(a[2]);
+    if (most < 0) refuse("draft_tree", "max_tokens is negative");
+    if (most > tokens) most = tokens;
+    const long long words = (most + 31) / 32;
+    if (most > MMQ_MAX_DRAFT) refuse("draft_tree", "a sequence has more drafted tokens than MMQ_MAX_DRAFT");
+    at::Tensor depths = at::empty({tokens}, parents.options()), masks = at::empty({tokens, words}, parents.options());
+    check(mmq_draft_masks(p, c, (int32_t)seqs, tokens, most, static_cast<int32_t*>(depths.data_ptr()),
+                          static_cast<uint32_t*>(masks.data_ptr()), (int32_t)words, stream),
+          "mmq_draft_masks");
+    PyObject *d = THPVariable_Wrap(std::move(depths)), *m = THPVariable_Wrap(std::move(masks));
+    PyObject* both = PyTuple_Pack(2, d, m);
+    Py_XDECREF(d);
+    Py_XDECREF(m);
+    return both;
+}
+
+// cache, page_table, kv_lens, tokens, kept, counts, cu_tokens, stream
+PyObject* kv_keep(PyObject* const* a, Py_ssize_t n) {
+    need(n, 8);
+    const OnStream stream(a[7]);
+    const mmq_kv_cache* c = cache_of(a[0]);
+    const mmq_kv_seqs sq = sequences(a[1], a[2], a[6]);
+    const long long tokens = integer(a[3]);
+    const at::Tensor &kept = tensor(a[4], "kept"), &counts = tensor(a[5], "counts");
+    if (kept.dim() != 2 || kept.size(0) != sq.seqs) refuse("kept", "expected int32 [sequences, rows]");
+    const auto* k = static_cast<const int32_t*>(plain(&kept, at::kInt, -1, "kept"));
+    const auto* m = static_cast<const int32_t*>(plain(&counts, at::kInt, sq.seqs, "counts"));
+    check(mmq_kv_keep(c, &sq, tokens, k, kept.size(1), m, stream), "mmq_kv_keep");
+    return none();
 }
 
 // k, v, k_scale, v_scale -> (packed cache, pages, kv_heads, page_size, head_dim, block)
@@ -349,7 +422,8 @@ PyObject* set_errors(PyObject*, PyObject* types) {
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(qk_norm_rope), FAST(kv_append), FAST(kv_read), FAST(attention), FAST(make_cache),
+PyMethodDef methods[] = {FAST(qk_norm_rope), FAST(kv_append), FAST(kv_read), FAST(attention), FAST(draft_masks),
+                         FAST(kv_keep), FAST(make_cache),
                          {"set_errors", set_errors, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attention", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -61,6 +61,7 @@ struct AppendArgs {
     int q_heads;               // 0: no queries
     RotaryArgs rot;
     float eps;
+    const int32_t* depths;     // null: a token turns at its place, else at this many past the cached text
 };
 cudaError_t run_kv_append(int dim, mmq_dtype t, mmq_dtype qot, const AppendArgs& a, cudaStream_t s);
 
@@ -104,6 +105,44 @@ cudaError_t run_attention_tiled(int dim, mmq_dtype qt, mmq_dtype ot, const AttnA
 // Joins the parts of rows whose cache range was split (attn_few.cu).
 cudaError_t run_attention_join(int dim, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
+// Trees of drafted tokens (draft.cu).
+struct DraftArgs {
+    const int32_t* parents;
+    const int32_t* cu;         // null: token t is sequence t
+    int seqs, tokens, max_tokens;
+    int32_t* depths;
+    uint32_t* masks;
+    int words;                 // of a row of masks
+};
+cudaError_t run_draft_masks(const DraftArgs& a, cudaStream_t s);
+
+struct KeepArgs {
+    CacheArgs c;
+    SeqArgs sq;
+    const int32_t* kept;       // [seqs][stride] rows, of which counts[s] count
+    const int32_t* counts;
+    long long stride;
+};
+cudaError_t run_kv_keep(int dim, const KeepArgs& a, cudaStream_t s);
+
+// Attention of a tree's rows (attn_tree.cu).
+struct TreeArgs {
+    HeadRows q, out;
+    CacheArgs c;
+    SeqArgs sq;
+    const int32_t* depths;
+    const uint32_t* masks;
+    int words;
+    int heads, group;
+    int max_tokens, max_kv;
+    float scale;
+    int window;                // 0: none
+    float* lse;
+};
+cudaError_t run_attention_tree(int dim, mmq_dtype qt, mmq_dtype ot, const TreeArgs& a, cudaStream_t s);
+
+cudaError_t read_clear_errors_draft(unsigned* bits, cudaStream_t s);
+cudaError_t read_clear_errors_attn_tree(unsigned* bits, cudaStream_t s);
 cudaError_t read_clear_errors_kv_cache(unsigned* bits, cudaStream_t s);
 cudaError_t read_clear_errors_attn_few(unsigned* bits, cudaStream_t s);
 cudaError_t read_clear_errors_attn_tiled(unsigned* bits, cudaStream_t s);

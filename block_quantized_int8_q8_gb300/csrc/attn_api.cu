@@ -76,6 +76,40 @@ mmq_status done(cudaError_t e, const char* where) { return e == cudaSuccess ? MM
         if (st_ != MMQ_OK) return st_;                 \
     } while (0)
 
+// What mmq_kv_append and mmq_kv_append_tree (tree given) share.
+mmq_status append(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, const mmq_draft_tree* tree, int64_t tokens,
+                  const mmq_heads* k, const mmq_heads* v, const float* k_weight, const mmq_heads* q, int q_heads,
+                  const float* q_weight, const mmq_heads* q_out, const mmq_rotary* rotary, float eps, cudaStream_t s,
+                  const char* where) {
+    MMQ_TRY(check_cache(cache));
+    bool work;
+    MMQ_TRY(check_seqs(seqs, tokens, &work));
+    MMQ_TRY(check_rotary(rotary, cache->head_dim));
+    if (!q != !q_out || (q && q_heads <= 0)) return MMQ_ERR_INVALID_ARG;
+    if (!work) return MMQ_OK;
+    MMQ_TRY(check_rows(k));
+    MMQ_TRY(check_rows(v));
+    if (q) MMQ_TRY(check_rows(q));
+    if (q) MMQ_TRY(check_rows(q_out));
+    if (k->dtype != v->dtype || (q && q->dtype != k->dtype)) return MMQ_ERR_UNSUPPORTED;
+    MMQ_TRY(check_weight(k_weight));
+    MMQ_TRY(check_weight(q_weight));
+    AppendArgs a{};
+    a.c = cache_of(cache);
+    a.sq = seqs_of(seqs, tokens);
+    a.k = rows_of(k);
+    a.v = rows_of(v);
+    a.q = rows_of(q);
+    a.q_out = rows_of(q_out);
+    a.k_weight = k_weight;
+    a.q_weight = q ? q_weight : nullptr;
+    a.q_heads = q ? q_heads : 0;
+    a.rot = rotary_of(rotary);
+    a.eps = eps;
+    a.depths = tree ? tree->depths : nullptr;
+    return done(run_kv_append(cache->head_dim, k->dtype, q ? q_out->dtype : k->dtype, a, s), where);
+}
+
 }  // namespace
 
 namespace mmq {
@@ -182,33 +216,18 @@ mmq_status mmq_kv_append(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int
                          const mmq_heads* v, const float* k_weight, const mmq_heads* q, int q_heads,
                          const float* q_weight, const mmq_heads* q_out, const mmq_rotary* rotary, float eps,
                          mmq_stream_t stream) {
-    MMQ_TRY(check_cache(cache));
-    bool work;
-    MMQ_TRY(check_seqs(seqs, tokens, &work));
-    MMQ_TRY(check_rotary(rotary, cache->head_dim));
-    if (!q != !q_out || (q && q_heads <= 0)) return MMQ_ERR_INVALID_ARG;
-    if (!work) return MMQ_OK;
-    MMQ_TRY(check_rows(k));
-    MMQ_TRY(check_rows(v));
-    if (q) MMQ_TRY(check_rows(q));
-    if (q) MMQ_TRY(check_rows(q_out));
-    if (k->dtype != v->dtype || (q && q->dtype != k->dtype)) return MMQ_ERR_UNSUPPORTED;
-    MMQ_TRY(check_weight(k_weight));
-    MMQ_TRY(check_weight(q_weight));
-    AppendArgs a{};
-    a.c = cache_of(cache);
-    a.sq = seqs_of(seqs, tokens);
-    a.k = rows_of(k);
-    a.v = rows_of(v);
-    a.q = rows_of(q);
-    a.q_out = rows_of(q_out);
-    a.k_weight = k_weight;
-    a.q_weight = q ? q_weight : nullptr;
-    a.q_heads = q ? q_heads : 0;
-    a.rot = rotary_of(rotary);
-    a.eps = eps;
-    return done(run_kv_append(cache->head_dim, k->dtype, q ? q_out->dtype : k->dtype, a, stream_of(stream)),
-                "mmq_kv_append");
+    return append(cache, seqs, nullptr, tokens, k, v, k_weight, q, q_heads, q_weight, q_out, rotary, eps,
+                  stream_of(stream), "mmq_kv_append");
+}
+
+mmq_status mmq_kv_append_tree(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, const mmq_draft_tree* tree,
+                              int64_t tokens, const mmq_heads* k, const mmq_heads* v, const float* k_weight,
+                              const mmq_heads* q, int q_heads, const float* q_weight, const mmq_heads* q_out,
+                              const mmq_rotary* rotary, float eps, mmq_stream_t stream) {
+    if (!tree || !tree->depths) return MMQ_ERR_INVALID_ARG;
+    if (!aligned16(tree->depths)) return MMQ_ERR_ALIGN;
+    return append(cache, seqs, tree, tokens, k, v, k_weight, q, q_heads, q_weight, q_out, rotary, eps, stream_of(stream),
+                  "mmq_kv_append_tree");
 }
 
 mmq_status mmq_kv_read(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const mmq_heads* k_out,
@@ -283,6 +302,80 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
                           : run_attention_tiled(cache->head_dim, q->dtype, out->dtype, a, p, s);
     if (e == cudaSuccess && p.splits > 1) e = run_attention_join(cache->head_dim, out->dtype, a, p, s);
     return done(e, "mmq_attention");
+}
+
+mmq_status mmq_draft_masks(const int32_t* parents, const int32_t* cu_tokens, int32_t seqs, int64_t tokens,
+                           int64_t max_tokens, int32_t* depths, uint32_t* masks, int32_t mask_words,
+                           mmq_stream_t stream) {
+    if (seqs < 0 || tokens < 0 || max_tokens < 0 || mask_words < 0) return MMQ_ERR_INVALID_ARG;
+    if (tokens > kMaxDim || max_tokens > MMQ_MAX_DRAFT) return MMQ_ERR_SHAPE;
+    if (!cu_tokens && tokens != seqs) return MMQ_ERR_INVALID_ARG;
+    if (tokens == 0) return MMQ_OK;
+    if (seqs == 0 || max_tokens == 0 || !parents || !depths || !masks) return MMQ_ERR_INVALID_ARG;
+    if (mask_words < (max_tokens + 31) / 32 || mask_words * tokens > kMaxDim) return MMQ_ERR_SHAPE;
+    if (!aligned16(parents) || !aligned16(cu_tokens) || !aligned16(depths) || !aligned16(masks)) return MMQ_ERR_ALIGN;
+    const DraftArgs a{parents, cu_tokens, seqs, (int)tokens, (int)max_tokens, depths, masks, mask_words};
+    return done(run_draft_masks(a, stream_of(stream)), "mmq_draft_masks");
+}
+
+mmq_status mmq_kv_keep(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const int32_t* kept,
+                       int64_t kept_stride, const int32_t* counts, mmq_stream_t stream) {
+    MMQ_TRY(check_cache(cache));
+    bool work;
+    MMQ_TRY(check_seqs(seqs, tokens, &work));
+    if (kept_stride < 0) return MMQ_ERR_INVALID_ARG;
+    if (kept_stride > MMQ_MAX_DRAFT) return MMQ_ERR_SHAPE;
+    if (!work) return MMQ_OK;
+    if (!kept || !counts) return MMQ_ERR_INVALID_ARG;
+    if (!aligned16(kept) || !aligned16(counts)) return MMQ_ERR_ALIGN;
+    const KeepArgs a{cache_of(cache), seqs_of(seqs, tokens), kept, counts, kept_stride};
+    return done(run_kv_keep(cache->head_dim, a, stream_of(stream)), "mmq_kv_keep");
+}
+
+size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
+                                          int64_t max_tokens, int64_t max_kv_len) {
+    return 0;
+}
+
+mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs,
+                              const mmq_draft_tree* tree, int64_t tokens, int64_t max_tokens, int64_t max_kv_len,
+                              float scale, int64_t window, const mmq_heads* out, float* lse, void* workspace,
+                              size_t workspace_bytes, mmq_stream_t stream) {
+    MMQ_TRY(check_cache(cache));
+    bool work;
+    MMQ_TRY(check_seqs(seqs, tokens, &work));
+    if (!tree || n_heads <= 0 || max_tokens < 0 || max_kv_len < 0 || window < 0 || !std::isfinite(scale))
+        return MMQ_ERR_INVALID_ARG;
+    if (n_heads % cache->kv_heads || tokens * n_heads > kMaxDim || max_kv_len > kMaxDim - 4096) return MMQ_ERR_SHAPE;
+    if (!work) return MMQ_OK;
+    if (max_tokens == 0) return MMQ_ERR_INVALID_ARG;
+    if (max_tokens > tokens) max_tokens = tokens;
+    if (max_tokens > MMQ_MAX_DRAFT) return MMQ_ERR_SHAPE;
+    MMQ_TRY(check_rows(q));
+    MMQ_TRY(check_rows(out));
+    if (q->dtype == MMQ_F32) return MMQ_ERR_UNSUPPORTED;
+    if (!aligned16(lse)) return MMQ_ERR_ALIGN;
+    const bool windowed = window > 0 && window < max_kv_len;
+    if (windowed && window < max_tokens) return MMQ_ERR_UNSUPPORTED;
+    if (!tree->masks || (windowed && !tree->depths)) return MMQ_ERR_INVALID_ARG;
+    if (tree->mask_words < (max_tokens + 31) / 32 || tree->mask_words * tokens > kMaxDim) return MMQ_ERR_SHAPE;
+    if (!aligned16(tree->masks) || !aligned16(tree->depths)) return MMQ_ERR_ALIGN;
+    TreeArgs a{};
+    a.q = rows_of(q);
+    a.out = rows_of(out);
+    a.c = cache_of(cache);
+    a.sq = seqs_of(seqs, tokens);
+    a.depths = tree->depths;
+    a.masks = tree->masks;
+    a.words = tree->mask_words;
+    a.heads = n_heads;
+    a.group = n_heads / cache->kv_heads;
+    a.max_tokens = (int)max_tokens;
+    a.max_kv = (int)max_kv_len;
+    a.scale = scale;
+    a.window = windowed ? (int)window : 0;
+    a.lse = lse;
+    return done(run_attention_tree(cache->head_dim, q->dtype, out->dtype, a, stream_of(stream)), "mmq_attention_tree");
 }
 
 }  // extern "C"

@@ -12,6 +12,7 @@ namespace mmq {
 constexpr unsigned DEVERR_PAGE = 8u;
 constexpr unsigned DEVERR_POSITION = 16u;
 constexpr unsigned DEVERR_LENGTH = 32u;
+constexpr unsigned DEVERR_DRAFT = 64u;
 
 __device__ __forceinline__ void flag_error(unsigned bit) { atomicOr(&g_mmq_device_errors, bit); }
 
@@ -63,6 +64,14 @@ __device__ __forceinline__ void store4(float* p, const Quad& x) {
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const Quad& x) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f2_lo(x[0]), f2_hi(x[0]), T()), pack2(f2_lo(x[1]), f2_hi(x[1]), T()));
+}
+
+// four codes times a ratio of scales, rounded half to even
+__device__ __forceinline__ uint32_t scale_codes4(uint32_t w, float r) {
+    uint32_t o = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) o |= ((uint32_t)(int)rintf((float)(int8_t)(w >> (8 * i)) * r) & 0xFFu) << (8 * i);
+    return o;
 }
 
 // launch_pdl with dynamic shared memory.

@@ -132,12 +132,6 @@ __device__ __forceinline__ float largest(const Quad& x, float m) {
     m = fmaxf(m, fmaxf(fabsf(f2_lo(x[0])), fabsf(f2_hi(x[0]))));
     return fmaxf(m, fmaxf(fabsf(f2_lo(x[1])), fabsf(f2_hi(x[1]))));
 }
-__device__ __forceinline__ uint32_t scale_codes4(uint32_t w, float r) {
-    uint32_t o = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) o |= ((uint32_t)(int)rintf((float)(int8_t)(w >> (8 * i)) * r) & 0xFFu) << (8 * i);
-    return o;
-}
 
 template <int D, int B, typename T>
 __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int head, bool isv, bool by_token) {
@@ -176,11 +170,14 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     const Chunks ch = head_chunks(l, rotate ? a.rot.half : 0, a.rot.interleaved);
     Raw<T> in0[NR] = {}, in1[NR] = {};
     bool fill[NR];
+    int turn_at[NR];                                         // position that the row turns at
 #pragma unroll
     for (int i = 0; i < NR; i++) {
         const int j = r0 + i * S::kRows, pos = b0 + j;
         fill[i] = j < B && pos >= p0 && pos < q.end;
+        turn_at[i] = pos;
         if (fill[i]) {
+            if (rotate && a.depths) turn_at[i] = p0 + a.depths[q.n0 + pos - p0];
             const T* p = static_cast<const T*>(in.data) + (long long)(q.n0 + pos - p0) * in.ts + head * in.hs;
             in0[i] = load_raw(p + ch.o0);
             in1[i] = load_raw(p + ch.o1);
@@ -202,9 +199,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < NR; i++) {
-        const int pos = b0 + r0 + i * S::kRows;
+        const int pos = turn_at[i];
         if (rotate && fill[i]) {
-            if (pos >= a.rot.positions) {
+            if (pos < 0 || pos >= a.rot.positions) {
                 fill[i] = false;
                 if (l == 0) flag_error(DEVERR_POSITION);
                 x0[i][0] = x0[i][1] = x1[i][0] = x1[i][1] = 0ull;
@@ -267,7 +264,7 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
                 while (s + 1 < a.sq.seqs && a.sq.cu[s + 1] <= t) s++;
                 q = load_seq(a.sq, s, a.c.page);
             }
-            if (t >= q.n0 && t < q.n0 + q.n) pos = q.len - q.n + (t - q.n0);
+            if (t >= q.n0 && t < q.n0 + q.n) pos = q.len - q.n + (a.depths ? a.depths[t] : t - q.n0);
             if (a.rot.cos && pos >= a.rot.positions) {
                 pos = -1;
                 flag_error(DEVERR_POSITION);

@@ -109,6 +109,8 @@ typedef enum {
 #define MMQ_DEVERR_LENGTH     32u  /* a sequence was longer than its page table or the stated maximum, or (append, read)
                                       shorter than its new tokens, or the token offsets fell or did not run from 0
                                       to the number of tokens; what does not fit was skipped */
+#define MMQ_DEVERR_DRAFT      64u  /* a drafted token's parent was not a row before it (taken as -1), or the rows to keep of
+                                      a sequence were too many, not ascending or not its own (it was left as it was) */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mmq_status_string(mmq_status s);
@@ -367,6 +369,78 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
                          int64_t tokens, int64_t max_tokens, int64_t max_kv_len, float scale, int causal,
                          int64_t window, const mmq_heads* out, float* lse, void* workspace,
                          size_t workspace_bytes, mmq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------------
+ * A tree of drafted tokens over the 8-bit cache
+ *
+ * A draft model proposes several continuations of a sequence at once; one pass of the target model checks them all
+ * and one path is kept.  The new tokens of a sequence (mmq_kv_seqs) are then the nodes of a tree, or of several: token i
+ * of a sequence names its parent, a token before it in the sequence, or -1 where it continues the cached text.  Of the new
+ * tokens it sees its ancestors and itself; its depth is the number of its ancestors, its position kv_len - n + depth.
+ * The cache holds the tokens in row order until mmq_kv_keep moves the kept path up.  The pass:
+ *   mmq_draft_masks once; for each layer mmq_kv_append_tree and mmq_attention_tree; the path is chosen; for each layer's
+ *   cache mmq_kv_keep; kv_lens[s] becomes kv_lens[s] - n + counts[s].
+ * A sequence has at most MMQ_MAX_DRAFT new tokens in such a pass.
+ */
+#define MMQ_MAX_DRAFT 1024
+
+/* Depths int32 [tokens] and masks [tokens][mask_words] of packed tokens: bit j % 32 of word j / 32 of token i's mask is set
+ * where it sees token j of its sequence.  mask_words is at least (max_tokens + 31) / 32. */
+typedef struct {
+    const int32_t* depths;
+    const uint32_t* masks;
+    int32_t mask_words;
+} mmq_draft_tree;
+
+/*
+ * mmq_draft_masks -- depths and masks from the parents.
+ * parents   : int32 [tokens], counted within the sequence.  One that is not before its token or below -1 sets
+ *             MMQ_DEVERR_DRAFT and is taken as -1.
+ * cu_tokens : int32 [seqs+1] as in mmq_kv_seqs (null: one token for each sequence).
+ * max_tokens: upper bound of a sequence's new tokens, at most MMQ_MAX_DRAFT.  Tokens past it are left unwritten
+ *             (MMQ_DEVERR_LENGTH).
+ * depths, masks : the outputs; every word of a mask is written.
+ */
+mmq_status mmq_draft_masks(const int32_t* parents, const int32_t* cu_tokens, int32_t seqs, int64_t tokens,
+                           int64_t max_tokens, int32_t* depths, uint32_t* masks, int32_t mask_words,
+                           mmq_stream_t stream);
+
+/*
+ * mmq_kv_append_tree -- mmq_kv_append with the rotation at the tokens' depths: key and query of token i turn at position
+ * kv_len - n + depths[i] (one outside the rotation table is skipped, MMQ_DEVERR_POSITION), and are stored at
+ * kv_len - n + i.  tree's masks are not used and may be null.
+ */
+mmq_status mmq_kv_append_tree(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, const mmq_draft_tree* tree,
+                              int64_t tokens, const mmq_heads* k, const mmq_heads* v, const float* k_weight,
+                              const mmq_heads* q, int q_heads, const float* q_weight, const mmq_heads* q_out,
+                              const mmq_rotary* rotary, float eps, mmq_stream_t stream);
+
+/*
+ * mmq_attention_tree -- mmq_attention where token i of a sequence's n new ones sees the cached positions j < kv_len - n and, of
+ * the new tokens, those that its mask says.  With window > 0 it sees j > kv_len - n + depths[i] - window only; a window must
+ * not hide a new token: one below max_tokens is refused (MMQ_ERR_UNSUPPORTED).  depths are used with a window only and may
+ * be null without.  max_tokens is at most MMQ_MAX_DRAFT.  The other arguments, the arithmetic and its bounds are
+ * mmq_attention's; the workspace is mmq_attention_tree_workspace_bytes(...) bytes.
+ */
+size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
+                                          int64_t max_tokens, int64_t max_kv_len);
+mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs,
+                              const mmq_draft_tree* tree, int64_t tokens, int64_t max_tokens, int64_t max_kv_len,
+                              float scale, int64_t window, const mmq_heads* out, float* lse, void* workspace,
+                              size_t workspace_bytes, mmq_stream_t stream);
+
+/*
+ * mmq_kv_keep -- keep some of the new tokens of each sequence: token kept[s*kept_stride + i] of its n new ones moves to
+ * position kv_len - n + i, for i < counts[s].  The rows ascend (0 <= kept[0] < kept[1] < ...); a sequence where they do
+ * not, or where counts[s] is negative or above n or kept_stride, is left as it was (MMQ_DEVERR_DRAFT).  kv_lens are the
+ * lengths before the call and are not changed; what was cached past the kept tokens is undefined afterwards.
+ * A block into which a token moves gets the largest scale s' that one of its tokens had (those that stay in it among
+ * them); a code of a token whose block had the scale s becomes round-half-even(code * (s/s')), quotient and product in f32
+ * (0 where s' is 0).  A block whose tokens all stay is not touched.  Tokens on an invalid page become zeros.
+ * kept_stride is at most MMQ_MAX_DRAFT.
+ */
+mmq_status mmq_kv_keep(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const int32_t* kept,
+                       int64_t kept_stride, const int32_t* counts, mmq_stream_t stream);
 
 #ifdef __cplusplus
 }
