@@ -30,7 +30,9 @@ EXPORTS = ("mmq_status_string", "mmq_last_cuda_error", "mmq_q8_1_bytes", "mmq_we
            "mmq_gemm", "mmq_gemm_id_workspace_bytes", "mmq_gemm_id", "mmq_gemm_debug_partials",
            "mmq_gemm_debug_block_sums", "mmq_selftest_bounded_wait",
            "mmq_read_device_errors", "mmq_gemm_id_noalloc", "mmq_q8_1_prepare",
-           "mmq_qk_norm_rope", "mmq_kv_append", "mmq_kv_read", "mmq_attention_workspace_bytes", "mmq_attention")
+           "mmq_qk_norm_rope", "mmq_kv_append", "mmq_kv_read", "mmq_attention_workspace_bytes", "mmq_attention",
+           "mmq_draft_masks", "mmq_kv_append_tree", "mmq_attention_tree_workspace_bytes", "mmq_attention_tree",
+           "mmq_kv_keep")
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
 _lib = None

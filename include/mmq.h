@@ -374,7 +374,7 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
  * A tree of drafted tokens over the 8-bit cache
  *
  * A draft model proposes several continuations of a sequence at once; one pass of the target model checks them all
- * and one path is kept.  The new tokens of a sequence (mmq_kv_seqs) are then the nodes of a tree, or of several: token i
+ * and one path is kept.  The new tokens of a sequence of the batch are then the nodes of a tree, or of several: token i
  * of a sequence names its parent, a token before it in the sequence, or -1 where it continues the cached text.  Of the new
  * tokens it sees its ancestors and itself; its depth is the number of its ancestors, its position kv_len - n + depth.
  * The cache holds the tokens in row order until mmq_kv_keep moves the kept path up.  The pass:
@@ -396,7 +396,7 @@ typedef struct {
  * mmq_draft_masks -- depths and masks from the parents.
  * parents   : int32 [tokens], counted within the sequence.  One that is not before its token or below -1 sets
  *             MMQ_DEVERR_DRAFT and is taken as -1.
- * cu_tokens : int32 [seqs+1] as in mmq_kv_seqs (null: one token for each sequence).
+ * cu_tokens : int32 [seqs+1] as in the batch's mmq_kv_seqs; null: one token for each sequence.
  * max_tokens: upper bound of a sequence's new tokens, at most MMQ_MAX_DRAFT.  Tokens past it are left unwritten
  *             (MMQ_DEVERR_LENGTH).
  * depths, masks : the outputs; every word of a mask is written.
