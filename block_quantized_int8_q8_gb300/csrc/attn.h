@@ -139,7 +139,15 @@ struct TreeArgs {
     int window;                // 0: none
     float* lse;
 };
-cudaError_t run_attention_tree(int dim, mmq_dtype qt, mmq_dtype ot, const TreeArgs& a, cudaStream_t s);
+// How a problem is shared out: rows of a row block, ranges of the line of tiles, workspace offsets and size.
+struct TreePlan {
+    int rows, ranges;
+    bool many_parts;           // a unit is cut into many
+    size_t joins, part_ml, part_o, total;
+};
+TreePlan tree_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv);
+cudaError_t run_attention_tree(int dim, mmq_dtype qt, mmq_dtype ot, const TreeArgs& a, const TreePlan& p, void* workspace,
+                               cudaStream_t s);
 
 cudaError_t read_clear_errors_draft(unsigned* bits, cudaStream_t s);
 cudaError_t read_clear_errors_attn_tree(unsigned* bits, cudaStream_t s);

@@ -334,7 +334,12 @@ mmq_status mmq_kv_keep(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64
 
 size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
                                           int64_t max_tokens, int64_t max_kv_len) {
-    return 0;
+    if (tokens <= 0 || n_heads <= 0 || kv_heads <= 0 || n_heads % kv_heads || !head_dim_ok(head_dim) || seqs <= 0 ||
+        max_tokens <= 0 || max_kv_len < 0 || max_kv_len > kMaxDim - 4096 || tokens > kMaxDim || tokens * n_heads > kMaxDim)
+        return 0;
+    if (max_tokens > tokens) max_tokens = tokens;
+    if (max_tokens > MMQ_MAX_DRAFT) return 0;
+    return tree_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len).total;
 }
 
 mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs,
@@ -360,6 +365,9 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     if (!tree->masks || (windowed && !tree->depths)) return MMQ_ERR_INVALID_ARG;
     if (tree->mask_words < (max_tokens + 31) / 32 || tree->mask_words * tokens > kMaxDim) return MMQ_ERR_SHAPE;
     if (!aligned16(tree->masks) || !aligned16(tree->depths)) return MMQ_ERR_ALIGN;
+    const TreePlan p = tree_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
+    if (!workspace || workspace_bytes < p.total) return MMQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
     TreeArgs a{};
     a.q = rows_of(q);
     a.out = rows_of(out);
@@ -375,7 +383,8 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     a.scale = scale;
     a.window = windowed ? (int)window : 0;
     a.lse = lse;
-    return done(run_attention_tree(cache->head_dim, q->dtype, out->dtype, a, stream_of(stream)), "mmq_attention_tree");
+    return done(run_attention_tree(cache->head_dim, q->dtype, out->dtype, a, p, workspace, stream_of(stream)),
+                "mmq_attention_tree");
 }
 
 }  // extern "C"

@@ -4,8 +4,8 @@ import struct
 
 import pytest
 
-from test_attention_host import (ALIGN, CACHE_AND_SEQS, F16, F32, FAKE, INVALID, SHAPE, UNSUPPORTED, cache, heads, lib,
-                                 rotary, seqs)  # noqa: F401
+from test_attention_host import (ALIGN, BF16, CACHE_AND_SEQS, F16, F32, FAKE, INVALID, SHAPE, UNSUPPORTED, WORKSPACE, cache,
+                                 heads, lib, rotary, seqs)  # noqa: F401
 
 from block_quantized_int8_q8_gb300 import api
 
@@ -64,6 +64,47 @@ def test_append_refusals(lib, kw, status):  # noqa: F811
 
 
 @pytest.mark.parametrize("kw,status", CACHE_AND_SEQS + [
+    (dict(t=None), INVALID),
+    (dict(t=tree(masks=None)), INVALID),
+    (dict(t=tree(depths=None), window=500), INVALID),         # a window goes by depth
+    (dict(t=tree(masks=FAKE + 4)), ALIGN),
+    (dict(t=tree(depths=FAKE + 4)), ALIGN),
+    (dict(t=tree(words=0)), SHAPE),
+    (dict(t=tree(words=1 << 30)), SHAPE),
+    (dict(tokens=2000, max_tokens=1025, t=tree(words=33)), SHAPE),
+    (dict(tokens=40, max_tokens=33), SHAPE),                  # more tokens than a mask's words hold
+    (dict(window=3, max_tokens=4), UNSUPPORTED),              # could hide a drafted token
+    (dict(window=-1), INVALID),
+    (dict(hq=0), INVALID),
+    (dict(hq=7), SHAPE),
+    (dict(tokens=1 << 30), SHAPE),
+    (dict(max_tokens=0), INVALID),
+    (dict(max_tokens=-1), INVALID),
+    (dict(max_kv=-1), INVALID),
+    (dict(max_kv=1 << 31), SHAPE),
+    (dict(scale=float("inf")), INVALID),
+    (dict(scale=float("nan")), INVALID),
+    (dict(q=heads(dtype=F32)), UNSUPPORTED),
+    (dict(q=heads(data=None)), INVALID),
+    (dict(out=None), INVALID),
+    (dict(out=heads(ts=4)), ALIGN),
+    (dict(lse=FAKE + 4), ALIGN),
+    (dict(ws=None), WORKSPACE),
+    (dict(ws_bytes=-1), WORKSPACE),                           # one byte short
+    (dict(ws=FAKE + 8), ALIGN),
+])
+def test_attention_refusals(lib, kw, status):  # noqa: F811
+    a = dict(c=cache(), s=seqs(), t=tree(), tokens=5, hq=4, q=heads(), out=heads(), max_tokens=4, max_kv=100000, scale=0.1,
+             window=0, lse=None, ws=FAKE, ws_bytes=0)
+    a.update(kw)
+    need = lib.mmq_attention_tree_workspace_bytes(5, 4, 2, 128, 3, 4, 100000)
+    assert need > 0
+    assert lib.mmq_attention_tree(a["q"], a["hq"], a["c"], a["s"], a["t"], a["tokens"], a["max_tokens"], a["max_kv"],
+                                  a["scale"], a["window"], a["out"], a["lse"], a["ws"], need + a["ws_bytes"],
+                                  None) == status
+
+
+@pytest.mark.parametrize("kw,status", CACHE_AND_SEQS + [
     (dict(kept=None), INVALID),
     (dict(counts=None), INVALID),
     (dict(stride=-1), INVALID),
@@ -75,6 +116,15 @@ def test_keep_refusals(lib, kw, status):  # noqa: F811
     a = dict(c=cache(), s=seqs(), tokens=5, kept=FAKE, stride=4, counts=FAKE)
     a.update(kw)
     assert lib.mmq_kv_keep(a["c"], a["s"], a["tokens"], a["kept"], a["stride"], a["counts"], None) == status
+
+
+def test_workspace_sizes(lib):  # noqa: F811
+    size = lib.mmq_attention_tree_workspace_bytes
+    assert size(26, 32, 8, 128, 1, 26, 100000) >= 26 * 32 * 128 * 4
+    for bad in ((0, 32, 8, 128, 1, 26, 1000), (26, 32, 7, 128, 1, 26, 1000), (26, 32, 8, 96, 1, 26, 1000),
+                (26, 32, 8, 128, 0, 26, 1000), (26, 32, 8, 128, 1, 0, 1000), (26, 32, 8, 128, 1, 26, -1),
+                (2000, 32, 8, 128, 1, 1025, 1000)):
+        assert size(*bad) == 0, bad
 
 
 def test_binding_refuses_what_it_cannot_pass(lib):  # noqa: F811
