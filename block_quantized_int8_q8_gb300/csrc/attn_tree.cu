@@ -8,19 +8,20 @@
 // cache tokens and head dimensions on the 128 lanes and the query rows along the columns:
 //   S^T [128 tokens x R] = K Q^T       K: fp16 codes in TMEM (A operand), Q: shared memory, K-major
 //   O^T [128 dims x R]  += V^T P^T     V: shared memory [token][64 dims of 128 bytes], M-major, P the same way, N-major
-// A thread of the softmax then owns a token, with its scales in registers, and R or R/2 rows of it; what it costs goes with the
-// rows that there are.  K never passes through shared memory, whose bandwidth is the next bound after the cache's.
+// A thread of the softmax then owns a token, with its scales in registers, and a quarter of the rows; what it costs goes with
+// the rows that there are.  K never passes through shared memory, whose bandwidth is the next bound after the cache's.
 //
 // One thread block an SM.  The cache tiles of all (sequence, head, row block) units stand in one line, and each block takes an
 // equal share of it, wherever that begins and ends (lengths are on the device: the blocks work out the line by themselves);
 // units that are cut leave parts in the workspace, which a second launch joins.  Roles:
-//   * eight softmax warps in two groups, each half of the rows: a tile's S^T, the mask, the exponentials, P as fp16 to shared
-//     memory.  The reference m of a row is raised only when a term passes it by 2^LAZY, which a group votes on; then O is
-//     rescaled.  They also bring the queries in and the results out.
-//   * four warps turn the codes of K into fp16 in TMEM and four those of V into shared memory, 16 tokens at a time, with several
-//     such loads in flight.
+//   * sixteen softmax warps in four groups, each a quarter of the rows: a tile's S^T, the mask, the exponentials, P as fp16 to
+//     shared memory.  The reference m of a row is raised only when a term passes it by 2^LAZY, which a group votes on; then
+//     O is rescaled.  They also bring the queries in and the results out.
+//   * four warps turn the codes of K into fp16 in TMEM and seven (128 rows: three) those of V into shared memory, 32 tokens at
+//     a time; the next codes are on their way to the registers that the last ones leave.
 //   * one warp issues the products.
 #include <algorithm>
+#include <type_traits>
 #include "attn_device.cuh"
 #include "attn_math.cuh"
 #include "internal.h"
@@ -30,33 +31,36 @@ namespace mmq {
 namespace {
 
 constexpr int KT = 128;                      // cache tokens of a tile
-constexpr int W_CONVK = 8, W_CONVV = 12, W_MMA = 16;
-constexpr int TREE_THREADS = 17 * 32;
+constexpr int GROUPS = 4, SOFTMAX_WARPS = 4 * GROUPS;                            // of the softmax: a quarter of the rows each
 constexpr int WINDOW = kChain / KT;          // most tiles that are listed, and summed, in one go
-constexpr int SCAN = 512;                    // sequences looked at together
 constexpr float UNSET = 1e30f;               // -m of a row that has seen nothing yet
 
 template <int D, int R> struct Tree {
-    static constexpr int kChunks = D / 64, kHalves = D == 256 ? 2 : 1;           // 64 dimensions; O^T of 128 dimensions
-    static constexpr int kKStages = D == 256 || R == 128 ? 2 : 3;
-    static constexpr int kVStages = D == 64 ? 6 : (D == 128 ? 4 : 2);
-    static constexpr int kPBufs = D == 128 && R == 128 ? 1 : 2;
-    static constexpr int kAhead = D == 64 ? 8 : (D == 128 ? 4 : 2);              // loads of 16 tokens in flight a warp
+    // warps of the converters and the products, after those of the softmax
+    static constexpr int kWarpsV = R == 128 ? 3 : 7;
+    static constexpr int kWarpK = SOFTMAX_WARPS, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kWarpsV, kWarps = kWarpMma + 1;
+    static constexpr int kThreads = kWarps * 32;
+    // registers a thread: 72 at launch of 28 warps; of 24 warps 80, moved to the softmax warps for the longer rows
+    static constexpr int kRegsSoftmax = 88, kRegsRest = 64;
+    static_assert(R == 64 || SOFTMAX_WARPS * kRegsSoftmax + 8 * kRegsRest <= 24 * 80, "register budget");
+    static constexpr int kHalves = D == 256 ? 2 : 1;                             // O^T of 128 dimensions
+    static constexpr int kStrips = D == 256 ? 2 : 1, kChunks = D == 64 ? 1 : 2;   // of up to 128 dimensions, of 64 each
     static constexpr int kVBytes = KT * D * 2, kQBytes = R * D * 2, kPBytes = KT * R * 2;
-    static constexpr int kScaleSlots = 16;
+    static constexpr int kScaleSlots = 8;
     static constexpr int kKCols = D / 2;
+    // TMEM columns: two buffers of S, O, two of K
     static constexpr int kOCol = 2 * R, kKCol = kOCol + kHalves * R;
-    static_assert(kKCol + kKStages * kKCols <= 512, "TMEM budget");
+    static_assert(kKCol + 2 * kKCols <= 512, "TMEM budget");
     // V first: for head_dim 64 the products read the next 16 KB as 64 more dimensions, whose results nothing looks at
     static constexpr int v_off = 0;
-    static constexpr int q_off = v_off + kVStages * kVBytes;
+    static constexpr int q_off = v_off + 2 * kVBytes;
     static constexpr int p_off = q_off + kQBytes;
-    static constexpr int sc_off = p_off + kPBufs * kPBytes;                      // float4 [slots][8]
+    static constexpr int sc_off = p_off + 2 * kPBytes;                           // float4 [slots][8]
     static constexpr int bar_off = sc_off + kScaleSlots * 8 * 16;
-    static constexpr int n_bars = 2 * kKStages + 2 * kVStages + kScaleSlots + 6 + 2 + 1;
+    static constexpr int n_bars = kScaleSlots + 13;
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int total = misc_off + 16, alloc = total + 1024;
-    static_assert(alloc <= 232448 - 26 * 1024, "shared memory budget (the rest is static)");
+    static_assert(alloc <= 232448 - (R == 64 ? 16 : 20) * 1024, "shared memory budget (the rest is static)");
 };
 
 // A run of tiles of one unit (sequence, key/value head, row block) in the block's share.
@@ -78,7 +82,8 @@ struct TreeWork {                // the workspace
     int4* joins;                 // [ranges][2]
 };
 
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) { tmem_ld_wait(r); }
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
@@ -87,7 +92,17 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -131,6 +146,11 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(DESC_HI)
         : "memory");
 }
+// As mbar_wait, the first look without its loop.
+__device__ __forceinline__ bool wait_for(uint32_t b, uint32_t parity, volatile int* abort_flag) {
+    if (__builtin_expect(mbar_try_wait(b, parity), 1)) return true;
+    return mbar_wait(b, parity, abort_flag);
+}
 // Whether any of the 128 threads at named barrier `id` says so.
 __device__ __forceinline__ bool group_any(int id, bool x) {
     uint32_t r;
@@ -147,12 +167,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// 32 values of each lane, joined over the warp: lane c gets the result of the c-th.
-template <bool MAX>
-__device__ __forceinline__ float across(float (&x)[32]) {
+// N values of each lane (16 or 32), joined over the warp: lanes c mod N get the result of the c-th.
+template <bool MAX, int N>
+__device__ __forceinline__ float across(float (&x)[N]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = N / 2; o > 0; o >>= 1) {
 #pragma unroll
         for (int i = 0; i < o; i++) {
             const bool up = lane & o;
@@ -161,26 +181,27 @@ __device__ __forceinline__ float across(float (&x)[32]) {
             x[i] = MAX ? fmaxf(keep, got) : keep + got;
         }
     }
+    if (N == 16) {
+        const float got = __shfl_xor_sync(0xffffffffu, x[0], 16);
+        x[0] = MAX ? fmaxf(x[0], got) : x[0] + got;
+    }
     return x[0];
 }
 
 template <int D, int R> struct TreeBars {
     using C = Tree<D, R>;
     uint32_t b;
-    __device__ uint32_t kfull(int i) const { return b + 8u * i; }
-    __device__ uint32_t kempty(int i) const { return b + 8u * (C::kKStages + i); }
-    __device__ uint32_t vfull(int i) const { return b + 8u * (2 * C::kKStages + i); }
-    __device__ uint32_t vempty(int i) const { return b + 8u * (2 * C::kKStages + C::kVStages + i); }
-    __device__ uint32_t scale(int i) const { return b + 8u * (2 * C::kKStages + 2 * C::kVStages + i); }
-    __device__ uint32_t rest(int i) const {
-        return b + 8u * (2 * C::kKStages + 2 * C::kVStages + C::kScaleSlots + i);
-    }
-    __device__ uint32_t sfull(int i) const { return rest(i); }                   // S of tiles i mod 2
-    __device__ uint32_t pready(int i) const { return rest(2 + i); }
-    __device__ uint32_t pvdone(int i) const { return rest(4 + i); }
-    __device__ uint32_t qfull() const { return rest(6); }                        // a piece's queries
-    __device__ uint32_t ofree() const { return rest(7); }                        // a piece's O is read
-    __device__ uint32_t done() const { return rest(8); }
+    __device__ uint32_t scale(int i) const { return b + 8u * i; }                // a tile's scales are published
+    __device__ uint32_t rest(int i) const { return b + 8u * (C::kScaleSlots + i); }
+    // of tiles i mod 2; S and the product with V release the stages that they read
+    __device__ uint32_t kfull(int i) const { return rest(i); }
+    __device__ uint32_t vfull(int i) const { return rest(2 + i); }
+    __device__ uint32_t sfull(int i) const { return rest(4 + i); }
+    __device__ uint32_t pready(int i) const { return rest(6 + i); }
+    __device__ uint32_t pvdone(int i) const { return rest(8 + i); }
+    __device__ uint32_t qfull() const { return rest(10); }                       // a piece's queries
+    __device__ uint32_t ofree() const { return rest(11); }                       // a piece's O is read
+    __device__ uint32_t done() const { return rest(12); }
 };
 
 // A sequence's place in the line of tiles.
@@ -188,7 +209,7 @@ struct Line {
     Seq q;
     int n, base;                 // new tokens, first token of the first tile
     int blocks;                  // row blocks
-    long long tiles;             // of a unit
+    int tiles;                   // of a unit
 };
 template <int R>
 __device__ __forceinline__ Line line_of(const TreeArgs& a, int s) {
@@ -202,30 +223,28 @@ __device__ __forceinline__ Line line_of(const TreeArgs& a, int s) {
     return x;
 }
 
-template <int D, int R>
-__global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a, const TreeWork work, int qt, int ot) {
-    using C = Tree<D, R>;
-    constexpr int CH = C::kChunks, NC = R / 64;               // 32-column chunks of a group's rows
-    pdl_wait();
-    pdl_trigger();                                            // after the wait: the join reads its inputs before its own
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ Piece s_piece[WINDOW];
-    __shared__ long long s_w[17], s_out[R];
-    __shared__ int s_u[17], s_span[2], s_tok[R], s_low[R];
-    __shared__ float4 s_col[R / 2];                           // of two rows: factors of S, and -m
-    __shared__ float s_m[R], s_fac[R], s_add[R], s_next[R], s_red[2][4][R / 2];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The line of tiles: every sequence's units one after the other, heads before row blocks, shared out evenly.  The host keeps
+// it below 2^31 tiles.
+struct LineShare {
+    int w[32], u[32];            // of the scan
+    int span[2];                 // first and last unit of the window
+    int all, ranges;             // tiles of the line; shares that are not empty
+    __device__ int start(int c) const { return c * (all / ranges) + min(c, all % ranges); }
+    __device__ int range_of(int t) const {
+        const int q = all / ranges, r = all % ranges;
+        return t < r * (q + 1) ? t / (q + 1) : r + (t - r * (q + 1)) / q;
+    }
+};
 
-    // The line of tiles: every sequence's units one after the other, heads before row blocks.
-    const int range = blockIdx.x;
-    auto exclusive = [&](long long w, int u, long long& wx, int& ux, long long& wall, int& uall) {
-        long long wi = w;
-        int ui = u;
+// Lists the pieces of window `window` of this block's share; all its threads take part.  The first call works out the line.
+template <int R>
+__device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& work, LineShare& sh, Piece* pieces, int window) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, range = blockIdx.x;
+    auto exclusive = [&](int w, int u, int& wx, int& ux, int& wall, int& uall) {
+        int wi = w, ui = u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, wi, o);
-            const int z = __shfl_up_sync(0xffffffffu, ui, o);
+            const int v = __shfl_up_sync(0xffffffffu, wi, o), z = __shfl_up_sync(0xffffffffu, ui, o);
             if (lane >= o) {
                 wi += v;
                 ui += z;
@@ -233,70 +252,140 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
         }
         __syncthreads();                                      // the arrays' last readers are done
         if (lane == 31) {
-            s_w[warp] = wi;
-            s_u[warp] = ui;
+            sh.w[warp] = wi;
+            sh.u[warp] = ui;
         }
         __syncthreads();
-        wx = wi - w;
-        ux = ui - u;
-        wall = 0;
-        uall = 0;
-        for (int i = 0; i < 17; i++) {
-            if (i < warp) {
-                wx += s_w[i];
-                ux += s_u[i];
+        // every warp joins the warps' sums for itself
+        int wv = lane < warps ? sh.w[lane] : 0, uv = lane < warps ? sh.u[lane] : 0;
+        const int wm = wv, um = uv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, wv, o), z = __shfl_up_sync(0xffffffffu, uv, o);
+            if (lane >= o) {
+                wv += v;
+                uv += z;
             }
-            wall += s_w[i];
-            uall += s_u[i];
         }
+        wx = wi - w + __shfl_sync(0xffffffffu, wv - wm, warp);
+        ux = ui - u + __shfl_sync(0xffffffffu, uv - um, warp);
+        wall = __shfl_sync(0xffffffffu, wv, 31);
+        uall = __shfl_sync(0xffffffffu, uv, 31);
     };
-    long long all = 0;                                        // tiles of the line
-    for (int s0 = 0; s0 < a.sq.seqs; s0 += SCAN) {
+    Line x{};
+    int w = 0, units = 0, wx = 0, ux = 0, wall = 0, uall = 0;
+    auto look = [&](int s0) {
         const int s = s0 + threadIdx.x;
-        long long w = 0, wx, wall;
-        int ux, uall;
-        if (threadIdx.x < SCAN && s < a.sq.seqs) {
-            const Line x = line_of<R>(a, s);
-            w = x.tiles * x.blocks * a.c.heads;
-            if (range == 0) {
+        w = units = 0;
+        x = Line{};
+        if (s < a.sq.seqs) {
+            x = line_of<R>(a, s);
+            units = x.blocks * a.c.heads;
+            w = x.tiles * units;
+        }
+        exclusive(w, units, wx, ux, wall, uall);
+    };
+    if (window == 0) {
+        int all = 0;
+        for (int s0 = 0; s0 < a.sq.seqs; s0 += blockDim.x) {
+            look(s0);
+            all += wall;
+            const int s = s0 + threadIdx.x;
+            if (range == 0 && s < a.sq.seqs) {
                 const bool odd = a.sq.cu && odd_offsets(a.sq, s, a.sq.cu[s], a.sq.cu[s + 1]);
                 if (odd || (x.n > 0 && (x.q.n > x.n || min(x.q.end, a.max_kv) < x.q.len))) flag_error(DEVERR_LENGTH);
             }
         }
-        exclusive(w, 0, wx, ux, wall, uall);
-        all += wall;
+        if (threadIdx.x == 0) {
+            sh.all = all;
+            sh.ranges = max(min((int)gridDim.x, all), 1);
+        }
+        __syncthreads();
     }
-    const long long ranges = min((long long)gridDim.x, all);
-    if (range >= ranges) {
+    if (range >= sh.ranges || sh.all == 0) {
         if (threadIdx.x == 0) work.joins[2 * range + 1] = make_int4(0, 0, 0, 0);
-        return;                                               // uniform, nothing set up yet
+        return;
     }
-    auto start_of = [&](long long c) { return c * all / ranges; };
-    const long long g0 = start_of(range), g1 = start_of(range + 1);
+    const int g0 = sh.start(range), g1 = sh.start(range + 1), g = g0 + window * WINDOW, gz = min(g + WINDOW, g1);
+    const bool once = a.sq.seqs <= blockDim.x;                // what the first pass saw is still there
+    int wbase = 0, ubase = 0;
+    for (int s0 = 0; wbase < gz; s0 += blockDim.x) {
+        if (!once || window > 0) look(s0);
+        const int ws = wbase + wx, us = ubase + ux;
+        if (ws <= g && g - ws < w) sh.span[0] = us + (g - ws) / x.tiles;
+        if (ws < gz && gz - ws <= w) sh.span[1] = us + (gz - 1 - ws) / x.tiles;
+        __syncthreads();
+        if (ws < gz && g - ws < w) {
+            const int u0 = sh.span[0], first = x.q.len - x.q.n, s = s0 + threadIdx.x;
+            const int k1 = min((gz - 1 - ws) / x.tiles, units - 1);
+            for (int k = g > ws ? (g - ws) / x.tiles : 0; k <= k1; k++) {
+                const int u = ws + k * x.tiles, uz = u + x.tiles, lo = max(u, g), hi = min(uz, gz);
+                Piece p;
+                p.s = s;
+                p.head = k / x.blocks;
+                p.n0 = x.q.n0;
+                p.first = first;
+                p.lim = min(min(x.q.end, a.max_kv), first + x.n);
+                p.row0 = (k - p.head * x.blocks) * R;
+                p.rows = min(x.n * a.group - p.row0, R);
+                p.tok0 = x.base + (lo - u) * KT;
+                p.x0 = lo - g;
+                p.tiles = hi - lo;
+                p.slot = 2 * range + (u > g0);
+                p.flags = (lo > max(u, g0) ? P_PREV : 0) | (hi == uz && u >= g0 ? P_DIRECT : 0);
+                pieces[us + k - u0] = p;
+                if (window == 0 && u <= g0 && uz > g0) {
+                    // the join of the unit that this range begins within, if the range before is the unit's first
+                    int parts = 0, slot0 = 0;
+                    if (u < g0 && u >= sh.start(range - 1)) {
+                        parts = sh.range_of(uz - 1) - (range - 1) + 1;
+                        slot0 = 2 * (range - 1) + (u > sh.start(range - 1));
+                    }
+                    work.joins[2 * range] = make_int4(p.n0, p.row0, p.rows, p.head);
+                    work.joins[2 * range + 1] = make_int4(parts, slot0, 2 * range, 0);
+                }
+            }
+        }
+        wbase += wall;
+        ubase += uall;
+    }
+    __syncthreads();
+}
 
+template <int D, int R>
+__global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
+    tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeWork work, int qt, int ot) {
+    using C = Tree<D, R>;
+    constexpr int N = R / GROUPS;                             // columns of a group
+    constexpr int STRIPS = C::kStrips, CU = C::kChunks;
+    pdl_wait();
+    pdl_trigger();                                            // after the wait: the join reads its inputs before its own
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ Piece s_piece[WINDOW];
+    __shared__ LineShare s_line;
+    __shared__ long long s_out[R];
+    __shared__ int s_tok[R], s_low[R];
+    __shared__ float4 s_col[R / 2];                           // of two rows: factors of S, and -m
+    __shared__ float s_m[R], s_fac[R], s_add[R], s_next[R], s_red[GROUPS][4][N];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sb = smem_u32(smem);
     const TreeBars<D, R> bar{sb + C::bar_off};
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc_off + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc_off);
     float4* scales = reinterpret_cast<float4*>(smem + C::sc_off);
-    if (warp == W_MMA) {
+    if (warp == C::kWarpMma) {
         if (lane == 0) {
-            for (int i = 0; i < C::kKStages; i++) {
-                mbar_init(bar.kfull(i), 8);
-                mbar_init(bar.kempty(i), 1);
-            }
-            for (int i = 0; i < C::kVStages; i++) {
-                mbar_init(bar.vfull(i), 8);
-                mbar_init(bar.vempty(i), 1);
-            }
-            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), 8);
+            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), 4);
             for (int i = 0; i < 2; i++) {
+                mbar_init(bar.kfull(i), 4 * STRIPS);
+                mbar_init(bar.vfull(i), 4 * STRIPS);
                 mbar_init(bar.sfull(i), 1);
-                mbar_init(bar.pready(i), 8);
+                mbar_init(bar.pready(i), SOFTMAX_WARPS);
                 mbar_init(bar.pvdone(i), 1);
             }
-            mbar_init(bar.qfull(), 8);
-            mbar_init(bar.ofree(), 8);
+            mbar_init(bar.qfull(), SOFTMAX_WARPS);
+            mbar_init(bar.ofree(), SOFTMAX_WARPS);
             mbar_init(bar.done(), 1);
             *abort_flag = 0;
             fence_barrier_init();
@@ -305,244 +394,225 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    list_pieces<R>(a, work, s_line, s_piece, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-
-    int y0 = 0, k0 = 0;                                       // tiles and pieces of the windows before
-    for (long long g = g0; g < g1; g += WINDOW) {
-        const long long gz = min(g + WINDOW, g1);
-        const int tiles = (int)(gz - g);
-        // ---- the window's pieces
-        long long wbase = 0;
-        int ubase = 0;
-        for (int s0 = 0; wbase < gz; s0 += SCAN) {
-            const int s = s0 + threadIdx.x;
-            long long w = 0, wx, wall;
-            int units = 0, ux, uall;
-            Line x{};
-            if (threadIdx.x < SCAN && s < a.sq.seqs) {
-                x = line_of<R>(a, s);
-                units = x.blocks * a.c.heads;
-                w = x.tiles * units;
-            }
-            exclusive(w, units, wx, ux, wall, uall);
-            wx += wbase;
-            ux += ubase;
-            if (wx <= g && g < wx + w) s_span[0] = ux + (int)((g - wx) / x.tiles);
-            if (wx < gz && gz <= wx + w) s_span[1] = ux + (int)((gz - 1 - wx) / x.tiles);
+    const int share = blockIdx.x < s_line.ranges && s_line.all > 0 ? s_line.start(blockIdx.x + 1) - s_line.start(blockIdx.x) : 0;
+    // Every role goes over the windows; all meet when one is listed and when it is done.  The roles stand inside the branch that
+    // sets their share of registers.
+    auto windows = [&](auto&& role) {
+        int y0 = 0, k0 = 0;                                   // tiles and pieces of the windows before
+#pragma unroll 1
+        for (int window = 0; y0 < share; window++) {
+            if (window > 0) list_pieces<R>(a, work, s_line, s_piece, window);
+            const int tiles = min(share - y0, WINDOW), pieces = s_line.span[1] - s_line.span[0] + 1;
+            role(tiles, pieces, y0, k0);
             __syncthreads();
-            if (wx < gz && wx + w > g) {
-                const int u0 = s_span[0], first = x.q.len - x.q.n;
-                const long long k1 = min((gz - 1 - wx) / x.tiles, (long long)units - 1);
-                for (long long k = g > wx ? (g - wx) / x.tiles : 0; k <= k1; k++) {
-                    const long long u = wx + k * x.tiles, uz = u + x.tiles, lo = max(u, g), hi = min(uz, gz);
-                    Piece p;
-                    p.s = s;
-                    p.head = (int)(k / x.blocks);
-                    p.n0 = x.q.n0;
-                    p.first = first;
-                    p.lim = min(min(x.q.end, a.max_kv), first + x.n);
-                    p.row0 = (int)(k % x.blocks) * R;
-                    p.rows = min(x.n * a.group - p.row0, R);
-                    p.tok0 = x.base + (int)(lo - u) * KT;
-                    p.x0 = (int)(lo - g);
-                    p.tiles = (int)(hi - lo);
-                    p.slot = 2 * range + (u > g0);
-                    p.flags = (lo > max(u, g0) ? P_PREV : 0) | (hi == uz && u >= g0 ? P_DIRECT : 0);
-                    s_piece[ux + (int)k - u0] = p;
-                    if (g == g0 && u <= g0 && uz > g0) {
-                        // the join of the unit that this range begins within, if the range before is the unit's first
-                        int parts = 0, slot0 = 0;
-                        if (u < g0 && u >= start_of(range - 1)) {
-                            parts = (int)((uz * ranges - 1) / all) - (range - 1) + 1;
-                            slot0 = 2 * (range - 1) + (u > start_of(range - 1));
-                        }
-                        work.joins[2 * range] = make_int4(p.n0, p.row0, p.rows, p.head);
-                        work.joins[2 * range + 1] = make_int4(parts, slot0, 2 * range, 0);
-                    }
-                }
-            }
-            wbase += wall;
-            ubase += uall;
+            y0 += tiles;
+            k0 += pieces;
+            if (*abort_flag) break;                           // (nothing waits here: the same for all)
         }
-        __syncthreads();
-        const int pieces = s_span[1] - s_span[0] + 1;
-
-        if (warp >= W_CONVK && warp < W_MMA) {
+    };
+    if (warp >= C::kWarpK) {
+        if constexpr (R == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
+        windows([&](const int tiles, const int pieces, const int y0, const int k0) {
+        if (warp != C::kWarpMma) {
             // ======================================================= converters
-            // Units of 16 tokens (within one page and scale block); warp w of four takes tokens 32w .. of a tile.  Lane (g, t)
-            // reads rows g, g+8, 16 bytes at 16t of each 64.
-            const bool isv = warp >= W_CONVV;
-            const int w = warp & 3, gr = lane >> 2, t = lane & 3, units = 2 * tiles;
-            const int blocks = a.c.page / a.c.block;
-            const int8_t* codes = (isv ? a.c.v : a.c.k) + gr * D + 16 * t;
-            long long src = -1;                               // lane i: the i-th of the warp's next 32 units (negative: zeros)
-            float ks = 0.f, lv = -INFINITY, iv = 0.f;
-            auto lookup = [&](int v0) {
-                const int v = v0 + lane, x = v >> 1;
-                src = -1, ks = 0.f, lv = -INFINITY, iv = 0.f;
-                if (v >= units) return;
-                int lo = 0, hi = pieces;                      // the piece that tile x lies in
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    if (s_piece[mid].x0 <= x) lo = mid;
-                    else hi = mid;
-                }
-                const Piece& p = s_piece[lo];
-                const int tok = p.tok0 + (x - p.x0) * KT + 32 * w + 16 * (v & 1);
-                if (tok >= p.lim) return;
-                const int page = tok / a.c.page, off = tok - page * a.c.page;
-                const int pg = a.sq.table[p.s * a.sq.stride + page];
-                if ((unsigned)pg < (unsigned long long)a.c.pages) {
-                    const long long ph = (long long)pg * a.c.heads + p.head;
-                    src = (ph * a.c.page + off) * D;
-                    if (!isv) {
-                        const long long sc = ph * blocks + off / a.c.block;
-                        ks = a.c.ks[sc];
-                        const float vs = fmaxf(a.c.vs[sc], SCALE_FLOOR);
-                        lv = __log2f(vs);
-                        iv = __fdividef(1.f, vs);
+            // Units of 32 tokens (two groups of 16, each within one page and scale block) and up to 128 dimensions.  Of K, a warp
+            // takes the quarter of a tile whose lanes of TMEM it can reach; of V, the warps take turns.  Lane (g, t) turns rows
+            // g, g+8 of a group, 16 bytes at 16t of each 64.
+            auto units_of = [&](auto side) {
+                constexpr bool isv = decltype(side)::value;
+                constexpr int TURN = isv ? C::kWarpsV : STRIPS;
+                const int gr = lane >> 2, t = lane & 3, w = isv ? warp - C::kWarpV : warp - C::kWarpK;
+                // the warp's u-th unit: tile, quarter of it, strip of 128 dimensions
+                auto number = [&](int u) { return isv ? w + TURN * u : (u / STRIPS * 4 + w) * STRIPS + u % STRIPS; };
+                const int units = isv ? (4 * STRIPS * tiles - w + TURN - 1) / TURN : STRIPS * tiles;
+                const int8_t* codes = (isv ? a.c.v : a.c.k) + gr * D + 16 * t;
+                // lanes 2i, 2i+1: the groups of the i-th of the warp's next 16 units: place / 16, and the scales.  Where there is
+                // nothing, any codes will do: the score's factor and iv are zero, and so is the probability.
+                int src = 0;
+                float ks = 0.f, lv = -INFINITY, iv = 0.f;
+                auto lookup = [&](int u0) {
+                    const int u = u0 + (lane >> 1), v = number(u), x = v / (4 * STRIPS);
+                    src = 0, ks = 0.f, lv = -INFINITY, iv = 0.f;
+                    if (u >= units) return;
+                    int lo = 0, hi = pieces;                  // the piece that tile x lies in
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) / 2;
+                        if (s_piece[mid].x0 <= x) lo = mid;
+                        else hi = mid;
                     }
-                } else {
-                    flag_error(DEVERR_PAGE);
-                }
-            };
-            uint4 r[C::kAhead][2][CH];
-            auto load = [&](int v, uint4 (&to)[2][CH]) {
-                if (v >= units) return;
-                if ((v & 31) == 0) lookup(v);
-                const long long at = __shfl_sync(0xffffffffu, src, v & 31);
+                    const Piece& p = s_piece[lo];
+                    const int tok = p.tok0 + (x - p.x0) * KT + 32 * (v / STRIPS & 3) + 16 * (lane & 1);
+                    if (tok >= p.lim) return;
+                    const int page = tok / a.c.page, off = tok - page * a.c.page;
+                    const int pg = a.sq.table[p.s * a.sq.stride + page];
+                    if ((unsigned)pg < (unsigned long long)a.c.pages) {
+                        const int ph = pg * a.c.heads + p.head;
+                        src = ph * (a.c.page / 16) + off / 16;
+                        if constexpr (!isv) {
+                            const long long sc = (long long)ph * (a.c.page / a.c.block) + off / a.c.block;
+                            ks = a.c.ks[sc];
+                            const float vs = fmaxf(a.c.vs[sc], SCALE_FLOOR);
+                            lv = __log2f(vs);
+                            iv = __fdividef(1.f, vs);
+                        }
+                    } else {
+                        flag_error(DEVERR_PAGE);
+                    }
+                };
+                const int8_t* from[2];
+                auto point = [&](int u) {                     // at unit u's codes; publishes its scales
+                    const int strip = number(u) % STRIPS;
 #pragma unroll
-                for (int h = 0; h < 2; h++)
+                    for (int g = 0; g < 2; g++)
+                        from[g] = codes + (long long)__shfl_sync(0xffffffffu, src, 2 * (u & 15) + g) * (16 * D) + 128 * strip;
+                    // (the slot's last readers are far behind: K runs at most three tiles ahead of the softmax, its loads one more)
+                    if (!isv && (lane >> 1) == (u & 15) && u < units && strip == 0)
+                        scales[(y0 + u / STRIPS) % C::kScaleSlots * 8 + 2 * w + (lane & 1)] = make_float4(ks, lv, iv, 0.f);
+                };
+                uint4 r[2][2][CU];
+                lookup(0);
+                point(0);
 #pragma unroll
-                    for (int c = 0; c < CH; c++)
-                        to[h][c] = at >= 0 ? ld_cache(codes + at + 8 * h * D + 64 * c) : make_uint4(0, 0, 0, 0);
-                // (the slot's last readers are far behind: K runs at most kKStages + 1 tiles ahead of the softmax, these
-                // loads kAhead / 2 more)
-                if (!isv && lane == (v & 31))
-                    scales[(y0 + (v >> 1)) % C::kScaleSlots * 8 + 2 * w + (v & 1)] = make_float4(ks, lv, iv, 0.f);
-            };
-            static_assert(C::kKStages + 2 + C::kAhead / 2 < C::kScaleSlots, "scale slots");
-            bool ok = true;
+                for (int g = 0; g < 2; g++)
 #pragma unroll
-            for (int i = 0; i < C::kAhead; i++) load(i, r[i]);
-            for (int v0 = 0; ok && v0 < units; v0 += C::kAhead) {
+                    for (int h = 0; h < 2; h++)
 #pragma unroll
-                for (int i = 0; i < C::kAhead; i++) {
-                    const int v = v0 + i, y = y0 + (v >> 1);
-                    if (v >= units || !ok) continue;
-                    if (isv) {
-                        const int st = y % C::kVStages;
-                        ok = mbar_wait(bar.vempty(st), ((y / C::kVStages) & 1) ^ 1, abort_flag);
-                        if (!ok) continue;
-                        const uint32_t to = sb + C::v_off + st * C::kVBytes;
+                        for (int c = 0; c < CU; c++) r[g][h][c] = ld_cache(from[g] + 8 * h * D + 64 * c);
+                bool ok = true;
+#pragma unroll 1
+                for (int u = 0; u < units; u++) {
+                    if (((u + 1) & 15) == 0) lookup(u + 1);
+                    point(u + 1);
+                    const int v = number(u), y = y0 + v / (4 * STRIPS), quarter = v / STRIPS & 3, strip = v % STRIPS;
+                    // the stage is free once the product that read it is complete
+                    if (y >= 2) ok = ok && wait_for(isv ? bar.pvdone(y & 1) : bar.sfull(y & 1), ((y - 2) >> 1) & 1, abort_flag);
+                    if constexpr (isv) {
+                        const uint32_t to = sb + C::v_off + (y & 1) * C::kVBytes + quarter * (32 * 128) + strip * (2 * KT * 128);
 #pragma unroll
-                        for (int h = 0; h < 2; h++)
+                        for (int g = 0; g < 2; g++)
 #pragma unroll
-                            for (int c = 0; c < CH; c++) {
-                                const uint4 x = r[i][h][c];
-                                uint32_t z[8];
-                                codes_even_odd(x.x, z[0], z[1]);
-                                codes_even_odd(x.y, z[2], z[3]);
-                                codes_even_odd(x.z, z[4], z[5]);
-                                codes_even_odd(x.w, z[6], z[7]);
-                                const uint32_t at = to + c * (KT * 128), row = 32 * w + 16 * (v & 1) + 8 * h + gr;
-                                st_shared_v4(at + sw128_off(row, 2 * t), z[0], z[1], z[2], z[3]);
-                                st_shared_v4(at + sw128_off(row, 2 * t + 1), z[4], z[5], z[6], z[7]);
-                            }
+                            for (int h = 0; h < 2; h++)
+#pragma unroll
+                                for (int c = 0; c < CU; c++) {
+                                    const uint4 x = r[g][h][c];
+                                    uint32_t z[8];
+                                    codes_even_odd(x.x, z[0], z[1]);
+                                    codes_even_odd(x.y, z[2], z[3]);
+                                    codes_even_odd(x.z, z[4], z[5]);
+                                    codes_even_odd(x.w, z[6], z[7]);
+                                    r[g][h][c] = ld_cache(from[g] + 8 * h * D + 64 * c);
+                                    const uint32_t place = to + c * (KT * 128) + g * 2048 + h * 1024;
+                                    st_shared_v4(place + sw128_off(gr, 2 * t), z[0], z[1], z[2], z[3]);
+                                    st_shared_v4(place + sw128_off(gr, 2 * t + 1), z[4], z[5], z[6], z[7]);
+                                }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar.vfull(st));
+                        if (lane == 0) mbar_arrive(bar.vfull(y & 1));
                     } else {
-                        const int st = y % C::kKStages;
-                        ok = mbar_wait(bar.kempty(st), ((y / C::kKStages) & 1) ^ 1, abort_flag);
-                        if (!ok) continue;
                         tc_fence_after();
-                        const uint32_t to = tmem + ((uint32_t)(32 * w + 16 * (v & 1)) << 16) + C::kKCol + st * C::kKCols;
+                        const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + C::kKCol + (y & 1) * C::kKCols + 64 * strip;
 #pragma unroll
-                        for (int c = 0; c < CH; c++) {
-                            uint32_t z[16];
+                        for (int g = 0; g < 2; g++)
 #pragma unroll
-                            for (int h = 0; h < 2; h++) {
-                                const uint4 x = r[i][h][c];
-                                codes_even_odd(x.x, z[2 * h], z[2 * h + 1]);
-                                codes_even_odd(x.y, z[4 + 2 * h], z[4 + 2 * h + 1]);
-                                codes_even_odd(x.z, z[8 + 2 * h], z[8 + 2 * h + 1]);
-                                codes_even_odd(x.w, z[12 + 2 * h], z[12 + 2 * h + 1]);
+                            for (int c = 0; c < CU; c++) {
+                                uint32_t z[16];
+#pragma unroll
+                                for (int h = 0; h < 2; h++) {
+                                    const uint4 x = r[g][h][c];
+                                    codes_even_odd(x.x, z[2 * h], z[2 * h + 1]);
+                                    codes_even_odd(x.y, z[4 + 2 * h], z[4 + 2 * h + 1]);
+                                    codes_even_odd(x.z, z[8 + 2 * h], z[8 + 2 * h + 1]);
+                                    codes_even_odd(x.w, z[12 + 2 * h], z[12 + 2 * h + 1]);
+                                    r[g][h][c] = ld_cache(from[g] + 8 * h * D + 64 * c);
+                                }
+                                tmem_st_16x256b_x4(to + ((uint32_t)(16 * g) << 16) + 32 * c, z);
                             }
-                            tmem_st_16x256b_x4(to + 32 * c, z);
-                        }
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(bar.kfull(st));
-                            mbar_arrive(bar.scale(y % C::kScaleSlots));
+                            mbar_arrive(bar.kfull(y & 1));
+                            if (strip == 0) mbar_arrive(bar.scale(y % C::kScaleSlots));
                         }
                     }
-                    load(v + C::kAhead, r[i]);
                 }
-            }
-        } else if (warp == W_MMA) {
+            };
+            if (warp >= C::kWarpV) units_of(std::true_type());
+            else units_of(std::false_type());
+        } else {
             // ======================================================= products
             constexpr uint32_t idesc_s = idesc_f16_f32(128, R);
             constexpr uint32_t idesc_o = idesc_f16_f32(128, R) | (1u << 15) | (1u << 16);     // M and N along the rows
             const uint32_t q_lo = desc_lo(sb + C::q_off, 16), v_lo = desc_lo(sb + C::v_off, KT * 128);
             const uint32_t p_lo = desc_lo(sb + C::p_off, KT * 128);
             bool ok = true;
-            int ks = 0, kx = s_piece[0].x0;                   // the piece whose S comes next, and its first tile
+            int ks = 0, kx = 0;                               // the piece whose S comes next, and its first tile
             auto product_s = [&](int x) {
-                const int y = y0 + x, st = y % C::kKStages;
+                const int y = y0 + x;
                 if (x == kx) {
-                    ok = ok && mbar_wait(bar.qfull(), (k0 + ks) & 1, abort_flag);
+                    ok = ok && wait_for(bar.qfull(), (k0 + ks) & 1, abort_flag);
                     ks++;
                     kx = ks < pieces ? s_piece[ks].x0 : tiles;
                 }
-                ok = ok && mbar_wait(bar.kfull(st), (y / C::kKStages) & 1, abort_flag);
+                ok = ok && wait_for(bar.kfull(y & 1), (y >> 1) & 1, abort_flag);
                 if (!ok) return;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; k++)
-                        umma_ts(tmem + (y & 1) * R, tmem + C::kKCol + st * C::kKCols + 8 * k,
+                        umma_ts(tmem + (y & 1) * R, tmem + C::kKCol + (y & 1) * C::kKCols + 8 * k,
                                 q_lo + (k / 4) * (R * 128 >> 4) + 2 * (k % 4), idesc_s, k > 0);
                     umma_commit(bar.sfull(y & 1));
-                    umma_commit(bar.kempty(st));
                 }
                 __syncwarp();
             };
             product_s(0);
-            int ko = 0;                                       // the piece whose O is summed
+            int ko = 0, xo = 0;                               // the piece whose O is summed next, and its first tile
             for (int x = 0; ok && x < tiles; x++) {
-                const int y = y0 + x, st = y % C::kVStages;
-                while (x >= s_piece[ko].x0 + s_piece[ko].tiles) ko++;
-                const bool fresh = x == s_piece[ko].x0, more = x + 1 < tiles, ahead = more && x + 1 != kx;
+                const int y = y0 + x;
+                const bool fresh = x == xo, ahead = x + 1 < tiles && x + 1 != kx;
                 if (ahead) product_s(x + 1);
-                ok = ok && mbar_wait(bar.vfull(st), (y / C::kVStages) & 1, abort_flag);
-                if (fresh && k0 + ko > 0) ok = ok && mbar_wait(bar.ofree(), (k0 + ko - 1) & 1, abort_flag);
-                ok = ok && mbar_wait(bar.pready(y & 1), (y >> 1) & 1, abort_flag);
+                if (fresh) {
+                    if (k0 + ko > 0) ok = ok && wait_for(bar.ofree(), (k0 + ko - 1) & 1, abort_flag);
+                    ko++;
+                    xo = ko < pieces ? s_piece[ko].x0 : tiles;
+                }
+                ok = ok && wait_for(bar.vfull(y & 1), (y >> 1) & 1, abort_flag);
+                ok = ok && wait_for(bar.pready(y & 1), (y >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t p = p_lo + (y % C::kPBufs) * (C::kPBytes >> 4), v = v_lo + st * (C::kVBytes >> 4);
+                    const uint32_t p = p_lo + (y & 1) * (C::kPBytes >> 4), v = v_lo + (y & 1) * (C::kVBytes >> 4);
 #pragma unroll
                     for (int h = 0; h < C::kHalves; h++)
 #pragma unroll
                         for (int k = 0; k < KT / 16; k++)
-                            umma_ss(tmem + C::kOCol + h * R, v + h * (2 * KT * 128 >> 4) + k * (2048 >> 4),
-                                    p + k * (2048 >> 4), idesc_o, !fresh || k > 0);
+                            umma_ss(tmem + C::kOCol + h * R, v + h * (2 * KT * 128 >> 4) + k * (2048 >> 4), p + k * (2048 >> 4),
+                                    idesc_o, !fresh || k > 0);
                     umma_commit(bar.pvdone(y & 1));
-                    umma_commit(bar.vempty(st));
                 }
                 __syncwarp();
-                if (more && !ahead) product_s(x + 1);
+                if (!ahead && x + 1 < tiles) product_s(x + 1);
             }
-        } else {
+        }
+        });
+        if (warp == C::kWarpMma) {
+            if (elect_one()) umma_commit(bar.done());
+            __syncwarp();
+            mbar_wait_final(bar.done(), 0);
+            __syncwarp();
+        }
+    } else {
+        if constexpr (R == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+        windows([&](const int, const int pieces, const int y0, const int) {
             // ======================================================= softmax: one thread a token
             // A failed wait does not leave the loops (the group meets at barriers); later waits then return at once.
-            const int grp = warp >> 2, w = warp & 3, tk = 32 * w + lane, gt = threadIdx.x & 127, c0 = grp * (R / 2);
+            const int grp = warp >> 2, w = warp & 3, tk = 32 * w + lane, gt = threadIdx.x & 127, c0 = grp * N;
             const int id = 1 + grp;
             constexpr int LPR = D / 8, RPP = 4 * 32 / LPR;    // lanes on a row of queries, rows at a time
             const uint32_t lanes = (uint32_t)(32 * w) << 16;
@@ -550,7 +620,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
             auto fetch_q = [&](const Piece& p) {
                 if (p.rows <= c0) return;
 #pragma unroll
-                for (int i = 0; i < R / 2; i += RPP) {
+                for (int i = 0; i < N; i += RPP) {
                     const int c = c0 + i + (w * 32 + lane) / LPR, row = p.row0 + min(c, p.rows - 1), m = lane % LPR;
                     const uint16_t* from = static_cast<const uint16_t*>(a.q.data) + (long long)(p.n0 + row / a.group) * a.q.ts +
                                            (long long)(p.head * a.group + row % a.group) * a.q.hs + 8 * m;
@@ -564,7 +634,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
                 if (p.rows > c0) {
                     cp_async_wait<0>();
 #pragma unroll 2
-                    for (int i = 0; i < R / 2; i += RPP) {
+                    for (int i = 0; i < N; i += RPP) {
                         const int c = c0 + i + (w * 32 + lane) / LPR, m = lane % LPR;
                         const uint32_t panel = sb + C::q_off + (m / 8) * (R * 128);
                         float x[8], top = 0.f, up, down;
@@ -597,7 +667,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
                 const Piece p = s_piece[k];
                 const bool busy = p.rows > c0, more = k + 1 < pieces;
                 named_bar_sync(id, 128);                      // s_next is there, the last piece's values are read
-                if (gt < R / 2) {
+                if (gt < N) {
                     const int c = c0 + gt, row = p.row0 + min(c, p.rows - 1), tok = p.n0 + row / a.group;
                     const bool real = c < p.rows;
                     float* col = reinterpret_cast<float*>(&s_col[c / 2]) + (c & 1);
@@ -609,132 +679,115 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
                     s_out[c] = (long long)tok * a.out.ts + (p.head * a.group + row % a.group) * a.out.hs;
                 }
                 named_bar_sync(id, 128);
-                uint64_t l2[NC][16];
+                uint64_t l2[N / 2];
 #pragma unroll
-                for (int h = 0; h < NC; h++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) l2[h][i] = 0ull;
+                for (int i = 0; i < N / 2; i++) l2[i] = 0ull;
                 for (int x = p.x0; x < p.x0 + p.tiles; x++) {
                     const int y = y0 + x, tok = p.tok0 + (x - p.x0) * KT, j = tok + tk;
                     // which rows see the token: all, but for the new tokens and the window's edge
                     const bool masked = tok + KT > p.first || (a.window > 0 && tok <= p.first + a.max_tokens - a.window);
-                    uint32_t see[NC];
-#pragma unroll
-                    for (int h = 0; h < NC; h++) see[h] = 0xFFFFFFFFu;
+                    uint32_t see = 0xFFFFFFFFu;
                     if (masked && busy) {
                         const int d = j - p.first;
-#pragma unroll
-                        for (int h = 0; h < NC; h++) {
-                            if (j >= p.lim) {
-                                see[h] = 0u;
-                            } else if (d >= 0) {
-                                uint32_t bits = 0u;
-                                if (d / 32 < a.words)
+                        if (j >= p.lim) {
+                            see = 0u;
+                        } else if (d >= 0) {
+                            see = 0u;
+                            if (d / 32 < a.words)
 #pragma unroll 8
-                                    for (int i = 0; i < 32; i++)
-                                        bits |= (a.masks[(long long)s_tok[c0 + 32 * h + i] * a.words + d / 32] >> (d % 32) & 1u)
-                                                << i;
-                                see[h] = bits;
-                            } else if (a.window > 0) {
+                                for (int i = 0; i < N; i++)
+                                    see |= (a.masks[(long long)s_tok[c0 + i] * a.words + d / 32] >> (d % 32) & 1u) << i;
+                        } else if (a.window > 0) {
 #pragma unroll 8
-                                for (int i = 0; i < 32; i++)
-                                    if (j < s_low[c0 + 32 * h + i]) see[h] &= ~(1u << i);
-                            }
+                            for (int i = 0; i < N; i++)
+                                if (j < s_low[c0 + i]) see &= ~(1u << i);
                         }
                     }
-                    ok = mbar_wait(bar.scale(y % C::kScaleSlots), (y / C::kScaleSlots) & 1, abort_flag) && ok;
-                    ok = mbar_wait(bar.sfull(y & 1), (y >> 1) & 1, abort_flag) && ok;
+                    ok = wait_for(bar.scale(y % C::kScaleSlots), (y / C::kScaleSlots) & 1, abort_flag) && ok;
+                    ok = wait_for(bar.sfull(y & 1), (y >> 1) & 1, abort_flag) && ok;
                     tc_fence_after();
                     if (more && x + 1 == p.x0 + p.tiles) fetch_q(s_piece[k + 1]);             // every S of the piece is complete
                     if (busy) {
                         const float4 sc = scales[y % C::kScaleSlots * 8 + tk / 16];
                         const uint64_t ks2 = f2_pack(sc.x, sc.x), lv2 = f2_pack(sc.y, sc.y), iv2 = f2_pack(sc.z, sc.z);
+                        uint32_t xr[N];
+                        float e[N];
+                        auto terms = [&](auto shifted) {      // e = t - m, or t
+                            tmem_load(tmem + lanes + (y & 1) * R + c0, xr);
+                            tmem_wait(xr);
 #pragma unroll
-                        for (int h = 0; h < NC; h++) {
-                            const int cb = c0 + 32 * h;
-                            uint32_t xr[32];
-                            float e[32];
-                            auto terms = [&](bool shifted) {  // e = t - m, or t
-                                tmem_ld32(tmem + lanes + (y & 1) * R + cb, xr);
-                                tmem_wait32(xr);
-#pragma unroll
-                                for (int i = 0; i < 16; i++) {
-                                    const float4 f = s_col[cb / 2 + i];
-                                    const uint64_t sh = shifted ? f2_add(f2_pack(f.z, f.w), lv2) : lv2;
-                                    const uint64_t s2 = f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1]));
-                                    f2_unpack(f2_fma(s2, f2_mul(f2_pack(f.x, f.y), ks2), sh), e[2 * i], e[2 * i + 1]);
-                                }
-                                if (masked)
-#pragma unroll
-                                    for (int i = 0; i < 32; i++)
-                                        if (!(see[h] >> i & 1u)) e[i] = -INFINITY;
-                            };
-                            terms(true);
-                            float top = e[31];
-#pragma unroll
-                            for (int i = 0; i < 30; i += 2) top = max3(top, e[i], e[i + 1]);
-                            top = fmaxf(top, e[30]);
-                            if (group_any(id, top > LAZY)) {
-                                terms(false);
-                                const float mine = across<true>(e);
-                                s_red[grp][w][32 * h + lane] = mine;
-                                named_bar_sync(id, 128);
-                                if (gt < 32) {
-                                    const int c = cb + gt;
-                                    const float(&red)[4][R / 2] = s_red[grp];
-                                    const int at = 32 * h + gt;
-                                    const float most = fmaxf(fmaxf(red[0][at], red[1][at]), fmaxf(red[2][at], red[3][at]));
-                                    const float m = s_m[c], mn = fmaxf(m, most - HEAD);
-                                    s_fac[c] = m == -INFINITY ? 1.f : ex2(m - mn);
-                                    if (c < p.rows && mn > -INFINITY) {
-                                        s_m[c] = mn;
-                                        reinterpret_cast<float*>(&s_col[c / 2])[2 + (c & 1)] = -mn;
-                                    }
-                                }
-                                named_bar_sync(id, 128);
-                                uint64_t fac[16];
-#pragma unroll
-                                for (int i = 0; i < 16; i++) {
-                                    fac[i] = f2_pack(s_fac[cb + 2 * i], s_fac[cb + 2 * i + 1]);
-                                    l2[h][i] = f2_mul(l2[h][i], fac[i]);
-                                }
-                                if (x > p.x0) {
-                                    ok = mbar_wait(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
-                                    tc_fence_after();
-#pragma unroll
-                                    for (int o = 0; o < C::kHalves; o++) {
-                                        const uint32_t at = tmem + lanes + C::kOCol + o * R + cb;
-                                        tmem_ld32(at, xr);
-                                        tmem_wait32(xr);
-#pragma unroll
-                                        for (int i = 0; i < 16; i++) {
-                                            float z0, z1;
-                                            f2_unpack(f2_mul(f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])),
-                                                             fac[i]), z0, z1);
-                                            xr[2 * i] = __float_as_uint(z0);
-                                            xr[2 * i + 1] = __float_as_uint(z1);
-                                        }
-                                        tmem_st32(at, xr);
-                                    }
-                                    tmem_st_wait();
-                                }
-                                terms(true);
+                            for (int i = 0; i < N / 2; i++) {
+                                const float4 f = s_col[c0 / 2 + i];
+                                const uint64_t sh = decltype(shifted)::value ? f2_add(f2_pack(f.z, f.w), lv2) : lv2;
+                                const uint64_t s2 = f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1]));
+                                f2_unpack(f2_fma(s2, f2_mul(f2_pack(f.x, f.y), ks2), sh), e[2 * i], e[2 * i + 1]);
                             }
-                            // P's buffer is free once the product that read it is complete
-                            if (h == 0 && y >= C::kPBufs)
-                                ok = mbar_wait(bar.pvdone((y - C::kPBufs) & 1), ((y - C::kPBufs) >> 1) & 1, abort_flag) && ok;
-                            const uint32_t row = sb + C::p_off + (y % C::kPBufs) * C::kPBytes + (cb / 64) * (KT * 128);
+                            if (masked)
 #pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                uint32_t z[4];
+                                for (int i = 0; i < N; i++)
+                                    if (!(see >> i & 1u)) e[i] = -INFINITY;
+                        };
+#pragma unroll 1
+                        for (int raised = 0;; raised++) {
+                            terms(std::true_type());
+                            float tops[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
-                                for (int u = 0; u < 4; u++) {
-                                    const float p0 = ex2(e[8 * i + 2 * u]), p1 = ex2(e[8 * i + 2 * u + 1]);
-                                    l2[h][4 * i + u] = f2_fma(f2_pack(p0, p1), iv2, l2[h][4 * i + u]);
-                                    z[u] = pack2(p0, p1, __half());
+                            for (int i = 4; i < N; i++) tops[i & 3] = fmaxf(tops[i & 3], e[i]);
+                            const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+                            if (__builtin_expect(!group_any(id, top > LAZY) || raised, 1)) break;
+                            // a term passes its row's reference by 2^LAZY: raise the references (once: then none does)
+                            terms(std::false_type());
+                            s_red[grp][w][lane % N] = across<true, N>(e);
+                            named_bar_sync(id, 128);
+                            if (gt < N) {
+                                const int c = c0 + gt;
+                                const float(&red)[4][N] = s_red[grp];
+                                const float most = fmaxf(fmaxf(red[0][gt], red[1][gt]), fmaxf(red[2][gt], red[3][gt]));
+                                const float m = s_m[c], mn = fmaxf(m, most - HEAD);
+                                s_fac[c] = m == -INFINITY ? 1.f : ex2(m - mn);
+                                if (c < p.rows && mn > -INFINITY) {
+                                    s_m[c] = mn;
+                                    reinterpret_cast<float*>(&s_col[c / 2])[2 + (c & 1)] = -mn;
                                 }
-                                st_shared_v4(row + sw128_off(tk, cb % 64 / 8 + i), z[0], z[1], z[2], z[3]);
                             }
+                            named_bar_sync(id, 128);
+                            const auto fac = [&](int i) { return f2_pack(s_fac[c0 + 2 * i], s_fac[c0 + 2 * i + 1]); };
+#pragma unroll
+                            for (int i = 0; i < N / 2; i++) l2[i] = f2_mul(l2[i], fac(i));
+                            if (x > p.x0) {
+                                ok = wait_for(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
+                                tc_fence_after();
+#pragma unroll
+                                for (int o = 0; o < C::kHalves; o++) {
+                                    const uint32_t at = tmem + lanes + C::kOCol + o * R + c0;
+                                    tmem_load(at, xr);
+                                    tmem_wait(xr);
+#pragma unroll
+                                    for (int i = 0; i < N / 2; i++) {
+                                        float z0, z1;
+                                        f2_unpack(f2_mul(f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])), fac(i)),
+                                                  z0, z1);
+                                        xr[2 * i] = __float_as_uint(z0);
+                                        xr[2 * i + 1] = __float_as_uint(z1);
+                                    }
+                                    tmem_store(at, xr);
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                        // P's buffer is free once the product that read it is complete
+                        if (y >= 2) ok = wait_for(bar.pvdone(y & 1), ((y - 2) >> 1) & 1, abort_flag) && ok;
+                        const uint32_t row = sb + C::p_off + (y & 1) * C::kPBytes + (c0 / 64) * (KT * 128);
+#pragma unroll
+                        for (int i = 0; i < N / 8; i++) {
+                            uint32_t z[4];
+#pragma unroll
+                            for (int u = 0; u < 4; u++) {
+                                const float p0 = ex2(e[8 * i + 2 * u]), p1 = ex2(e[8 * i + 2 * u + 1]);
+                                l2[4 * i + u] = f2_fma(f2_pack(p0, p1), iv2, l2[4 * i + u]);
+                                z[u] = pack2(p0, p1, __half());
+                            }
+                            st_shared_v4(row + sw128_off(tk, c0 % 64 / 8 + i), z[0], z[1], z[2], z[3]);
                         }
                         fence_proxy_async_smem();
                     }
@@ -745,20 +798,19 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
                 if (more) convert_q(s_piece[k + 1]);
                 // ---- the piece's result
                 const int yz = y0 + p.x0 + p.tiles - 1;
-                ok = mbar_wait(bar.pvdone(yz & 1), (yz >> 1) & 1, abort_flag) && ok;
+                ok = wait_for(bar.pvdone(yz & 1), (yz >> 1) & 1, abort_flag) && ok;
                 tc_fence_after();
                 if (busy) {
+                    {
+                        float e[N];
 #pragma unroll
-                    for (int h = 0; h < NC; h++) {
-                        float e[32];
-#pragma unroll
-                        for (int i = 0; i < 16; i++) f2_unpack(l2[h][i], e[2 * i], e[2 * i + 1]);
-                        s_red[grp][w][32 * h + lane] = across<false>(e);
+                        for (int i = 0; i < N / 2; i++) f2_unpack(l2[i], e[2 * i], e[2 * i + 1]);
+                        s_red[grp][w][lane % N] = across<false, N>(e);
                     }
                     named_bar_sync(id, 128);
-                    if (gt < R / 2 && c0 + gt < p.rows) {
+                    if (gt < N && c0 + gt < p.rows) {
                         const int c = c0 + gt;
-                        const float(&red)[4][R / 2] = s_red[grp];
+                        const float(&red)[4][N] = s_red[grp];
                         float l = red[0][gt] + red[1][gt] + (red[2][gt] + red[3][gt]), m = s_m[c], keep = 1.f, add = 0.f;
                         float2* ml = work.part_ml + (long long)p.slot * R + c;
                         if (p.flags & P_PREV) {
@@ -787,21 +839,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
                     if (ok && (D != 64 || w < 2)) {
                         const int dim = 32 * w + ((lane & ~3) | (lane & 1) << 1 | (lane >> 1 & 1));       // order 0 2 1 3 undone
 #pragma unroll 1
-                        for (int b = 0; b < NC * C::kHalves; b++) {
-                            const int o = b / NC, cb = c0 + 32 * (b % NC), d = 128 * o + dim;
-                            if (cb >= p.rows) continue;
-                            uint32_t xr[32];
-                            tmem_ld32(tmem + lanes + C::kOCol + o * R + cb, xr);
-                            tmem_wait32(xr);
-                            float* part = work.part_o + ((long long)p.slot * R + cb) * D + d;
+                        for (int o = 0; o < C::kHalves; o++) {
+                            const int d = 128 * o + dim;
+                            uint32_t xr[N];
+                            tmem_load(tmem + lanes + C::kOCol + o * R + c0, xr);
+                            tmem_wait(xr);
+                            float* part = work.part_o + ((long long)p.slot * R + c0) * D + d;
 #pragma unroll
-                            for (int i = 0; i < 32; i++) {
-                                if (cb + i >= p.rows) break;
-                                const float keep = s_fac[cb + i];
+                            for (int i = 0; i < N; i++) {
+                                if (c0 + i >= p.rows) break;
+                                const float keep = s_fac[c0 + i];
                                 float v = keep == 0.f ? 0.f : __uint_as_float(xr[i]) * keep;
-                                if (p.flags & P_PREV) v = fmaf(part[i * D], s_add[cb + i], v);
+                                if (p.flags & P_PREV) v = fmaf(part[i * D], s_add[c0 + i], v);
                                 if (p.flags & P_DIRECT) {
-                                    const long long at = s_out[cb + i] + d;
+                                    const long long at = s_out[c0 + i] + d;
                                     if (ot == MMQ_F32) static_cast<float*>(a.out.data)[at] = v;
                                     else if (ot == MMQ_BF16) static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16(v);
                                     else static_cast<__half*>(a.out.data)[at] = __float2half(v);
@@ -816,23 +867,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) tree_kernel(const TreeArgs a,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.ofree());
             }
-        }
-        __syncthreads();                                      // every role is done with the window
-        y0 += tiles;
-        k0 += pieces;
-        if (*abort_flag) break;                               // (nothing waits here: the same for all)
-    }
-    if (warp == W_MMA) {
-        if (elect_one()) umma_commit(bar.done());
-        __syncwarp();
-        mbar_wait_final(bar.done(), 0);
-        __syncwarp();
+        });
     }
     // ---- teardown
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == W_MMA) tmem_dealloc(tmem, 512);
+    if (warp == C::kWarpMma) tmem_dealloc(tmem, 512);
 }
 
 // The parts of a unit that several ranges hold, on a common reference and in their order.  A block looks after rows of the
@@ -905,7 +946,7 @@ cudaError_t launch_tree(mmq_dtype qt, mmq_dtype ot, const TreeArgs& a, const Tre
         if (e != cudaSuccess) return e;
         done = true;
     }
-    cudaError_t e = launch_pdl_smem(kern, dim3((unsigned)p.ranges), dim3(TREE_THREADS), Tree<D, R>::alloc, s, a, work, (int)qt,
+    cudaError_t e = launch_pdl_smem(kern, dim3((unsigned)p.ranges), dim3(Tree<D, R>::kThreads), Tree<D, R>::alloc, s, a, work, (int)qt,
                                     (int)ot);
     if (e != cudaSuccess || p.ranges == 1) return e;
     if (p.many_parts)
