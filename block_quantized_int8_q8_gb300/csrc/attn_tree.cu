@@ -8,16 +8,16 @@
 // cache tokens and head dimensions on the 128 lanes and the query rows along the columns:
 //   S^T [128 tokens x R] = K Q^T       K: fp16 codes in TMEM (A operand), Q: shared memory, K-major
 //   O^T [128 dims x R]  += V^T P^T     V: shared memory [token][64 dims of 128 bytes], M-major, P the same way, N-major
-// A thread of the softmax then owns a token, with its scales in registers, and a quarter of the rows; what it costs goes with
+// A thread of the softmax then owns a token, with its scales in registers, and half of the rows; what it costs goes with
 // the rows that there are.  K never passes through shared memory, whose bandwidth is the next bound after the cache's.
 //
 // One thread block an SM.  The cache tiles of all (sequence, head, row block) units stand in one line, and each block takes an
 // equal share of it, wherever that begins and ends (lengths are on the device: the blocks work out the line by themselves);
 // units that are cut leave parts in the workspace, which a second launch joins.  Roles:
-//   * sixteen softmax warps in four groups, each a quarter of the rows: a tile's S^T, the mask, the exponentials, P as fp16 to
+//   * eight softmax warps in two groups, each half of the rows: a tile's S^T, the mask, the exponentials, P as fp16 to
 //     shared memory.  The reference m of a row is raised only when a term passes it by 2^LAZY, which a group votes on; then
 //     O is rescaled.  They also bring the queries in and the results out.
-//   * four warps turn the codes of K into fp16 in TMEM and seven (128 rows: three) those of V into shared memory, 32 tokens at
+//   * four warps turn the codes of K into fp16 in TMEM and seven those of V into shared memory, 32 tokens at
 //     a time; the next codes are on their way to the registers that the last ones leave.
 //   * one warp issues the products.
 #include <algorithm>
@@ -31,33 +31,36 @@ namespace mmq {
 namespace {
 
 constexpr int KT = 128;                      // cache tokens of a tile
-constexpr int GROUPS = 4, SOFTMAX_WARPS = 4 * GROUPS;                            // of the softmax: a quarter of the rows each
+constexpr int N = 32;                        // columns of a softmax group
 constexpr int WINDOW = kChain / KT;          // most tiles that are listed, and summed, in one go
 constexpr float UNSET = 1e30f;               // -m of a row that has seen nothing yet
 
 template <int D, int R> struct Tree {
     // warps of the converters and the products, after those of the softmax
-    static constexpr int kWarpsV = R == 128 ? 3 : 7;
-    static constexpr int kWarpK = SOFTMAX_WARPS, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kWarpsV, kWarps = kWarpMma + 1;
+    static constexpr int kGroups = R / N, kSoftmaxWarps = 4 * kGroups, kWarpsV = R == 128 ? 3 : 7;
+    static constexpr int kWarpK = kSoftmaxWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kWarpsV, kWarps = kWarpMma + 1;
     static constexpr int kThreads = kWarps * 32;
-    // registers a thread: 72 at launch of 28 warps; of 24 warps 80, moved to the softmax warps for the longer rows
+    // registers a thread: 96 at launch of 20 warps; of 24 warps 80, some of which move to the softmax warps
     static constexpr int kRegsSoftmax = 88, kRegsRest = 64;
-    static_assert(R == 64 || SOFTMAX_WARPS * kRegsSoftmax + 8 * kRegsRest <= 24 * 80, "register budget");
+    static_assert(R == 64 || kSoftmaxWarps * kRegsSoftmax + 8 * kRegsRest <= 24 * 80, "register budget");
     static constexpr int kHalves = D == 256 ? 2 : 1;                             // O^T of 128 dimensions
     static constexpr int kStrips = D == 256 ? 2 : 1, kChunks = D == 64 ? 1 : 2;   // of up to 128 dimensions, of 64 each
     static constexpr int kVBytes = KT * D * 2, kQBytes = R * D * 2, kPBytes = KT * R * 2;
-    static constexpr int kScaleSlots = 8;
+    static constexpr int kScaleSlots = 16;
     static constexpr int kKCols = D / 2;
-    // TMEM columns: two buffers of S, O, two of K
+    // Tiles of K and V that the converters may be ahead: with two of each every wait of one role stops the others.
+    static constexpr int kKStages = D == 64 ? 4 : (R == 64 && D == 128 ? 4 : 2);
+    static constexpr int kVStages = D == 64 ? 4 : (D == 128 ? (R == 64 ? 4 : 3) : 2);
+    // TMEM columns: two buffers of S, O, K
     static constexpr int kOCol = 2 * R, kKCol = kOCol + kHalves * R;
-    static_assert(kKCol + 2 * kKCols <= 512, "TMEM budget");
+    static_assert(kKCol + kKStages * kKCols <= 512, "TMEM budget");
     // V first: for head_dim 64 the products read the next 16 KB as 64 more dimensions, whose results nothing looks at
     static constexpr int v_off = 0;
-    static constexpr int q_off = v_off + 2 * kVBytes;
+    static constexpr int q_off = v_off + kVStages * kVBytes;
     static constexpr int p_off = q_off + kQBytes;
     static constexpr int sc_off = p_off + 2 * kPBytes;                           // float4 [slots][8]
     static constexpr int bar_off = sc_off + kScaleSlots * 8 * 16;
-    static constexpr int n_bars = kScaleSlots + 13;
+    static constexpr int n_bars = 9 + 2 * (kKStages + kVStages);
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int total = misc_off + 16, alloc = total + 1024;
     static_assert(alloc <= 232448 - (R == 64 ? 16 : 20) * 1024, "shared memory budget (the rest is static)");
@@ -82,8 +85,7 @@ struct TreeWork {                // the workspace
     int4* joins;                 // [ranges][2]
 };
 
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) { tmem_ld_wait(r); }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
@@ -92,17 +94,7 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -167,12 +159,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// N values of each lane (16 or 32), joined over the warp: lanes c mod N get the result of the c-th.
-template <bool MAX, int N>
-__device__ __forceinline__ float across(float (&x)[N]) {
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
+// 32 values of each lane, joined over the warp: lane c gets the result of the c-th.
+template <bool MAX>
+__device__ __forceinline__ float across(float (&x)[32]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) {
+    for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
         for (int i = 0; i < o; i++) {
             const bool up = lane & o;
@@ -181,27 +175,25 @@ __device__ __forceinline__ float across(float (&x)[N]) {
             x[i] = MAX ? fmaxf(keep, got) : keep + got;
         }
     }
-    if (N == 16) {
-        const float got = __shfl_xor_sync(0xffffffffu, x[0], 16);
-        x[0] = MAX ? fmaxf(x[0], got) : x[0] + got;
-    }
     return x[0];
 }
 
 template <int D, int R> struct TreeBars {
     using C = Tree<D, R>;
     uint32_t b;
-    __device__ uint32_t scale(int i) const { return b + 8u * i; }                // a tile's scales are published
-    __device__ uint32_t rest(int i) const { return b + 8u * (C::kScaleSlots + i); }
-    // of tiles i mod 2; S and the product with V release the stages that they read
-    __device__ uint32_t kfull(int i) const { return rest(i); }
-    __device__ uint32_t vfull(int i) const { return rest(2 + i); }
-    __device__ uint32_t sfull(int i) const { return rest(4 + i); }
-    __device__ uint32_t pready(int i) const { return rest(6 + i); }
-    __device__ uint32_t pvdone(int i) const { return rest(8 + i); }
-    __device__ uint32_t qfull() const { return rest(10); }                       // a piece's queries
-    __device__ uint32_t ofree() const { return rest(11); }                       // a piece's O is read
-    __device__ uint32_t done() const { return rest(12); }
+    __device__ uint32_t rest(int i) const { return b + 8u * i; }
+    // Of tiles i mod 2.  As products complete in their order, S of a tile shows that the product with V two tiles before is
+    // complete.
+    __device__ uint32_t sfull(int i) const { return rest(i); }
+    __device__ uint32_t pready(int i) const { return rest(2 + i); }
+    __device__ uint32_t pvdone(int i) const { return rest(4 + i); }
+    __device__ uint32_t qfull() const { return rest(6); }                        // a piece's queries
+    __device__ uint32_t ofree() const { return rest(7); }                        // a piece's O is read
+    __device__ uint32_t done() const { return rest(8); }
+    __device__ uint32_t kfull(int i) const { return rest(9 + i); }
+    __device__ uint32_t kempty(int i) const { return rest(9 + C::kKStages + i); }
+    __device__ uint32_t vfull(int i) const { return rest(9 + 2 * C::kKStages + i); }
+    __device__ uint32_t vempty(int i) const { return rest(9 + 2 * C::kKStages + C::kVStages + i); }
 };
 
 // A sequence's place in the line of tiles.
@@ -356,8 +348,7 @@ template <int D, int R>
 __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
     tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeWork work, int qt, int ot) {
     using C = Tree<D, R>;
-    constexpr int N = R / GROUPS;                             // columns of a group
-    constexpr int STRIPS = C::kStrips, CU = C::kChunks;
+    constexpr int STRIPS = C::kStrips, CU = C::kChunks, AHEAD = 3;
     pdl_wait();
     pdl_trigger();                                            // after the wait: the join reads its inputs before its own
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -366,8 +357,9 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
     __shared__ LineShare s_line;
     __shared__ long long s_out[R];
     __shared__ int s_tok[R], s_low[R];
-    __shared__ float4 s_col[R / 2];                           // of two rows: factors of S, and -m
-    __shared__ float s_m[R], s_fac[R], s_add[R], s_next[R], s_red[GROUPS][4][N];
+    __shared__ __align__(16) float s_neg[R], s_next[R];       // -m; largest magnitude of a query
+    __shared__ float s_even[R];                               // what a row's S is to be multiplied by before the rest
+    __shared__ float s_m[R], s_fac[R], s_add[R], s_red[C::kGroups][4][N];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sb = smem_u32(smem);
     const TreeBars<D, R> bar{sb + C::bar_off};
@@ -376,16 +368,21 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
     float4* scales = reinterpret_cast<float4*>(smem + C::sc_off);
     if (warp == C::kWarpMma) {
         if (lane == 0) {
-            for (int i = 0; i < C::kScaleSlots; i++) mbar_init(bar.scale(i), 4);
-            for (int i = 0; i < 2; i++) {
+            for (int i = 0; i < C::kKStages; i++) {
                 mbar_init(bar.kfull(i), 4 * STRIPS);
+                mbar_init(bar.kempty(i), 1);
+            }
+            for (int i = 0; i < C::kVStages; i++) {
                 mbar_init(bar.vfull(i), 4 * STRIPS);
-                mbar_init(bar.sfull(i), 1);
-                mbar_init(bar.pready(i), SOFTMAX_WARPS);
+                mbar_init(bar.vempty(i), 1);
+            }
+            for (int i = 0; i < 2; i++) {
+                mbar_init(bar.sfull(i), 2);                   // the product, and the thread that saw K and its scales
+                mbar_init(bar.pready(i), C::kSoftmaxWarps);
                 mbar_init(bar.pvdone(i), 1);
             }
-            mbar_init(bar.qfull(), SOFTMAX_WARPS);
-            mbar_init(bar.ofree(), SOFTMAX_WARPS);
+            mbar_init(bar.qfull(), C::kSoftmaxWarps);
+            mbar_init(bar.ofree(), C::kSoftmaxWarps);
             mbar_init(bar.done(), 1);
             *abort_flag = 0;
             fence_barrier_init();
@@ -464,18 +461,36 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                         flag_error(DEVERR_PAGE);
                     }
                 };
-                const int8_t* from[2];
-                auto point = [&](int u) {                     // at unit u's codes; publishes its scales
-                    const int strip = number(u) % STRIPS;
+                // Places of the next AHEAD units, whose codes are on their way to the L2 cache: from there they come in half
+                // the time that memory takes, and a warp holds no more than one unit's loads.
+                int place[AHEAD][2];
+                auto step = [&](int u) {                      // unit u's place goes into the queue, its scales to the softmax
+                    if ((u & 15) == 0) lookup(u);
 #pragma unroll
-                    for (int g = 0; g < 2; g++)
-                        from[g] = codes + (long long)__shfl_sync(0xffffffffu, src, 2 * (u & 15) + g) * (16 * D) + 128 * strip;
-                    // (the slot's last readers are far behind: K runs at most three tiles ahead of the softmax, its loads one more)
-                    if (!isv && (lane >> 1) == (u & 15) && u < units && strip == 0)
+                    for (int i = 0; i + 1 < AHEAD; i++)
+#pragma unroll
+                        for (int g = 0; g < 2; g++) place[i][g] = place[i + 1][g];
+#pragma unroll
+                    for (int g = 0; g < 2; g++) place[AHEAD - 1][g] = __shfl_sync(0xffffffffu, src, 2 * (u & 15) + g);
+                    const int strip = number(u) % STRIPS;
+                    if (u >= units) return;
+                    // lane -> a row's codes of the strip, 128 bytes at most
+                    prefetch_l2((isv ? a.c.v : a.c.k) + (long long)(lane < 16 ? place[AHEAD - 1][0] : place[AHEAD - 1][1]) * (16 * D) +
+                                (lane & 15) * D + 128 * strip);
+                    // (the slot's last readers are behind: K is at most kKStages + 1 tiles ahead of the softmax, this AHEAD more)
+                    if (!isv && (lane >> 1) == (u & 15) && strip == 0)
                         scales[(y0 + u / STRIPS) % C::kScaleSlots * 8 + 2 * w + (lane & 1)] = make_float4(ks, lv, iv, 0.f);
                 };
+                static_assert(C::kKStages + 1 + AHEAD < C::kScaleSlots, "scale slots");
+                const int8_t* from[2];
+                auto point = [&](int u) {                     // at unit u's codes, the queue's first
+                    const int strip = number(u) % STRIPS;
+#pragma unroll
+                    for (int g = 0; g < 2; g++) from[g] = codes + (long long)place[0][g] * (16 * D) + 128 * strip;
+                };
                 uint4 r[2][2][CU];
-                lookup(0);
+#pragma unroll 1
+                for (int u = 0; u < AHEAD; u++) step(u);
                 point(0);
 #pragma unroll
                 for (int g = 0; g < 2; g++)
@@ -486,13 +501,15 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 bool ok = true;
 #pragma unroll 1
                 for (int u = 0; u < units; u++) {
-                    if (((u + 1) & 15) == 0) lookup(u + 1);
+                    step(u + AHEAD);
                     point(u + 1);
                     const int v = number(u), y = y0 + v / (4 * STRIPS), quarter = v / STRIPS & 3, strip = v % STRIPS;
-                    // the stage is free once the product that read it is complete
-                    if (y >= 2) ok = ok && wait_for(isv ? bar.pvdone(y & 1) : bar.sfull(y & 1), ((y - 2) >> 1) & 1, abort_flag);
+                    const int st = y % (isv ? C::kVStages : C::kKStages);
+                    const uint32_t full = isv ? bar.vfull(st) : bar.kfull(st);
+                    ok = ok && mbar_wait_relaxed(isv ? bar.vempty(st) : bar.kempty(st),
+                                                 ((y / (isv ? C::kVStages : C::kKStages)) & 1) ^ 1, abort_flag);
                     if constexpr (isv) {
-                        const uint32_t to = sb + C::v_off + (y & 1) * C::kVBytes + quarter * (32 * 128) + strip * (2 * KT * 128);
+                        const uint32_t to = sb + C::v_off + st * C::kVBytes + quarter * (32 * 128) + strip * (2 * KT * 128);
 #pragma unroll
                         for (int g = 0; g < 2; g++)
 #pragma unroll
@@ -512,10 +529,10 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                                 }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar.vfull(y & 1));
+                        if (lane == 0) mbar_arrive(full);
                     } else {
                         tc_fence_after();
-                        const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + C::kKCol + (y & 1) * C::kKCols + 64 * strip;
+                        const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + C::kKCol + st * C::kKCols + 64 * strip;
 #pragma unroll
                         for (int g = 0; g < 2; g++)
 #pragma unroll
@@ -536,8 +553,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(bar.kfull(y & 1));
-                            if (strip == 0) mbar_arrive(bar.scale(y % C::kScaleSlots));
+                            mbar_arrive(full);
                         }
                     }
                 }
@@ -559,15 +575,18 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     ks++;
                     kx = ks < pieces ? s_piece[ks].x0 : tiles;
                 }
-                ok = ok && wait_for(bar.kfull(y & 1), (y >> 1) & 1, abort_flag);
+                const int st = y % C::kKStages;
+                ok = ok && wait_for(bar.kfull(st), (y / C::kKStages) & 1, abort_flag);
                 if (!ok) return;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; k++)
-                        umma_ts(tmem + (y & 1) * R, tmem + C::kKCol + (y & 1) * C::kKCols + 8 * k,
+                        umma_ts(tmem + (y & 1) * R, tmem + C::kKCol + st * C::kKCols + 8 * k,
                                 q_lo + (k / 4) * (R * 128 >> 4) + 2 * (k % 4), idesc_s, k > 0);
+                    mbar_arrive(bar.sfull(y & 1));
                     umma_commit(bar.sfull(y & 1));
+                    umma_commit(bar.kempty(st));
                 }
                 __syncwarp();
             };
@@ -582,12 +601,13 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     ko++;
                     xo = ko < pieces ? s_piece[ko].x0 : tiles;
                 }
-                ok = ok && wait_for(bar.vfull(y & 1), (y >> 1) & 1, abort_flag);
+                const int st = y % C::kVStages;
+                ok = ok && wait_for(bar.vfull(st), (y / C::kVStages) & 1, abort_flag);
                 ok = ok && wait_for(bar.pready(y & 1), (y >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t p = p_lo + (y & 1) * (C::kPBytes >> 4), v = v_lo + (y & 1) * (C::kVBytes >> 4);
+                    const uint32_t p = p_lo + (y & 1) * (C::kPBytes >> 4), v = v_lo + st * (C::kVBytes >> 4);
 #pragma unroll
                     for (int h = 0; h < C::kHalves; h++)
 #pragma unroll
@@ -595,6 +615,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                             umma_ss(tmem + C::kOCol + h * R, v + h * (2 * KT * 128 >> 4) + k * (2048 >> 4), p + k * (2048 >> 4),
                                     idesc_o, !fresh || k > 0);
                     umma_commit(bar.pvdone(y & 1));
+                    umma_commit(bar.vempty(st));
                 }
                 __syncwarp();
                 if (!ahead && x + 1 < tiles) product_s(x + 1);
@@ -628,34 +649,62 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 }
                 cp_async_commit();
             };
-            // In place to fp16, each row times the power of two that brings its largest magnitude to [1, 2), in the order in
-            // which K's dimensions stand: group w of four dimensions of 16t .. 16t + 15 at place 4w + t, 0 2 1 3 within.
+            // In place to fp16, in the order in which K's dimensions stand: group w of four dimensions of 16t .. 16t + 15 at place
+            // 4w + t, 0 2 1 3 within.  All rows of the group by one power of two, which brings the largest magnitude to
+            // [2^14, 2^15), so that one factor turns S into scores: a row is then exact where it was exact on its own, down
+            // to 2^-14 of its largest value and rounded to 2^-25 of it below, as long as that is within 2^13 of the group's.
+            // A smaller row is brought that near, and its S is multiplied by the rest (s_even) first.
+            float factor = 0.f;                               // of the next piece's scores
+            bool uneven = false;
             auto convert_q = [&](const Piece& p) {
                 if (p.rows > c0) {
+                    const int m = lane % LPR;
+                    const uint32_t panel = sb + C::q_off + (m / 8) * (R * 128);
                     cp_async_wait<0>();
-#pragma unroll 2
+#pragma unroll 1
                     for (int i = 0; i < N; i += RPP) {
-                        const int c = c0 + i + (w * 32 + lane) / LPR, m = lane % LPR;
-                        const uint32_t panel = sb + C::q_off + (m / 8) * (R * 128);
-                        float x[8], top = 0.f, up, down;
+                        const int c = c0 + i + (w * 32 + lane) / LPR;
+                        float x[8], top = 0.f;
                         unpack8(ld_shared_u4(panel + sw128_off(c, m % 8)), qt == MMQ_BF16, x);
 #pragma unroll
                         for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
                         for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        row_scale(top, up, down);
+                        if (m == 0) s_next[c] = top;
+                    }
+                    named_bar_sync(id, 128);
+                    float most = fmaxf(s_next[c0 + lane], s_next[c0 + N - 32 + lane]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    // exponents count from 127; a zero row's does not matter
+                    const int high = max((int)(__float_as_uint(most) >> 23), 1);
+                    factor = a.scale * LOG2E * pow2((high - 141) / 2) * pow2(high - 141 - (high - 141) / 2);
+                    uneven = false;
+#pragma unroll 1
+                    for (int i = 0; i < N; i += RPP) {
+                        const int c = c0 + i + (w * 32 + lane) / LPR;
+                        const float top = s_next[c];
+                        const int rest = top == 0.f ? 0 : max(high - 13 - max((int)(__float_as_uint(top) >> 23), 1), 0);
+                        const int up = 141 - high + rest;
+                        const float up0 = pow2(up / 2), up1 = pow2(up - up / 2);
+                        float x[8];
+                        unpack8(ld_shared_u4(panel + sw128_off(c, m % 8)), qt == MMQ_BF16, x);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[e] = x[e] * up0 * up1;
+                        if (m == 0) s_even[c] = pow2(-min(rest, 126)) * pow2(min(126 - rest, 0));
+                        uneven |= rest > 0;
                         __syncwarp();                         // the rows are read
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
                             const int four = 2 * (m % 8) + e, place = 4 * (four & 3) + (four >> 2);
-                            const uint32_t lo = pack2(x[4 * e] * up, x[4 * e + 2] * up, __half());
-                            const uint32_t hi = pack2(x[4 * e + 1] * up, x[4 * e + 3] * up, __half());
+                            const uint32_t lo = pack2(x[4 * e], x[4 * e + 2], __half());
+                            const uint32_t hi = pack2(x[4 * e + 1], x[4 * e + 3], __half());
                             asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(panel + sw128_off(c, place >> 1) + 8 * (place & 1)),
                                          "r"(lo), "r"(hi)
                                          : "memory");
                         }
-                        if (m == 0) s_next[c] = a.scale * LOG2E * down;
                     }
+                    uneven = group_any(id, uneven);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -664,15 +713,13 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
             fetch_q(s_piece[0]);
             convert_q(s_piece[0]);
             for (int k = 0; k < pieces; k++) {
-                const Piece p = s_piece[k];
+                const Piece& p = s_piece[k];
                 const bool busy = p.rows > c0, more = k + 1 < pieces;
-                named_bar_sync(id, 128);                      // s_next is there, the last piece's values are read
+                named_bar_sync(id, 128);                      // the last piece's values are read
                 if (gt < N) {
                     const int c = c0 + gt, row = p.row0 + min(c, p.rows - 1), tok = p.n0 + row / a.group;
                     const bool real = c < p.rows;
-                    float* col = reinterpret_cast<float*>(&s_col[c / 2]) + (c & 1);
-                    col[0] = real ? s_next[c] : 0.f;
-                    col[2] = real ? UNSET : -INFINITY;
+                    s_neg[c] = real ? UNSET : -INFINITY;
                     s_m[c] = -INFINITY;
                     s_tok[c] = tok;
                     if (a.window > 0) s_low[c] = p.first + a.depths[tok] - a.window + 1;
@@ -682,112 +729,133 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 uint64_t l2[N / 2];
 #pragma unroll
                 for (int i = 0; i < N / 2; i++) l2[i] = 0ull;
-                for (int x = p.x0; x < p.x0 + p.tiles; x++) {
-                    const int y = y0 + x, tok = p.tok0 + (x - p.x0) * KT, j = tok + tk;
-                    // which rows see the token: all, but for the new tokens and the window's edge
-                    const bool masked = tok + KT > p.first || (a.window > 0 && tok <= p.first + a.max_tokens - a.window);
-                    uint32_t see = 0xFFFFFFFFu;
-                    if (masked && busy) {
-                        const int d = j - p.first;
-                        if (j >= p.lim) {
-                            see = 0u;
-                        } else if (d >= 0) {
-                            see = 0u;
-                            if (d / 32 < a.words)
+                // every row sees every token of the tiles from x_low to before x_high, between the window's edge and the new tokens
+                const int x0 = p.x0, x_end = x0 + p.tiles, x_high = x0 + (p.first - p.tok0 >= 0 ? (p.first - p.tok0) / KT : 0);
+                const int x_low = a.window > 0 ? x0 + (max(p.first + a.max_tokens - a.window - p.tok0, -1) + KT) / KT : 0;
+#pragma unroll 1
+                for (int x = x0; x < x_end; x++) {
+                    const int y = y0 + x;
+                    const bool masked = x >= x_high || x < x_low;
+                    uint32_t see[N / 32];
+#pragma unroll
+                    for (int b = 0; b < N / 32; b++) see[b] = 0xFFFFFFFFu;
+                    if (__builtin_expect(masked && busy, 0)) {
+                        const int j = p.tok0 + (x - x0) * KT + tk, d = j - p.first;
+#pragma unroll
+                        for (int b = 0; b < N / 32; b++) {
+                            if (j >= p.lim) {
+                                see[b] = 0u;
+                            } else if (d >= 0) {
+                                see[b] = 0u;
+                                if (d / 32 < a.words)
 #pragma unroll 8
-                                for (int i = 0; i < N; i++)
-                                    see |= (a.masks[(long long)s_tok[c0 + i] * a.words + d / 32] >> (d % 32) & 1u) << i;
-                        } else if (a.window > 0) {
+                                    for (int i = 0; i < 32; i++)
+                                        see[b] |= (a.masks[(long long)s_tok[c0 + 32 * b + i] * a.words + d / 32] >> (d % 32) & 1u) << i;
+                            } else if (a.window > 0) {
 #pragma unroll 8
-                            for (int i = 0; i < N; i++)
-                                if (j < s_low[c0 + i]) see &= ~(1u << i);
+                                for (int i = 0; i < 32; i++)
+                                    if (j < s_low[c0 + 32 * b + i]) see[b] &= ~(1u << i);
+                            }
                         }
                     }
-                    ok = wait_for(bar.scale(y % C::kScaleSlots), (y / C::kScaleSlots) & 1, abort_flag) && ok;
                     ok = wait_for(bar.sfull(y & 1), (y >> 1) & 1, abort_flag) && ok;
                     tc_fence_after();
-                    if (more && x + 1 == p.x0 + p.tiles) fetch_q(s_piece[k + 1]);             // every S of the piece is complete
+                    if (more && x + 1 == x_end) fetch_q(s_piece[k + 1]);                      // every S of the piece is complete
                     if (busy) {
                         const float4 sc = scales[y % C::kScaleSlots * 8 + tk / 16];
-                        const uint64_t ks2 = f2_pack(sc.x, sc.x), lv2 = f2_pack(sc.y, sc.y), iv2 = f2_pack(sc.z, sc.z);
-                        uint32_t xr[N];
-                        float e[N];
-                        auto terms = [&](auto shifted) {      // e = t - m, or t
-                            tmem_load(tmem + lanes + (y & 1) * R + c0, xr);
-                            tmem_wait(xr);
 #pragma unroll
-                            for (int i = 0; i < N / 2; i++) {
-                                const float4 f = s_col[c0 / 2 + i];
-                                const uint64_t sh = decltype(shifted)::value ? f2_add(f2_pack(f.z, f.w), lv2) : lv2;
-                                const uint64_t s2 = f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1]));
-                                f2_unpack(f2_fma(s2, f2_mul(f2_pack(f.x, f.y), ks2), sh), e[2 * i], e[2 * i + 1]);
-                            }
-                            if (masked)
+                        for (int b = 0; b < N / 32; b++) {    // 32 columns
+                            const int cb = c0 + 32 * b;
+                            uint32_t xr[32];
+                            float e[32];
+                            auto terms = [&](auto shifted) {  // e = t - m, or t
+                                const uint64_t g2 = f2_pack(factor * sc.x, factor * sc.x), lv2 = f2_pack(sc.y, sc.y);
+                                tmem_ld32(tmem + lanes + (y & 1) * R + cb, xr);
+                                tmem_wait32(xr);
+                                if (__builtin_expect(uneven, 0))
 #pragma unroll
-                                for (int i = 0; i < N; i++)
-                                    if (!(see >> i & 1u)) e[i] = -INFINITY;
-                        };
-#pragma unroll 1
-                        for (int raised = 0;; raised++) {
-                            terms(std::true_type());
-                            float tops[4] = {e[0], e[1], e[2], e[3]};
+                                    for (int i = 0; i < 32; i++) xr[i] = __float_as_uint(__uint_as_float(xr[i]) * s_even[cb + i]);
 #pragma unroll
-                            for (int i = 4; i < N; i++) tops[i & 3] = fmaxf(tops[i & 3], e[i]);
-                            const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-                            if (__builtin_expect(!group_any(id, top > LAZY) || raised, 1)) break;
-                            // a term passes its row's reference by 2^LAZY: raise the references (once: then none does)
-                            terms(std::false_type());
-                            s_red[grp][w][lane % N] = across<true, N>(e);
-                            named_bar_sync(id, 128);
-                            if (gt < N) {
-                                const int c = c0 + gt;
-                                const float(&red)[4][N] = s_red[grp];
-                                const float most = fmaxf(fmaxf(red[0][gt], red[1][gt]), fmaxf(red[2][gt], red[3][gt]));
-                                const float m = s_m[c], mn = fmaxf(m, most - HEAD);
-                                s_fac[c] = m == -INFINITY ? 1.f : ex2(m - mn);
-                                if (c < p.rows && mn > -INFINITY) {
-                                    s_m[c] = mn;
-                                    reinterpret_cast<float*>(&s_col[c / 2])[2 + (c & 1)] = -mn;
-                                }
-                            }
-                            named_bar_sync(id, 128);
-                            const auto fac = [&](int i) { return f2_pack(s_fac[c0 + 2 * i], s_fac[c0 + 2 * i + 1]); };
+                                for (int i = 0; i < 8; i++) {
+                                    const float4 neg = reinterpret_cast<const float4*>(s_neg + cb)[i];
 #pragma unroll
-                            for (int i = 0; i < N / 2; i++) l2[i] = f2_mul(l2[i], fac(i));
-                            if (x > p.x0) {
-                                ok = wait_for(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
-                                tc_fence_after();
-#pragma unroll
-                                for (int o = 0; o < C::kHalves; o++) {
-                                    const uint32_t at = tmem + lanes + C::kOCol + o * R + c0;
-                                    tmem_load(at, xr);
-                                    tmem_wait(xr);
-#pragma unroll
-                                    for (int i = 0; i < N / 2; i++) {
-                                        float z0, z1;
-                                        f2_unpack(f2_mul(f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])), fac(i)),
-                                                  z0, z1);
-                                        xr[2 * i] = __float_as_uint(z0);
-                                        xr[2 * i + 1] = __float_as_uint(z1);
+                                    for (int u = 0; u < 2; u++) {
+                                        const uint64_t n2 = u ? f2_pack(neg.z, neg.w) : f2_pack(neg.x, neg.y);
+                                        const uint64_t sh = decltype(shifted)::value ? f2_add(n2, lv2) : lv2;
+                                        const int at = 4 * i + 2 * u;
+                                        f2_unpack(f2_fma(f2_pack(__uint_as_float(xr[at]), __uint_as_float(xr[at + 1])), g2, sh), e[at],
+                                                  e[at + 1]);
                                     }
-                                    tmem_store(at, xr);
                                 }
-                                tmem_st_wait();
-                            }
-                        }
-                        // P's buffer is free once the product that read it is complete
-                        if (y >= 2) ok = wait_for(bar.pvdone(y & 1), ((y - 2) >> 1) & 1, abort_flag) && ok;
-                        const uint32_t row = sb + C::p_off + (y & 1) * C::kPBytes + (c0 / 64) * (KT * 128);
+                                if (__builtin_expect(masked, 0))
 #pragma unroll
-                        for (int i = 0; i < N / 8; i++) {
-                            uint32_t z[4];
+                                    for (int i = 0; i < 32; i++)
+                                        if (!(see[b] >> i & 1u)) e[i] = -INFINITY;
+                            };
+#pragma unroll 1
+                            for (int raised = 0;; raised++) {
+                                terms(std::true_type());
+                                float tops[4] = {max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), max3(e[6], e[7], e[8]), fmaxf(e[9], e[10])};
 #pragma unroll
-                            for (int u = 0; u < 4; u++) {
-                                const float p0 = ex2(e[8 * i + 2 * u]), p1 = ex2(e[8 * i + 2 * u + 1]);
-                                l2[4 * i + u] = f2_fma(f2_pack(p0, p1), iv2, l2[4 * i + u]);
-                                z[u] = pack2(p0, p1, __half());
+                                for (int i = 11; i < 27; i += 8)
+#pragma unroll
+                                    for (int u = 0; u < 4; u++) tops[u] = max3(tops[u], e[i + 2 * u], e[i + 2 * u + 1]);
+                                const float top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], e[27], e[28]), max3(e[29], e[30], e[31]));
+                                if (__builtin_expect(!group_any(id, top > LAZY) || raised, 1)) break;
+                                // a term passes its row's reference by 2^LAZY: raise the references (once: then none does)
+                                terms(std::false_type());
+                                s_red[grp][w][32 * b + lane] = across<true>(e);
+                                named_bar_sync(id, 128);
+                                if (gt < 32) {
+                                    const int c = cb + gt, at = 32 * b + gt;
+                                    const float(&red)[4][N] = s_red[grp];
+                                    const float most = fmaxf(fmaxf(red[0][at], red[1][at]), fmaxf(red[2][at], red[3][at]));
+                                    const float m = s_m[c], mn = fmaxf(m, most - HEAD);
+                                    s_fac[c] = m == -INFINITY ? 1.f : ex2(m - mn);
+                                    if (c < p.rows && mn > -INFINITY) {
+                                        s_m[c] = mn;
+                                        s_neg[c] = -mn;
+                                    }
+                                }
+                                named_bar_sync(id, 128);
+                                const auto fac = [&](int i) { return f2_pack(s_fac[cb + 2 * i], s_fac[cb + 2 * i + 1]); };
+#pragma unroll
+                                for (int i = 0; i < 16; i++) l2[16 * b + i] = f2_mul(l2[16 * b + i], fac(i));
+                                if (x > x0) {
+                                    ok = wait_for(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int o = 0; o < C::kHalves; o++) {
+                                        const uint32_t at = tmem + lanes + C::kOCol + o * R + cb;
+                                        tmem_ld32(at, xr);
+                                        tmem_wait32(xr);
+#pragma unroll
+                                        for (int i = 0; i < 16; i++) {
+                                            float z0, z1;
+                                            f2_unpack(f2_mul(f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])), fac(i)),
+                                                      z0, z1);
+                                            xr[2 * i] = __float_as_uint(z0);
+                                            xr[2 * i + 1] = __float_as_uint(z1);
+                                        }
+                                        tmem_st32(at, xr);
+                                    }
+                                    tmem_st_wait();
+                                }
                             }
-                            st_shared_v4(row + sw128_off(tk, c0 % 64 / 8 + i), z[0], z[1], z[2], z[3]);
+                            // (P's buffer is free: S of this tile came after the product that read it)
+                            const uint32_t row = sb + C::p_off + (y & 1) * C::kPBytes + (cb / 64) * (KT * 128);
+                            const uint64_t iv2 = f2_pack(sc.z, sc.z);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                uint32_t z[4];
+#pragma unroll
+                                for (int u = 0; u < 4; u++) {
+                                    const float p0 = ex2(e[8 * i + 2 * u]), p1 = ex2(e[8 * i + 2 * u + 1]);
+                                    l2[16 * b + 4 * i + u] = f2_fma(f2_pack(p0, p1), iv2, l2[16 * b + 4 * i + u]);
+                                    z[u] = pack2(p0, p1, __half());
+                                }
+                                st_shared_v4(row + sw128_off(tk, cb % 64 / 8 + i), z[0], z[1], z[2], z[3]);
+                            }
                         }
                         fence_proxy_async_smem();
                     }
@@ -797,15 +865,16 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 }
                 if (more) convert_q(s_piece[k + 1]);
                 // ---- the piece's result
-                const int yz = y0 + p.x0 + p.tiles - 1;
+                const int yz = y0 + x_end - 1;
                 ok = wait_for(bar.pvdone(yz & 1), (yz >> 1) & 1, abort_flag) && ok;
                 tc_fence_after();
                 if (busy) {
-                    {
-                        float e[N];
 #pragma unroll
-                        for (int i = 0; i < N / 2; i++) f2_unpack(l2[i], e[2 * i], e[2 * i + 1]);
-                        s_red[grp][w][lane % N] = across<false, N>(e);
+                    for (int b = 0; b < N / 32; b++) {
+                        float e[32];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) f2_unpack(l2[16 * b + i], e[2 * i], e[2 * i + 1]);
+                        s_red[grp][w][32 * b + lane] = across<false>(e);
                     }
                     named_bar_sync(id, 128);
                     if (gt < N && c0 + gt < p.rows) {
@@ -839,20 +908,21 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     if (ok && (D != 64 || w < 2)) {
                         const int dim = 32 * w + ((lane & ~3) | (lane & 1) << 1 | (lane >> 1 & 1));       // order 0 2 1 3 undone
 #pragma unroll 1
-                        for (int o = 0; o < C::kHalves; o++) {
-                            const int d = 128 * o + dim;
-                            uint32_t xr[N];
-                            tmem_load(tmem + lanes + C::kOCol + o * R + c0, xr);
-                            tmem_wait(xr);
-                            float* part = work.part_o + ((long long)p.slot * R + c0) * D + d;
+                        for (int b = 0; b < C::kHalves * (N / 16); b++) {
+                            const int o = b / (N / 16), cb = c0 + b % (N / 16) * 16, d = 128 * o + dim;
+                            uint32_t xr[16];
+                            tmem_ld16(tmem + lanes + C::kOCol + o * R + cb, xr);
+                            tmem_ld_wait(xr);
+                            float* part = work.part_o + ((long long)p.slot * R + cb) * D + d;
+                            const int left = p.rows - cb, flags = p.flags;
 #pragma unroll
-                            for (int i = 0; i < N; i++) {
-                                if (c0 + i >= p.rows) break;
-                                const float keep = s_fac[c0 + i];
+                            for (int i = 0; i < 16; i++) {
+                                if (i >= left) break;
+                                const float keep = s_fac[cb + i];
                                 float v = keep == 0.f ? 0.f : __uint_as_float(xr[i]) * keep;
-                                if (p.flags & P_PREV) v = fmaf(part[i * D], s_add[c0 + i], v);
-                                if (p.flags & P_DIRECT) {
-                                    const long long at = s_out[c0 + i] + d;
+                                if (flags & P_PREV) v = fmaf(part[i * D], s_add[cb + i], v);
+                                if (flags & P_DIRECT) {
+                                    const long long at = s_out[cb + i] + d;
                                     if (ot == MMQ_F32) static_cast<float*>(a.out.data)[at] = v;
                                     else if (ot == MMQ_BF16) static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16(v);
                                     else static_cast<__half*>(a.out.data)[at] = __float2half(v);
