@@ -51,16 +51,18 @@ template <int D, int R> struct Tree {
     // Tiles of K and V that the converters may be ahead: with two of each every wait of one role stops the others.
     static constexpr int kKStages = D == 64 ? 4 : (R == 64 && D == 128 ? 4 : 2);
     static constexpr int kVStages = D == 64 ? 4 : (D == 128 ? (R == 64 ? 4 : 3) : 2);
-    // TMEM columns: two buffers of S, O, K
-    static constexpr int kOCol = 2 * R, kKCol = kOCol + kHalves * R;
+    // Buffers of S and of P.  With two, S of a tile waits for the softmax two tiles before, and then for the products in between.
+    static constexpr int kBufs = R == 64 && D <= 128 ? 3 : 2;
+    // TMEM columns: S, O, K
+    static constexpr int kOCol = kBufs * R, kKCol = kOCol + kHalves * R;
     static_assert(kKCol + kKStages * kKCols <= 512, "TMEM budget");
     // V first: for head_dim 64 the products read the next 16 KB as 64 more dimensions, whose results nothing looks at
     static constexpr int v_off = 0;
     static constexpr int q_off = v_off + kVStages * kVBytes;
     static constexpr int p_off = q_off + kQBytes;
-    static constexpr int sc_off = p_off + 2 * kPBytes;                           // float4 [slots][8]
+    static constexpr int sc_off = p_off + kBufs * kPBytes;                           // float4 [slots][8]
     static constexpr int bar_off = sc_off + kScaleSlots * 8 * 16;
-    static constexpr int n_bars = 9 + 2 * (kKStages + kVStages);
+    static constexpr int n_bars = 5 + 2 * (kBufs + kKStages + kVStages);
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int total = misc_off + 16, alloc = total + 1024;
     static_assert(alloc <= 232448 - (R == 64 ? 16 : 20) * 1024, "shared memory budget (the rest is static)");
@@ -182,18 +184,18 @@ template <int D, int R> struct TreeBars {
     using C = Tree<D, R>;
     uint32_t b;
     __device__ uint32_t rest(int i) const { return b + 8u * i; }
-    // Of tiles i mod 2.  As products complete in their order, S of a tile shows that the product with V two tiles before is
-    // complete.
-    __device__ uint32_t sfull(int i) const { return rest(i); }
-    __device__ uint32_t pready(int i) const { return rest(2 + i); }
-    __device__ uint32_t pvdone(int i) const { return rest(4 + i); }
-    __device__ uint32_t qfull() const { return rest(6); }                        // a piece's queries
-    __device__ uint32_t ofree() const { return rest(7); }                        // a piece's O is read
-    __device__ uint32_t done() const { return rest(8); }
-    __device__ uint32_t kfull(int i) const { return rest(9 + i); }
-    __device__ uint32_t kempty(int i) const { return rest(9 + C::kKStages + i); }
-    __device__ uint32_t vfull(int i) const { return rest(9 + 2 * C::kKStages + i); }
-    __device__ uint32_t vempty(int i) const { return rest(9 + 2 * C::kKStages + C::kVStages + i); }
+    __device__ uint32_t pvdone(int i) const { return rest(i); }                  // of tiles i mod 2
+    __device__ uint32_t qfull() const { return rest(2); }                        // a piece's queries
+    __device__ uint32_t ofree() const { return rest(3); }                        // a piece's O is read
+    __device__ uint32_t done() const { return rest(4); }
+    // of tiles i mod kBufs; as products complete in their order, S of a tile shows that the product with V kBufs tiles before is
+    // complete
+    __device__ uint32_t sfull(int i) const { return rest(5 + i); }
+    __device__ uint32_t pready(int i) const { return rest(5 + C::kBufs + i); }
+    __device__ uint32_t kfull(int i) const { return rest(5 + 2 * C::kBufs + i); }
+    __device__ uint32_t kempty(int i) const { return rest(5 + 2 * C::kBufs + C::kKStages + i); }
+    __device__ uint32_t vfull(int i) const { return rest(5 + 2 * (C::kBufs + C::kKStages) + i); }
+    __device__ uint32_t vempty(int i) const { return rest(5 + 2 * (C::kBufs + C::kKStages) + C::kVStages + i); }
 };
 
 // A sequence's place in the line of tiles.
@@ -376,11 +378,11 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 mbar_init(bar.vfull(i), 4 * STRIPS);
                 mbar_init(bar.vempty(i), 1);
             }
-            for (int i = 0; i < 2; i++) {
+            for (int i = 0; i < C::kBufs; i++) {
                 mbar_init(bar.sfull(i), 2);                   // the product, and the thread that saw K and its scales
                 mbar_init(bar.pready(i), C::kSoftmaxWarps);
-                mbar_init(bar.pvdone(i), 1);
             }
+            for (int i = 0; i < 2; i++) mbar_init(bar.pvdone(i), 1);
             mbar_init(bar.qfull(), C::kSoftmaxWarps);
             mbar_init(bar.ofree(), C::kSoftmaxWarps);
             mbar_init(bar.done(), 1);
@@ -477,11 +479,11 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     // lane -> a row's codes of the strip, 128 bytes at most
                     prefetch_l2((isv ? a.c.v : a.c.k) + (long long)(lane < 16 ? place[AHEAD - 1][0] : place[AHEAD - 1][1]) * (16 * D) +
                                 (lane & 15) * D + 128 * strip);
-                    // (the slot's last readers are behind: K is at most kKStages + 1 tiles ahead of the softmax, this AHEAD more)
+                    // (the slot's last readers are behind: K is at most kKStages + kBufs tiles ahead of the softmax, this AHEAD more)
                     if (!isv && (lane >> 1) == (u & 15) && strip == 0)
                         scales[(y0 + u / STRIPS) % C::kScaleSlots * 8 + 2 * w + (lane & 1)] = make_float4(ks, lv, iv, 0.f);
                 };
-                static_assert(C::kKStages + 1 + AHEAD < C::kScaleSlots, "scale slots");
+                static_assert(C::kKStages + C::kBufs + AHEAD < C::kScaleSlots, "scale slots");
                 const int8_t* from[2];
                 auto point = [&](int u) {                     // at unit u's codes, the queue's first
                     const int strip = number(u) % STRIPS;
@@ -575,27 +577,28 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     ks++;
                     kx = ks < pieces ? s_piece[ks].x0 : tiles;
                 }
-                const int st = y % C::kKStages;
+                const int st = y % C::kKStages, buf = y % C::kBufs;
                 ok = ok && wait_for(bar.kfull(st), (y / C::kKStages) & 1, abort_flag);
                 if (!ok) return;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; k++)
-                        umma_ts(tmem + (y & 1) * R, tmem + C::kKCol + st * C::kKCols + 8 * k,
+                        umma_ts(tmem + buf * R, tmem + C::kKCol + st * C::kKCols + 8 * k,
                                 q_lo + (k / 4) * (R * 128 >> 4) + 2 * (k % 4), idesc_s, k > 0);
-                    mbar_arrive(bar.sfull(y & 1));
-                    umma_commit(bar.sfull(y & 1));
+                    mbar_arrive(bar.sfull(buf));
+                    umma_commit(bar.sfull(buf));
                     umma_commit(bar.kempty(st));
                 }
                 __syncwarp();
             };
-            product_s(0);
             int ko = 0, xo = 0;                               // the piece whose O is summed next, and its first tile
+            int xs = 0;                                       // tile whose S comes next
             for (int x = 0; ok && x < tiles; x++) {
-                const int y = y0 + x;
-                const bool fresh = x == xo, ahead = x + 1 < tiles && x + 1 != kx;
-                if (ahead) product_s(x + 1);
+                const int y = y0 + x, buf = y % C::kBufs;
+                // S is ahead of the softmax, but for a piece's first tile: its queries come after the last piece's last tile
+                while (ok && xs < tiles && xs < x + C::kBufs && (xs != kx || xs == x)) product_s(xs++);
+                const bool fresh = x == xo;
                 if (fresh) {
                     if (k0 + ko > 0) ok = ok && wait_for(bar.ofree(), (k0 + ko - 1) & 1, abort_flag);
                     ko++;
@@ -603,11 +606,11 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 }
                 const int st = y % C::kVStages;
                 ok = ok && wait_for(bar.vfull(st), (y / C::kVStages) & 1, abort_flag);
-                ok = ok && wait_for(bar.pready(y & 1), (y >> 1) & 1, abort_flag);
+                ok = ok && wait_for(bar.pready(buf), (y / C::kBufs) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t p = p_lo + (y & 1) * (C::kPBytes >> 4), v = v_lo + st * (C::kVBytes >> 4);
+                    const uint32_t p = p_lo + buf * (C::kPBytes >> 4), v = v_lo + st * (C::kVBytes >> 4);
 #pragma unroll
                     for (int h = 0; h < C::kHalves; h++)
 #pragma unroll
@@ -618,7 +621,6 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     umma_commit(bar.vempty(st));
                 }
                 __syncwarp();
-                if (!ahead && x + 1 < tiles) product_s(x + 1);
             }
         }
         });
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 const int x_low = a.window > 0 ? x0 + (max(p.first + a.max_tokens - a.window - p.tok0, -1) + KT) / KT : 0;
 #pragma unroll 1
                 for (int x = x0; x < x_end; x++) {
-                    const int y = y0 + x;
+                    const int y = y0 + x, buf = y % C::kBufs;
                     const bool masked = x >= x_high || x < x_low;
                     uint32_t see[N / 32];
 #pragma unroll
@@ -758,7 +760,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                             }
                         }
                     }
-                    ok = wait_for(bar.sfull(y & 1), (y >> 1) & 1, abort_flag) && ok;
+                    ok = wait_for(bar.sfull(buf), (y / C::kBufs) & 1, abort_flag) && ok;
                     tc_fence_after();
                     if (more && x + 1 == x_end) fetch_q(s_piece[k + 1]);                      // every S of the piece is complete
                     if (busy) {
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                             float e[32];
                             auto terms = [&](auto shifted) {  // e = t - m, or t
                                 const uint64_t g2 = f2_pack(factor * sc.x, factor * sc.x), lv2 = f2_pack(sc.y, sc.y);
-                                tmem_ld32(tmem + lanes + (y & 1) * R + cb, xr);
+                                tmem_ld32(tmem + lanes + buf * R + cb, xr);
                                 tmem_wait32(xr);
                                 if (__builtin_expect(uneven, 0))
 #pragma unroll
@@ -843,7 +845,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                                 }
                             }
                             // (P's buffer is free: S of this tile came after the product that read it)
-                            const uint32_t row = sb + C::p_off + (y & 1) * C::kPBytes + (cb / 64) * (KT * 128);
+                            const uint32_t row = sb + C::p_off + buf * C::kPBytes + (cb / 64) * (KT * 128);
                             const uint64_t iv2 = f2_pack(sc.z, sc.z);
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
@@ -861,7 +863,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.pready(y & 1));
+                    if (lane == 0) mbar_arrive(bar.pready(buf));
                 }
                 if (more) convert_q(s_piece[k + 1]);
                 // ---- the piece's result
