@@ -143,6 +143,7 @@ struct TreeArgs {
 struct TreePlan {
     int rows, ranges;
     bool many_parts;           // a unit is cut into many
+    bool fits;                 // positions in the line of tiles are 32-bit numbers
     size_t joins, part_ml, part_o, total;
 };
 TreePlan tree_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv);

@@ -339,7 +339,8 @@ size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_he
         return 0;
     if (max_tokens > tokens) max_tokens = tokens;
     if (max_tokens > MMQ_MAX_DRAFT) return 0;
-    return tree_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len).total;
+    const TreePlan p = tree_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
+    return p.fits ? p.total : 0;
 }
 
 mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs,
@@ -366,6 +367,7 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     if (tree->mask_words < (max_tokens + 31) / 32 || tree->mask_words * tokens > kMaxDim) return MMQ_ERR_SHAPE;
     if (!aligned16(tree->masks) || !aligned16(tree->depths)) return MMQ_ERR_ALIGN;
     const TreePlan p = tree_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
+    if (!p.fits) return MMQ_ERR_SHAPE;
     if (!workspace || workspace_bytes < p.total) return MMQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
     TreeArgs a{};

@@ -41,6 +41,9 @@ template <int D, int R> struct Tree {
     static constexpr int kWarpK = kSoftmaxWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kWarpsV, kWarps = kWarpMma + 1;
     static constexpr int kThreads = kWarps * 32;
     // registers a thread: 96 at launch of 20 warps; of 24 warps 80, some of which move to the softmax warps
+    // Units that a converter warp has on their way to L2 besides those in its registers: 16 sequences of 8192, 32 rows, take 89 us
+    // with one, 87 with two, 91 with three; with 128 rows, where fewer registers are left, 122, 130 and 142.
+    static constexpr int kAhead = R == 64 ? 2 : 1;
     static constexpr int kRegsSoftmax = 88, kRegsRest = 64;
     static_assert(R == 64 || kSoftmaxWarps * kRegsSoftmax + 8 * kRegsRest <= 24 * 80, "register budget");
     static constexpr int kHalves = D == 256 ? 2 : 1;                             // O^T of 128 dimensions
@@ -198,6 +201,11 @@ template <int D, int R> struct TreeBars {
     __device__ uint32_t vempty(int i) const { return rest(5 + 2 * (C::kBufs + C::kKStages) + C::kVStages + i); }
 };
 
+// What a unit costs besides its tiles, in tiles: its queries, its result, and the pipeline in between.  In the line it stands
+// before them, or a block whose share lies among short sequences would be the last by far: 24 sequences of up to 8192 tokens,
+// 64 rows, take 147 us with 0, 97 with 4, 91 with 5, 89 with 8; 16 of 8192 each, 32 rows, 91, 89, 87 and 91.
+constexpr int EXTRA = 5;
+
 // A sequence's place in the line of tiles.
 struct Line {
     Seq q;
@@ -218,11 +226,12 @@ __device__ __forceinline__ Line line_of(const TreeArgs& a, int s) {
 }
 
 // The line of tiles: every sequence's units one after the other, heads before row blocks, shared out evenly.  The host keeps
-// it below 2^31 tiles.
+// it below 2^30.
 struct LineShare {
     int w[32], u[32];            // of the scan
-    int span[2];                 // first and last unit of the window
-    int all, ranges;             // tiles of the line; shares that are not empty
+    int span[2];                 // first and last unit with tiles in the window
+    int skip, tiles;             // what the window has of the first one's EXTRA; the window's tiles
+    int all, ranges;             // length of the line; shares that are not empty
     __device__ int start(int c) const { return c * (all / ranges) + min(c, all % ranges); }
     __device__ int range_of(int t) const {
         const int q = all / ranges, r = all % ranges;
@@ -230,10 +239,11 @@ struct LineShare {
     }
 };
 
-// Lists the pieces of window `window` of this block's share; all its threads take part.  The first call works out the line.
-template <int R>
+// Lists the pieces of window `window` of this block's share; its first THREADS threads take part.  The first call works out
+// the line.
+template <int R, int THREADS>
 __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& work, LineShare& sh, Piece* pieces, int window) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, range = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = THREADS / 32, range = blockIdx.x;
     auto exclusive = [&](int w, int u, int& wx, int& ux, int& wall, int& uall) {
         int wi = w, ui = u;
 #pragma unroll
@@ -244,12 +254,12 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
                 ui += z;
             }
         }
-        __syncthreads();                                      // the arrays' last readers are done
+        named_bar_sync(15, THREADS);                          // the arrays' last readers are done
         if (lane == 31) {
             sh.w[warp] = wi;
             sh.u[warp] = ui;
         }
-        __syncthreads();
+        named_bar_sync(15, THREADS);
         // every warp joins the warps' sums for itself
         int wv = lane < warps ? sh.w[lane] : 0, uv = lane < warps ? sh.u[lane] : 0;
         const int wm = wv, um = uv;
@@ -275,13 +285,13 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
         if (s < a.sq.seqs) {
             x = line_of<R>(a, s);
             units = x.blocks * a.c.heads;
-            w = x.tiles * units;
+            w = (EXTRA + x.tiles) * units;
         }
         exclusive(w, units, wx, ux, wall, uall);
     };
     if (window == 0) {
         int all = 0;
-        for (int s0 = 0; s0 < a.sq.seqs; s0 += blockDim.x) {
+        for (int s0 = 0; s0 < a.sq.seqs; s0 += THREADS) {
             look(s0);
             all += wall;
             const int s = s0 + threadIdx.x;
@@ -294,26 +304,47 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
             sh.all = all;
             sh.ranges = max(min((int)gridDim.x, all), 1);
         }
-        __syncthreads();
+        named_bar_sync(15, THREADS);
     }
     if (range >= sh.ranges || sh.all == 0) {
         if (threadIdx.x == 0) work.joins[2 * range + 1] = make_int4(0, 0, 0, 0);
         return;
     }
     const int g0 = sh.start(range), g1 = sh.start(range + 1), g = g0 + window * WINDOW, gz = min(g + WINDOW, g1);
-    const bool once = a.sq.seqs <= blockDim.x;                // what the first pass saw is still there
+    if (g >= g1) return;
+    const bool once = a.sq.seqs <= THREADS;                // what the first pass saw is still there
     int wbase = 0, ubase = 0;
-    for (int s0 = 0; wbase < gz; s0 += blockDim.x) {
+    for (int s0 = 0; wbase < gz; s0 += THREADS) {
         if (!once || window > 0) look(s0);
-        const int ws = wbase + wx, us = ubase + ux;
-        if (ws <= g && g - ws < w) sh.span[0] = us + (g - ws) / x.tiles;
-        if (ws < gz && gz - ws <= w) sh.span[1] = us + (gz - 1 - ws) / x.tiles;
-        __syncthreads();
+        const int ws = wbase + wx, us = ubase + ux, each = EXTRA + x.tiles, s = s0 + threadIdx.x;
+        if (ws <= g && g - ws < w) {
+            const int k = (g - ws) / each, tile0 = ws + k * each + EXTRA;
+            sh.span[0] = us + k;
+            sh.skip = max(tile0 - g, 0);
+            if (window == 0) {
+                // The join of the unit that this range begins within, if the range before is the first with tiles of it.
+                const int head = k / x.blocks, row0 = (k - head * x.blocks) * R;
+                int parts = 0, slot0 = 0;
+                if (tile0 < g && tile0 >= sh.start(range - 1)) {
+                    parts = sh.range_of(tile0 + x.tiles - 1) - (range - 1) + 1;
+                    slot0 = 2 * (range - 1) + (tile0 > sh.start(range - 1));
+                }
+                work.joins[2 * range] = make_int4(x.q.n0, row0, min(x.n * a.group - row0, R), head);
+                work.joins[2 * range + 1] = make_int4(parts, slot0, 2 * range, 0);
+            }
+        }
+        named_bar_sync(15, THREADS);
         if (ws < gz && g - ws < w) {
-            const int u0 = sh.span[0], first = x.q.len - x.q.n, s = s0 + threadIdx.x;
-            const int k1 = min((gz - 1 - ws) / x.tiles, units - 1);
-            for (int k = g > ws ? (g - ws) / x.tiles : 0; k <= k1; k++) {
-                const int u = ws + k * x.tiles, uz = u + x.tiles, lo = max(u, g), hi = min(uz, gz);
+            const int u0 = sh.span[0], first = x.q.len - x.q.n;
+            const int k1 = min((gz - 1 - ws) / each, units - 1);
+            for (int k = g > ws ? (g - ws) / each : 0; k <= k1; k++) {
+                const int tile0 = ws + k * each + EXTRA, end = tile0 + x.tiles, lo = max(tile0, g), hi = min(end, gz);
+                const int at = us + k - u0, x0 = at == 0 ? 0 : tile0 - g - sh.skip - at * EXTRA;
+                if (end >= gz) {                              // the window's last, perhaps without tiles in it
+                    sh.tiles = x0 + max(hi - lo, 0);
+                    sh.span[1] = us + k - (hi <= lo);
+                }
+                if (hi <= lo) continue;
                 Piece p;
                 p.s = s;
                 p.head = k / x.blocks;
@@ -322,35 +353,24 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
                 p.lim = min(min(x.q.end, a.max_kv), first + x.n);
                 p.row0 = (k - p.head * x.blocks) * R;
                 p.rows = min(x.n * a.group - p.row0, R);
-                p.tok0 = x.base + (lo - u) * KT;
-                p.x0 = lo - g;
+                p.tok0 = x.base + (lo - tile0) * KT;
+                p.x0 = x0;
                 p.tiles = hi - lo;
-                p.slot = 2 * range + (u > g0);
-                p.flags = (lo > max(u, g0) ? P_PREV : 0) | (hi == uz && u >= g0 ? P_DIRECT : 0);
-                pieces[us + k - u0] = p;
-                if (window == 0 && u <= g0 && uz > g0) {
-                    // the join of the unit that this range begins within, if the range before is the unit's first
-                    int parts = 0, slot0 = 0;
-                    if (u < g0 && u >= sh.start(range - 1)) {
-                        parts = sh.range_of(uz - 1) - (range - 1) + 1;
-                        slot0 = 2 * (range - 1) + (u > sh.start(range - 1));
-                    }
-                    work.joins[2 * range] = make_int4(p.n0, p.row0, p.rows, p.head);
-                    work.joins[2 * range + 1] = make_int4(parts, slot0, 2 * range, 0);
-                }
+                p.slot = 2 * range + (tile0 > g0);
+                p.flags = (lo > max(tile0, g0) ? P_PREV : 0) | (hi == end && tile0 >= g0 ? P_DIRECT : 0);
+                pieces[at] = p;
             }
         }
         wbase += wall;
         ubase += uall;
     }
-    __syncthreads();
 }
 
 template <int D, int R>
 __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
     tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeWork work, int qt, int ot) {
     using C = Tree<D, R>;
-    constexpr int STRIPS = C::kStrips, CU = C::kChunks, AHEAD = 3;
+    constexpr int STRIPS = C::kStrips, CU = C::kChunks, AHEAD = C::kAhead;
     pdl_wait();
     pdl_trigger();                                            // after the wait: the join reads its inputs before its own
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -393,21 +413,20 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    list_pieces<R>(a, work, s_line, s_piece, 0);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const int share = blockIdx.x < s_line.ranges && s_line.all > 0 ? s_line.start(blockIdx.x + 1) - s_line.start(blockIdx.x) : 0;
-    // Every role goes over the windows; all meet when one is listed and when it is done.  The roles stand inside the branch that
-    // sets their share of registers.
-    auto windows = [&](auto&& role) {
+    // Every role goes over the windows, which the softmax warps list; all meet when one is listed and when it is done.  The roles
+    // stand inside the branch that sets their share of registers.
+    auto windows = [&](auto lists, auto&& role) {
         int y0 = 0, k0 = 0;                                   // tiles and pieces of the windows before
 #pragma unroll 1
-        for (int window = 0; y0 < share; window++) {
-            if (window > 0) list_pieces<R>(a, work, s_line, s_piece, window);
-            const int tiles = min(share - y0, WINDOW), pieces = s_line.span[1] - s_line.span[0] + 1;
-            role(tiles, pieces, y0, k0);
+        for (int window = 0;; window++) {
+            if constexpr (decltype(lists)::value) list_pieces<R, 32 * C::kSoftmaxWarps>(a, work, s_line, s_piece, window);
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+            if (blockIdx.x >= s_line.ranges || s_line.start(blockIdx.x) + window * WINDOW >= s_line.start(blockIdx.x + 1)) break;
+            const uint32_t tmem = *tmem_slot;
+            const int tiles = s_line.tiles, pieces = s_line.span[1] - s_line.span[0] + 1;
+            if (tiles > 0) role(tmem, tiles, pieces, y0, k0);       // (a share may lie between the tiles of two units)
             __syncthreads();
             y0 += tiles;
             k0 += pieces;
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
     };
     if (warp >= C::kWarpK) {
         if constexpr (R == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-        windows([&](const int tiles, const int pieces, const int y0, const int k0) {
+        windows(std::false_type{}, [&](const uint32_t tmem, const int tiles, const int pieces, const int y0, const int k0) {
         if (warp != C::kWarpMma) {
             // ======================================================= converters
             // Units of 32 tokens (two groups of 16, each within one page and scale block) and up to 128 dimensions.  Of K, a warp
@@ -632,7 +651,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
         }
     } else {
         if constexpr (R == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-        windows([&](const int, const int pieces, const int y0, const int) {
+        windows(std::true_type{}, [&](const uint32_t tmem, const int, const int pieces, const int y0, const int) {
             // ======================================================= softmax: one thread a token
             // A failed wait does not leave the loops (the group meets at barriers); later waits then return at once.
             const int grp = warp >> 2, w = warp & 3, tk = 32 * w + lane, gt = threadIdx.x & 127, c0 = grp * N;
@@ -732,17 +751,18 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < N / 2; i++) l2[i] = 0ull;
                 // every row sees every token of the tiles from x_low to before x_high, between the window's edge and the new tokens
-                const int x0 = p.x0, x_end = x0 + p.tiles, x_high = x0 + (p.first - p.tok0 >= 0 ? (p.first - p.tok0) / KT : 0);
-                const int x_low = a.window > 0 ? x0 + (max(p.first + a.max_tokens - a.window - p.tok0, -1) + KT) / KT : 0;
+                const int y_end = y0 + p.x0 + p.tiles;
+                const int y_high = y0 + p.x0 + (p.first - p.tok0 >= 0 ? (p.first - p.tok0) / KT : 0);
+                const int y_low = a.window > 0 ? y0 + p.x0 + (max(p.first + a.max_tokens - a.window - p.tok0, -1) + KT) / KT : 0;
 #pragma unroll 1
-                for (int x = x0; x < x_end; x++) {
-                    const int y = y0 + x, buf = y % C::kBufs;
-                    const bool masked = x >= x_high || x < x_low;
+                for (int y = y0 + p.x0; y < y_end; y++) {
+                    const int buf = y % C::kBufs;
+                    const bool masked = y >= y_high || y < y_low;
                     uint32_t see[N / 32];
 #pragma unroll
                     for (int b = 0; b < N / 32; b++) see[b] = 0xFFFFFFFFu;
                     if (__builtin_expect(masked && busy, 0)) {
-                        const int j = p.tok0 + (x - x0) * KT + tk, d = j - p.first;
+                        const int j = p.tok0 + (y - (y_end - p.tiles)) * KT + tk, d = j - p.first;
 #pragma unroll
                         for (int b = 0; b < N / 32; b++) {
                             if (j >= p.lim) {
@@ -762,7 +782,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     }
                     ok = wait_for(bar.sfull(buf), (y / C::kBufs) & 1, abort_flag) && ok;
                     tc_fence_after();
-                    if (more && x + 1 == x_end) fetch_q(s_piece[k + 1]);                      // every S of the piece is complete
+                    if (more && y + 1 == y_end) fetch_q(s_piece[k + 1]);                      // every S of the piece is complete
                     if (busy) {
                         const float4 sc = scales[y % C::kScaleSlots * 8 + tk / 16];
 #pragma unroll
@@ -823,7 +843,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                                 const auto fac = [&](int i) { return f2_pack(s_fac[cb + 2 * i], s_fac[cb + 2 * i + 1]); };
 #pragma unroll
                                 for (int i = 0; i < 16; i++) l2[16 * b + i] = f2_mul(l2[16 * b + i], fac(i));
-                                if (x > x0) {
+                                if (y > y_end - p.tiles) {
                                     ok = wait_for(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
                                     tc_fence_after();
 #pragma unroll 1
@@ -867,7 +887,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 }
                 if (more) convert_q(s_piece[k + 1]);
                 // ---- the piece's result
-                const int yz = y0 + x_end - 1;
+                const int yz = y_end - 1;
                 ok = wait_for(bar.pvdone(yz & 1), (yz >> 1) & 1, abort_flag) && ok;
                 tc_fence_after();
                 if (busy) {
@@ -945,7 +965,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == C::kWarpMma) tmem_dealloc(tmem, 512);
+    if (warp == C::kWarpMma) tmem_dealloc(*tmem_slot, 512);
 }
 
 // The parts of a unit that several ranges hold, on a common reference and in their order.  A block looks after rows of the
@@ -1037,6 +1057,8 @@ TreePlan tree_plan(long long tokens, int heads, int kv_heads, int dim, int seqs,
     p.rows = dim == 256 || rows <= 64 ? 64 : 128;
     const long long each = seqs * ((rows + p.rows - 1) / p.rows), packed = tokens * group / p.rows + seqs;
     const long long units = kv_heads * std::min(each, packed), tiles = std::max((max_kv + KT - 1) / KT, 1ll);
+    p.fits = (double)kv_heads * (double)each * (double)(EXTRA + tiles) < 1073741824.0;
+    if (!p.fits) return p;
     const long long shares = (units * tiles + LEAST - 1) / LEAST;
     p.ranges = (int)std::min(shares, SMS);
     p.many_parts = units <= SMS / 8;

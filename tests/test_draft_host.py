@@ -127,6 +127,19 @@ def test_workspace_sizes(lib):  # noqa: F811
         assert size(*bad) == 0, bad
 
 
+def test_line_of_tiles_is_bounded(lib):  # noqa: F811
+    """What the kernel numbers with 32 bits: the bounds' tiles over all sequences and heads."""
+    size = lib.mmq_attention_tree_workspace_bytes
+    big, most = 1 << 20, (1 << 30) // (16 * 8192) * 128 - 5 * 128
+    for tokens, kv_heads, n, max_kv, fits in ((8192, 16, 8192, most - 128, True), (8192, 16, 8192, most, False),
+                                                 (big, 64, big, 100000, False), (1, (1 << 31) - 1, (1 << 31) - 1, 1 << 30, False)):
+        need = size(tokens, kv_heads, kv_heads, 128, n, 1, max_kv)
+        assert (need > 0) == fits
+        if not fits and kv_heads < 100:
+            assert lib.mmq_attention_tree(heads(), kv_heads, cache(h=kv_heads), seqs(n=n), tree(), tokens, 1, max_kv, 0.1, 0,
+                                          heads(), None, FAKE, 1 << 40, None) == SHAPE
+
+
 def test_binding_refuses_what_it_cannot_pass(lib):  # noqa: F811
     torch = pytest.importorskip("torch")
     x = torch.zeros(2, dtype=torch.int32)
