@@ -99,15 +99,12 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 // 16 lanes x 32 columns in the layout of tmem_ld_16x256b_x4.
@@ -847,19 +844,15 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                                     ok = wait_for(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
                                     tc_fence_after();
 #pragma unroll 1
-                                    for (int o = 0; o < C::kHalves; o++) {
-                                        const uint32_t at = tmem + lanes + C::kOCol + o * R + cb;
-                                        tmem_ld32(at, xr);
-                                        tmem_wait32(xr);
+                                    for (int o = 0; o < 2 * C::kHalves; o++) {        // halves of the columns, dimensions
+                                        const uint32_t at = tmem + lanes + C::kOCol + (o >> 1) * R + cb + 16 * (o & 1);
+                                        uint32_t half[16];
+                                        tmem_ld16(at, half);
+                                        tmem_ld_wait(half);
 #pragma unroll
-                                        for (int i = 0; i < 16; i++) {
-                                            float z0, z1;
-                                            f2_unpack(f2_mul(f2_pack(__uint_as_float(xr[2 * i]), __uint_as_float(xr[2 * i + 1])), fac(i)),
-                                                      z0, z1);
-                                            xr[2 * i] = __float_as_uint(z0);
-                                            xr[2 * i + 1] = __float_as_uint(z1);
-                                        }
-                                        tmem_st32(at, xr);
+                                        for (int i = 0; i < 16; i++)
+                                            half[i] = __float_as_uint(__uint_as_float(half[i]) * s_fac[cb + 16 * (o & 1) + i]);
+                                        tmem_st16(at, half);
                                     }
                                     tmem_st_wait();
                                 }
