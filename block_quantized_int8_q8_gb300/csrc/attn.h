@@ -84,6 +84,10 @@ struct AttnArgs {
     // split along the cache, or a part longer than kChain: sums of rows [split][row] (row = token * heads + head)
     float* part_o;             // [splits][rows][dim], not divided by the denominator
     float2* part_ml;           // [splits][rows]: running maximum (log2) and denominator
+    // a tree of drafted tokens (the few-row kernel): null masks where there is none; words of a row of masks
+    const int32_t* depths;
+    const uint32_t* masks;
+    int words;
 };
 // Most tokens that the tiled kernel sums in one go.
 constexpr int kChain = 32768;
@@ -96,8 +100,10 @@ struct AttnPlan {
     int window;                // 0 where the asked one hides nothing: what the kernels are given
     size_t part_o, part_ml, total;     // workspace offsets and size
 };
+// Most rows (new tokens x query heads) of a key/value head that the few-row kernel takes at once, and by itself.
+constexpr int kFewRows = 16;
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                        long long max_kv, long long window);
+                        long long max_kv, long long window, long long few_rows = kFewRows);
 cudaError_t run_attention_few(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,
                               cudaStream_t s);
 cudaError_t run_attention_tiled(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,

@@ -131,12 +131,12 @@ namespace mmq {
 // so that the workspace does not depend on it.  One that no sequence outgrows hides nothing and is none: the largest
 // values of its type, a common way to ask for none, take no part in any sum.
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                        long long max_kv, long long window) {
+                        long long max_kv, long long window, long long few_rows) {
     AttnPlan p{};
     constexpr long long SMS = 152;
     const long long rows = max_tokens * (heads / kv_heads);
-    p.few = rows <= 16;
-    const long long pairs = (long long)seqs * kv_heads, granule = p.few ? 64 : 128;
+    p.few = rows <= few_rows;
+    const long long pairs = (long long)seqs * kv_heads * (p.few ? (rows + kFewRows - 1) / kFewRows : 1), granule = p.few ? 64 : 128;
     auto cut = [&](long long range) {                         // tokens of a part
         if (p.few) {
             const long long slots = few_blocks(dim, rows <= 8 ? 1 : 2) * SMS, want = (slots + pairs - 1) / pairs;
@@ -174,6 +174,46 @@ AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int 
     p.total = off;
     return p;
 }
+
+namespace {
+
+AttnArgs attention_args(const mmq_heads* q, int n_heads, const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens,
+                        int64_t max_tokens, int64_t max_kv_len, float scale, int causal, const AttnPlan& p,
+                        const mmq_heads* out, float* lse, void* workspace) {
+    AttnArgs a{};
+    a.q = rows_of(q);
+    a.out = rows_of(out);
+    a.c = cache_of(cache);
+    a.sq = seqs_of(seqs, tokens);
+    a.heads = n_heads;
+    a.group = n_heads / cache->kv_heads;
+    a.max_tokens = (int)max_tokens;
+    a.max_kv = (int)max_kv_len;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.window = p.window;
+    a.lse = lse;
+    if (p.total > 0) {
+        a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_ml);
+        a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_o);
+    }
+    return a;
+}
+
+// Which of the two kernels a tree's rows take: the few-row kernel where 16 rows are all, which the tiles of 64 leave mostly
+// empty, and for small problems, since its blocks start and end sooner (16 rows at a time, each reading the cache again).
+// Measured, microseconds few-row / tiles, 8 key/value heads of 128 unless stated:
+//   16 rows or fewer: 64 sequences of 2000: 71 / 108 (8 rows), 89 / 108 (16); 16 of 8192: 71 / 87, 85 / 86; one of 65536: 42 / 56;
+//     32 heads of 64, 16 of 2000: 44 / 83, 55 / 85; 4 heads of 256, 16 of 4000: 58 / 57, 60 / 58
+//   more, by bytes read of K: 2 MB (one of 300, 104 rows) 17 / 26, 4 MB (one of 2000, 32 rows) 18 / 24, 8 MB (4 of 1000, 4 heads of
+//     256, 32 rows) 24 / 30, 11 MB (4 of 300, 128 rows) 27 / 30, 16 MB (4 of 2000, 32 rows) 30 / 28, 33 MB (4 of 2000, 64 rows)
+//     38 / 30, 44 MB (16 of 300, 128 rows) 42 / 35, 67 MB (one of 8192, 128 rows) 53 / 38.
+bool tree_few(int group, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
+    const long long rows = max_tokens * group, reads = (rows + kFewRows - 1) / kFewRows;
+    return rows <= kFewRows || (double)seqs * kv_heads * reads * (max_kv + max_tokens) * dim <= 13e6;
+}
+
+}  // namespace
 
 }  // namespace mmq
 
@@ -280,23 +320,7 @@ mmq_status mmq_attention(const mmq_heads* q, int n_heads, const mmq_kv_cache* ca
                                                       max_tokens, max_kv_len);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MMQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
-    AttnArgs a{};
-    a.q = rows_of(q);
-    a.out = rows_of(out);
-    a.c = cache_of(cache);
-    a.sq = seqs_of(seqs, tokens);
-    a.heads = n_heads;
-    a.group = n_heads / cache->kv_heads;
-    a.max_tokens = (int)max_tokens;
-    a.max_kv = (int)max_kv_len;
-    a.scale = scale;
-    a.causal = causal != 0;
-    a.window = p.window;
-    a.lse = lse;
-    if (p.total > 0) {
-        a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.part_ml);
-        a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_o);
-    }
+    const AttnArgs a = attention_args(q, n_heads, cache, seqs, tokens, max_tokens, max_kv_len, scale, causal, p, out, lse, workspace);
     cudaStream_t s = stream_of(stream);
     cudaError_t e = p.few ? run_attention_few(cache->head_dim, q->dtype, out->dtype, a, p, s)
                           : run_attention_tiled(cache->head_dim, q->dtype, out->dtype, a, p, s);
@@ -339,6 +363,8 @@ size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_he
         return 0;
     if (max_tokens > tokens) max_tokens = tokens;
     if (max_tokens > MMQ_MAX_DRAFT) return 0;
+    if (tree_few(n_heads / kv_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len))
+        return attention_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len, 0, kMaxDim).total;
     const TreePlan p = tree_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
     return p.fits ? p.total : 0;
 }
@@ -366,10 +392,26 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     if (!tree->masks || (windowed && !tree->depths)) return MMQ_ERR_INVALID_ARG;
     if (tree->mask_words < (max_tokens + 31) / 32 || tree->mask_words * tokens > kMaxDim) return MMQ_ERR_SHAPE;
     if (!aligned16(tree->masks) || !aligned16(tree->depths)) return MMQ_ERR_ALIGN;
+    const int group = n_heads / cache->kv_heads;
+    const bool few = tree_few(group, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
     const TreePlan p = tree_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
-    if (!p.fits) return MMQ_ERR_SHAPE;
-    if (!workspace || workspace_bytes < p.total) return MMQ_ERR_WORKSPACE;
+    if (!few && !p.fits) return MMQ_ERR_SHAPE;
+    const size_t need = mmq_attention_tree_workspace_bytes(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs,
+                                                           max_tokens, max_kv_len);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MMQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
+    cudaStream_t s = stream_of(stream);
+    if (few) {
+        const AttnPlan fp = attention_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len,
+                                           windowed ? window : 0, kMaxDim);
+        AttnArgs a = attention_args(q, n_heads, cache, seqs, tokens, max_tokens, max_kv_len, scale, 1, fp, out, lse, workspace);
+        a.depths = tree->depths;
+        a.masks = tree->masks;
+        a.words = tree->mask_words;
+        cudaError_t e = run_attention_few(cache->head_dim, q->dtype, out->dtype, a, fp, s);
+        if (e == cudaSuccess && fp.splits > 1) e = run_attention_join(cache->head_dim, out->dtype, a, fp, s);
+        return done(e, "mmq_attention_tree");
+    }
     TreeArgs a{};
     a.q = rows_of(q);
     a.out = rows_of(out);
@@ -379,13 +421,13 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     a.masks = tree->masks;
     a.words = tree->mask_words;
     a.heads = n_heads;
-    a.group = n_heads / cache->kv_heads;
+    a.group = group;
     a.max_tokens = (int)max_tokens;
     a.max_kv = (int)max_kv_len;
     a.scale = scale;
     a.window = windowed ? (int)window : 0;
     a.lse = lse;
-    return done(run_attention_tree(cache->head_dim, q->dtype, out->dtype, a, p, workspace, stream_of(stream)),
+    return done(run_attention_tree(cache->head_dim, q->dtype, out->dtype, a, p, workspace, s),
                 "mmq_attention_tree");
 }
 

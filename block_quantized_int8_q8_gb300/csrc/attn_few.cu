@@ -81,7 +81,8 @@ __device__ __forceinline__ void store_out4(void* p, long long at, const float (&
     else store4(static_cast<__half*>(p) + at, v);
 }
 
-template <int D, int NT>
+// TREE: the new tokens are the nodes of a tree, and a row sees those that its mask says.
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(const AttnArgs a, int chunk, int splits, int row_blocks,
                                                           int qt, int ot) {
     pdl_wait();
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
     const int i0 = r0 / a.group, i1 = (r0 + rows - 1) / a.group;      // new tokens of the first and the last row
     // tiles of this part that some row of the block sees
     int t_begin = rg.tile0 + split * (chunk / 16), t_end = rg.tile0 + min(rg.tiles, (split + 1) * (chunk / 16));
-    if (a.causal) t_end = min(t_end, (min(end, first + i1 + 1) + 15) / 16);
-    if (a.window > 0) t_begin = max(t_begin, (first + i0 - a.window + 1) / 16);
+    if (a.causal) t_end = min(t_end, (min(end, first + (TREE ? n : i1 + 1)) + 15) / 16);
+    if (a.window > 0) t_begin = max(t_begin, (first + (TREE ? 0 : i0) - a.window + 1) / 16);
     // this warp's steps of U tiles: the first at t_begin + U warp, the next 4U on; lane i looks up the place and the scales
     // of the i-th of the warp's next 32 tiles
     const int blocks = a.c.page / a.c.block;
@@ -225,8 +226,9 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
             l[nt][e] = 0.f;
         }
     // tiles whose 16 tokens every row sees need no mask
-    const int lim_all = a.causal ? min(first + i0, end - 1) : end - 1;
-    const int low_all = a.window > 0 ? first + i1 - a.window + 1 : 0;
+    const int lim_all = a.causal ? min(first + (TREE ? -1 : i0), end - 1) : end - 1;
+    const int low_all = a.window > 0 ? first + (TREE ? a.max_tokens - 1 : i1) - a.window + 1 : 0;
+    const int lim_new = min(end, first + n);                  // past the new tokens
     float o[D / 16][NT][4];
 #pragma unroll
     for (int i = 0; i < D / 16; i++)
@@ -279,10 +281,21 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                     sc[u][nt][2 + e] = fmaf(sc[u][nt][2 + e], f, b.y);
                     if (masked) {
                         const int at = (r0 + min(8 * nt + 2 * t + e, rows - 1)) / a.group;   // new token of the row
-                        const int lim = a.causal ? min(first + at, end - 1) : end - 1;
-                        const int low = a.window > 0 ? first + at - a.window + 1 : 0, j = tok + 16 * u + g;
-                        if (j > lim || j < low) sc[u][nt][e] = -INFINITY;
-                        if (j + 8 > lim || j + 8 < low) sc[u][nt][2 + e] = -INFINITY;
+                        const int j = tok + 16 * u + g;
+                        if constexpr (TREE) {
+                            const uint32_t* mask = a.masks + (long long)(q.n0 + at) * a.words;
+                            const int low = a.window > 0 ? first + a.depths[q.n0 + at] - a.window + 1 : 0;
+                            auto hidden = [&](int j) {
+                                return j >= lim_new || (j < first ? j < low : !(mask[(j - first) / 32] >> ((j - first) % 32) & 1u));
+                            };
+                            if (hidden(j)) sc[u][nt][e] = -INFINITY;
+                            if (hidden(j + 8)) sc[u][nt][2 + e] = -INFINITY;
+                        } else {
+                            const int lim = a.causal ? min(first + at, end - 1) : end - 1;
+                            const int low = a.window > 0 ? first + at - a.window + 1 : 0;
+                            if (j > lim || j < low) sc[u][nt][e] = -INFINITY;
+                            if (j + 8 > lim || j + 8 < low) sc[u][nt][2 + e] = -INFINITY;
+                        }
                     }
                     grow |= fmaxf(sc[u][nt][e], sc[u][nt][2 + e]) > m[nt][e] + LAZY;
                 }
@@ -525,13 +538,13 @@ __global__ void __launch_bounds__(kJoinThreads<W>) join_kernel(const AttnArgs a,
     if (lane == 0 && a.lse) a.lse[row] = den == 0.f ? -INFINITY : LN2 * (mx + log2f(den));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 cudaError_t launch_few(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     const int row_blocks = (a.max_tokens * a.group + 8 * NT - 1) / (8 * NT);
     const long long grid = (long long)a.sq.seqs * a.c.heads * p.splits * row_blocks;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     constexpr int bytes = FewSmem<D, NT>::kBytes;
-    auto kern = few_kernel<D, NT>;
+    auto kern = few_kernel<D, NT, TREE>;
     static bool configured[64] = {};
     bool& done = device_flag(configured);
     if (!done) {
@@ -545,7 +558,9 @@ cudaError_t launch_few(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const Attn
 
 template <int D>
 cudaError_t launch_few_rows(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
-    return a.max_tokens * a.group <= 8 ? launch_few<D, 1>(qt, ot, a, p, s) : launch_few<D, 2>(qt, ot, a, p, s);
+    const bool one = a.max_tokens * a.group <= 8;
+    if (a.masks) return one ? launch_few<D, 1, true>(qt, ot, a, p, s) : launch_few<D, 2, true>(qt, ot, a, p, s);
+    return one ? launch_few<D, 1, false>(qt, ot, a, p, s) : launch_few<D, 2, false>(qt, ot, a, p, s);
 }
 
 template <int D>

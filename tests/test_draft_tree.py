@@ -9,6 +9,7 @@ Tolerances:
                <= vmax, 2^-16 of vmax for queries and scores, half a step of the output type; lse 2^-18 + 2^-20 |lse|.
 """
 import math
+import sys
 
 import pytest
 import torch
@@ -206,6 +207,20 @@ def ref_tree_attention(q, cache, table, lens, n, masks, scale, window):
     return out, lse, vmax
 
 
+@pytest.fixture(params=["close", "loose"])
+def bound(request, monkeypatch):
+    """Which kernel takes the rows depends on the bounds of the lengths: with a loose one, short sequences take the one that
+    long ones take."""
+    monkeypatch.setattr(sys.modules[__name__], "BOUND", 1 << 18 if request.param == "loose" else None)
+
+
+BOUND = None
+
+
+def top(lens):
+    return BOUND or max(lens)
+
+
 def check(past, n, Hq, H, D, page=64, block=16, qt=torch.bfloat16, ot=torch.float32, window=0, scale=None, kind="any",
           spread=1.0, tamper=None, seed=0, no_cu=False, **more):
     lens = [max(a + b, 0) for a, b in zip(past, n)]
@@ -218,7 +233,7 @@ def check(past, n, Hq, H, D, page=64, block=16, qt=torch.bfloat16, ot=torch.floa
     scale = D ** -0.5 if scale is None else scale
     want, wlse, vmax = ref_tree_attention(q, cache, table, lens, n, [sees(p) for p in parents], scale, window)
     api.read_device_errors()
-    out, lse = api.attention(q.cuda(), cache, table.cuda(), i32(lens), max_kv_len=more.pop("max_kv_len", max(lens)),
+    out, lse = api.attention(q.cuda(), cache, table.cuda(), i32(lens), max_kv_len=top(lens),
                              cu_tokens=None if no_cu else offsets(n).cuda(), max_tokens=max(n), scale=scale,
                              window=window, out_dtype=ot, return_lse=True, tree=make_tree(parents, n), **more)
     tol = vmax * (2.0 ** -11 + 2.0 ** -16 + ULP[ot])
@@ -236,6 +251,7 @@ SHAPES = [(4, 4, 64, 16, 16), (8, 2, 128, 64, 16), (7, 1, 128, 32, 32), (16, 1, 
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("Hq,H,D,page,block", SHAPES)
 @pytest.mark.parametrize("past,n", [([0], [1]), ([0], [5]), ([1, 15, 16, 17], [1, 2, 3, 4]), ([127, 128, 129], [1, 9, 30]),
                                     ([100, 255, 0, 250], [28, 1, 64, 26]), ([700, 64, 0], [40, 129, 70]),
@@ -245,6 +261,7 @@ def test_attention(Hq, H, D, page, block, past, n):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("kind", ["forest", "path", "star", "apart"])
 def test_attention_kinds_of_trees(kind):
     check([130, 0, 61], [33, 12, 97], 8, 2, 128, kind=kind)
@@ -260,12 +277,15 @@ def test_attention_split_along_the_cache(D, past, n):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 def test_attention_of_many_sequences():
     g = torch.Generator().manual_seed(5)
     n = torch.randint(0, 6, (1300,), generator=g).tolist()
     past = torch.randint(0, 40, (1300,), generator=g).tolist()
     check(past, n, 4, 2, 64, 16, 16)
+    check(past, n, 16, 2, 64, 16, 16)
     check([3] * 600, [1] * 600, 2, 1, 128, 16, 16, no_cu=True)
+    check([3] * 600, [1] * 600, 20, 1, 128, 16, 16, no_cu=True)
 
 
 @gpu
@@ -275,6 +295,7 @@ def test_attention_of_the_largest_trees():
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("window", [64, 70, 100, 300, 5000])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_window(window, D):
@@ -282,6 +303,7 @@ def test_attention_window(window, D):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_rows_without_a_place(D):
     """Sequences shorter than their new tokens: the first tokens have no place, rows that see only these see nothing."""
@@ -290,6 +312,7 @@ def test_attention_rows_without_a_place(D):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("qt", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("ot", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("n", [[2, 3], [70, 20]])
@@ -298,6 +321,7 @@ def test_attention_types(qt, ot, n):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("n", [[2, 1], [3, 100]])
 def test_attention_sharp_rows_and_scales(n):
     """Scores far apart, queries of extreme bf16 magnitude, zero value blocks, scales of many magnitudes."""
@@ -318,6 +342,7 @@ def test_attention_sharp_rows_and_scales(n):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_reference_that_grows_late(D):
     """Keys whose scores rise along the cache, so that the running reference is raised again and again."""
@@ -332,6 +357,7 @@ def test_attention_reference_that_grows_late(D):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("n", [[2, 3], [30, 100]])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_ignores_what_lies_past_the_length(n, D):
@@ -341,7 +367,7 @@ def test_attention_ignores_what_lies_past_the_length(n, D):
     cache, table = make_cache(g, lens, 2, D, 64, 16)
     q = torch.randn(sum(n), 8, D, generator=g).bfloat16().cuda()
     tree = make_tree([draw_parents(k, g) for k in n], n)
-    args = (i32(lens), max(lens), offsets(n).cuda(), max(n))
+    args = (i32(lens), top(lens), offsets(n).cuda(), max(n))
     first = api.attention(q, cache, table.cuda(), *args, tree=tree)
     used = torch.zeros(cache.pages, 64, dtype=torch.bool)
     for i, L in enumerate(lens):
@@ -387,17 +413,17 @@ def test_attention_strided_rows_streams_and_workspace(n):
 
 
 @gpu
-@pytest.mark.parametrize("n", [2, 60])
-def test_attention_flags_lengths_pages_and_offsets(n):
+@pytest.mark.parametrize("n,Hq,H,D", [(2, 4, 1, 64), (60, 4, 1, 64), (100, 32, 8, 256)])
+def test_attention_flags_lengths_pages_and_offsets(n, Hq, H, D):
     g = torch.Generator().manual_seed(2)
-    cache, table = make_cache(g, [300], 1, 64, 64, 16)
-    q = torch.randn(n, 4, 64, generator=g).bfloat16().cuda()
+    cache, table = make_cache(g, [300], H, D, 64, 16)
+    q = torch.randn(n, Hq, D, generator=g).bfloat16().cuda()
     tree = make_tree([draw_parents(n, g)], [n])
     cu, kv = i32([0, n]), i32([300])
     api.read_device_errors()
     api.attention(q, cache, table.cuda(), kv, 200, cu, n, tree=tree)
     assert api.read_device_errors() == api.DEVERR_LENGTH
-    out = torch.full((n, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((n, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
     api.attention(q, cache, table.cuda(), kv, 300, cu, n - 1, out=out, tree=tree)         # one token more than stated
     assert api.read_device_errors() == api.DEVERR_LENGTH
     assert (out[n - 1:] == 7).all() and (out[:n - 1] != 7).any(-1).all()
@@ -410,12 +436,13 @@ def test_attention_flags_lengths_pages_and_offsets(n):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 def test_attention_of_a_path_is_causal_attention():
     g = torch.Generator().manual_seed(8)
     n, lens = [5, 33, 1], [800, 33, 400]
     cache, table = make_cache(g, lens, 2, 128, 64, 16)
     q = torch.randn(sum(n), 8, 128, generator=g).bfloat16().cuda()
-    args = (q, cache, table.cuda(), i32(lens), max(lens), offsets(n).cuda(), max(n))
+    args = (q, cache, table.cuda(), i32(lens), top(lens), offsets(n).cuda(), max(n))
     a, la = api.attention(*args, out_dtype=torch.float32, return_lse=True)
     b, lb = api.attention(*args, out_dtype=torch.float32, return_lse=True,
                           tree=make_tree([draw_parents(k, g, "path") for k in n], n))
