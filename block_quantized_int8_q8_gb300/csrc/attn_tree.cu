@@ -35,6 +35,20 @@ constexpr int N = 32;                        // columns of a softmax group
 constexpr int WINDOW = kChain / KT;          // most tiles that are listed, and summed, in one go
 constexpr float UNSET = 1e30f;               // -m of a row that has seen nothing yet
 
+// The lowest n bits; none for a negative n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
+
+// Bit c of lane r becomes bit r of lane c: squares off the diagonal change places, ever smaller ones.
+__device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
+    uint32_t m = 0x0000FFFFu;
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1, m ^= m << j) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+        x = lane & j ? (x & ~m) | (y & ~m) >> j : (x & m) | (y & m) << j;
+    }
+    return x;
+}
+
 template <int D, int R> struct Tree {
     // warps of the converters and the products, after those of the softmax
     static constexpr int kGroups = R / N, kSoftmaxWarps = 4 * kGroups, kWarpsV = R == 128 ? 3 : 7;
@@ -759,22 +773,19 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < N / 32; b++) see[b] = 0xFFFFFFFFu;
                     if (__builtin_expect(masked && busy, 0)) {
-                        const int j = p.tok0 + (y - (y_end - p.tiles)) * KT + tk, d = j - p.first;
+                        // lane c: what column c sees of the warp's 32 tokens, which start d0 past the cached ones; then turned
+                        // over, so that a token has its columns
+                        const int j0 = p.tok0 + (y - (y_end - p.tiles)) * KT + 32 * w, d0 = j0 - p.first;
+                        const uint32_t there = low_bits(p.lim - j0), cached = low_bits(-d0);
 #pragma unroll
                         for (int b = 0; b < N / 32; b++) {
-                            if (j >= p.lim) {
-                                see[b] = 0u;
-                            } else if (d >= 0) {
-                                see[b] = 0u;
-                                if (d / 32 < a.words)
-#pragma unroll 8
-                                    for (int i = 0; i < 32; i++)
-                                        see[b] |= (a.masks[(long long)s_tok[c0 + 32 * b + i] * a.words + d / 32] >> (d % 32) & 1u) << i;
-                            } else if (a.window > 0) {
-#pragma unroll 8
-                                for (int i = 0; i < 32; i++)
-                                    if (j < s_low[c0 + 32 * b + i]) see[b] &= ~(1u << i);
-                            }
+                            const int c = c0 + 32 * b + lane;
+                            const uint32_t* mask = a.masks + (long long)s_tok[c] * a.words;
+                            const int at = d0 >> 5;           // of d0's word
+                            const uint32_t lo = at >= 0 && at < a.words ? mask[at] : 0u, hi = at >= -1 && at + 1 < a.words ? mask[at + 1] : 0u;
+                            uint32_t x = __funnelshift_r(lo, hi, d0 & 31) & ~cached;
+                            x |= cached & ~(a.window > 0 ? low_bits(s_low[c] - j0) : 0u);
+                            see[b] = transpose32(x & there, lane);
                         }
                     }
                     ok = wait_for(bar.sfull(buf), (y / C::kBufs) & 1, abort_flag) && ok;
