@@ -84,7 +84,7 @@ struct AttnArgs {
     // split along the cache, or a part longer than kChain: sums of rows [split][row] (row = token * heads + head)
     float* part_o;             // [splits][rows][dim], not divided by the denominator
     float2* part_ml;           // [splits][rows]: running maximum (log2) and denominator
-    // a tree of drafted tokens (the few-row kernel): null masks where there is none; words of a row of masks
+    // a tree of drafted tokens: null masks where there is none; words of a row of masks
     const int32_t* depths;
     const uint32_t* masks;
     int words;
@@ -131,7 +131,7 @@ struct KeepArgs {
 };
 cudaError_t run_kv_keep(int dim, const KeepArgs& a, cudaStream_t s);
 
-// Attention of a tree's rows (attn_tree.cu).
+// Attention of 17 to 128 rows of a tree (head_dim 256: 64) over long texts (attn_tree.cu).
 struct TreeArgs {
     HeadRows q, out;
     CacheArgs c;
@@ -145,14 +145,14 @@ struct TreeArgs {
     int window;                // 0: none
     float* lse;
 };
-// How a problem is shared out: rows of a row block, ranges of the line of tiles, workspace offsets and size.
+// How a problem is shared out: rows that a tile has room for, workspace offsets and size.
 struct TreePlan {
-    int rows, ranges;
+    int rows;
     bool many_parts;           // a unit is cut into many
     bool fits;                 // positions in the line of tiles are 32-bit numbers
     size_t joins, part_ml, part_o, total;
 };
-TreePlan tree_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv);
+TreePlan tree_plan(int heads, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv);
 cudaError_t run_attention_tree(int dim, mmq_dtype qt, mmq_dtype ot, const TreeArgs& a, const TreePlan& p, void* workspace,
                                cudaStream_t s);
 

@@ -200,17 +200,33 @@ AttnArgs attention_args(const mmq_heads* q, int n_heads, const mmq_kv_cache* cac
     return a;
 }
 
-// Which of the two kernels a tree's rows take: the few-row kernel where 16 rows are all, which the tiles of 64 leave mostly
-// empty, and for small problems, since its blocks start and end sooner (16 rows at a time, each reading the cache again).
-// Measured, microseconds few-row / tiles, 8 key/value heads of 128 unless stated:
-//   16 rows or fewer: 64 sequences of 2000: 71 / 108 (8 rows), 89 / 108 (16); 16 of 8192: 71 / 87, 85 / 86; one of 65536: 42 / 56;
-//     32 heads of 64, 16 of 2000: 44 / 83, 55 / 85; 4 heads of 256, 16 of 4000: 58 / 57, 60 / 58
-//   more, by bytes read of K: 2 MB (one of 300, 104 rows) 17 / 26, 4 MB (one of 2000, 32 rows) 18 / 24, 8 MB (4 of 1000, 4 heads of
-//     256, 32 rows) 24 / 30, 11 MB (4 of 300, 128 rows) 27 / 30, 16 MB (4 of 2000, 32 rows) 30 / 28, 33 MB (4 of 2000, 64 rows)
-//     38 / 30, 44 MB (16 of 300, 128 rows) 42 / 35, 67 MB (one of 8192, 128 rows) 53 / 38.
-bool tree_few(int group, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
-    const long long rows = max_tokens * group, reads = (rows + kFewRows - 1) / kFewRows;
-    return rows <= kFewRows || (double)seqs * kv_heads * reads * (max_kv + max_tokens) * dim <= 13e6;
+// Which kernel a tree's rows take (microseconds below: 8 key/value heads of 128 unless stated, bounds that hold).
+// FEW, the few-row kernel: for 16 rows (32 of head_dim 64), of which tiles of 64 would leave most empty, and for small problems,
+//   whose blocks start and end sooner, 16 rows at a time, each reading the cache again.
+//   16 rows, few / tiles: 64 sequences of 2000: 89 / 108; 16 of 8192: 85 / 86; 32 heads of 64, 16 of 2000: 55 / 85
+//   (32 rows: 79 / 91); 4 heads of 256, 16 of 4000: 60 / 58.  More rows, few / tiled, by the bytes of K that are read: 8 MB (one
+//   of 2000, 64 rows) 20 / 24, 8 MB (4 of 1000, 32 rows) 26 / 28, 17 MB (16 of 500, 32 rows) 30 / 22, 17 MB (one of 2000, 128
+//   rows) 28 / 24.
+// TILED, the kernel of prompts: 256 rows (head_dim 256: 128) that share the converted codes.
+// TILES, the tree kernel: tiles of 64 or 128 rows in equal shares, which wins where they fill the card.  Tiles / tiled, by the
+//   bytes of K, up to 64 rows: 17 MB (16 of 1000) 36 / 29, 34 MB (64 of 500) 69 / 72, 50 MB (16 of 3000) 52 / 57, 135 MB (16 of
+//   8192) 95 / 126; up to 128: 34 MB (64 of 500) 81 / 73, 50 MB (16 of 3000) 65 / 59, 70 MB (32 heads of 64, 16 of 2000) 121 / 132,
+//   135 MB (64 of 2000) 142 / 149.  With two blocks of 128 (16 of 8192, 192 rows) 201 / 134.
+enum class TreeKernel { FEW, TILES, TILED };
+
+TreeKernel tree_kernel(int group, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
+    const long long rows = max_tokens * group;
+    const double bytes = (double)seqs * kv_heads * (max_kv + max_tokens) * dim;
+    if (rows <= (dim == 64 ? 32 : 16) || bytes * ((rows + kFewRows - 1) / kFewRows) <= 10e6) return TreeKernel::FEW;
+    if (rows <= 64) return bytes < 25e6 ? TreeKernel::TILED : TreeKernel::TILES;
+    return rows > 128 || dim == 256 || bytes < 60e6 ? TreeKernel::TILED : TreeKernel::TILES;
+}
+
+// The other kernels' plan.
+AttnPlan tree_attention_plan(TreeKernel kernel, long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
+                             long long max_kv, long long window) {
+    return attention_plan(tokens, heads, kv_heads, dim, seqs, max_tokens, max_kv, window,
+                          kernel == TreeKernel::FEW ? kMaxDim : 0);
 }
 
 }  // namespace
@@ -363,9 +379,10 @@ size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_he
         return 0;
     if (max_tokens > tokens) max_tokens = tokens;
     if (max_tokens > MMQ_MAX_DRAFT) return 0;
-    if (tree_few(n_heads / kv_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len))
-        return attention_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len, 0, kMaxDim).total;
-    const TreePlan p = tree_plan(tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
+    const TreeKernel kernel = tree_kernel(n_heads / kv_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
+    if (kernel != TreeKernel::TILES)
+        return tree_attention_plan(kernel, tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len, 0).total;
+    const TreePlan p = tree_plan(n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
     return p.fits ? p.total : 0;
 }
 
@@ -393,22 +410,23 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     if (tree->mask_words < (max_tokens + 31) / 32 || tree->mask_words * tokens > kMaxDim) return MMQ_ERR_SHAPE;
     if (!aligned16(tree->masks) || !aligned16(tree->depths)) return MMQ_ERR_ALIGN;
     const int group = n_heads / cache->kv_heads;
-    const bool few = tree_few(group, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
-    const TreePlan p = tree_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
-    if (!few && !p.fits) return MMQ_ERR_SHAPE;
+    const TreeKernel kernel = tree_kernel(group, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
+    const TreePlan p = tree_plan(n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len);
+    if (kernel == TreeKernel::TILES && !p.fits) return MMQ_ERR_SHAPE;
     const size_t need = mmq_attention_tree_workspace_bytes(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs,
                                                            max_tokens, max_kv_len);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MMQ_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
     cudaStream_t s = stream_of(stream);
-    if (few) {
-        const AttnPlan fp = attention_plan(tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens, max_kv_len,
-                                           windowed ? window : 0, kMaxDim);
+    if (kernel != TreeKernel::TILES) {
+        const AttnPlan fp = tree_attention_plan(kernel, tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens,
+                                                max_kv_len, windowed ? window : 0);
         AttnArgs a = attention_args(q, n_heads, cache, seqs, tokens, max_tokens, max_kv_len, scale, 1, fp, out, lse, workspace);
         a.depths = tree->depths;
         a.masks = tree->masks;
         a.words = tree->mask_words;
-        cudaError_t e = run_attention_few(cache->head_dim, q->dtype, out->dtype, a, fp, s);
+        cudaError_t e = fp.few ? run_attention_few(cache->head_dim, q->dtype, out->dtype, a, fp, s)
+                               : run_attention_tiled(cache->head_dim, q->dtype, out->dtype, a, fp, s);
         if (e == cudaSuccess && fp.splits > 1) e = run_attention_join(cache->head_dim, out->dtype, a, fp, s);
         return done(e, "mmq_attention_tree");
     }

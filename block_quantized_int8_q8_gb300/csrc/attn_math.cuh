@@ -72,4 +72,15 @@ __device__ __forceinline__ Range visible_range(const AttnArgs& a, const Seq& q, 
     return r;
 }
 
+// The lowest n bits; none for a negative n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
+// What a row of a tree sees of 32 tokens, the first of which comes d0 after the cached text: of the new tokens what its mask
+// says, of the cached ones those from the low-th of the 32 on; nothing from the there-th on.
+__device__ __forceinline__ uint32_t tree_sees(const uint32_t* mask, int words, int d0, int low, int there) {
+    const uint32_t cached = low_bits(-d0);
+    const int at = d0 >> 5;                                   // d0's word
+    const uint32_t lo = at >= 0 && at < words ? mask[at] : 0u, hi = at >= -1 && at + 1 < words ? mask[at + 1] : 0u;
+    return ((__funnelshift_r(lo, hi, d0 & 31) & ~cached) | (cached & ~low_bits(low))) & low_bits(there);
+}
+
 }  // namespace mmq

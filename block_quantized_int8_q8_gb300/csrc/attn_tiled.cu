@@ -156,8 +156,9 @@ struct TileSpan {
 };
 
 // PACKED: row blocks numbered through the packed rows instead of for every sequence the most that one has.
-// LONG: parts may be longer than kChain tokens, after which the sums are put aside.
-template <int D, bool PACKED, bool LONG>
+// LONG: parts may be longer than kChain tokens, after which the sums are put aside.  TREE: the new tokens are the nodes of a
+// tree, and a row sees those that its mask says.
+template <int D, bool PACKED, bool LONG, bool TREE>
 __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, int chunk, int slots, int qt, int ot) {
     using C = Tiled<D>;
     constexpr int KT = C::kTokens, NQ = C::kQTiles, ROWS = 128 * NQ;
@@ -206,8 +207,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         int lo = base, hi = min(stop, end);
         if (left > 0) {
             const int ta = first + (row0 + 128 * i) / a.group, tb = first + (row0 + 128 * i + left - 1) / a.group;
-            if (a.causal) hi = min(hi, tb + 1);
-            if (a.window > 0) lo = max(lo, ta - a.window + 1);
+            if (a.causal) hi = min(hi, TREE ? first + n : tb + 1);
+            if (a.window > 0) lo = max(lo, (TREE ? first : ta) - a.window + 1);
         } else {
             hi = lo;
         }
@@ -508,11 +509,11 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         // in the loop everything counts from the first tile: tiles kt, columns that the row sees, and the tiles that every
         // row of this warp sees whole and that need no mask
         const int b0 = base + j0 * KT, k_s = span[i].s - j0, k_e = span[i].e - j0;
-        const int lim = (!real ? -1 : (a.causal ? min(first + tokrow, end - 1) : end - 1)) - b0;
-        const int low = (a.window > 0 ? first + tokrow - a.window + 1 : 0) - b0;
+        const int lim = (!real ? -1 : (a.causal ? min(first + (TREE ? n - 1 : tokrow), end - 1) : end - 1)) - b0;
+        const int low = (a.window > 0 ? first + (TREE ? a.depths[tok] : tokrow) - a.window + 1 : 0) - b0;
         const int ra = min(row0 + (r & ~31), row0 + rows - 1), rz = min(row0 + (r | 31), row0 + rows - 1);
-        const int k_hi = max((a.causal ? min(first + ra / a.group, end - 1) : end - 1) - b0 + 1, 0) / KT;
-        const int k_lo = a.window > 0 ? (max(first + rz / a.group - a.window + 1 - b0, 0) + KT - 1) / KT : 0;
+        const int k_hi = max((a.causal ? min(first + (TREE ? -1 : ra / a.group), end - 1) : end - 1) - b0 + 1, 0) / KT;
+        const int k_lo = a.window > 0 ? (max(first + (TREE ? a.max_tokens - 1 : rz / a.group) - a.window + 1 - b0, 0) + KT - 1) / KT : 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + C::kOCol + i * D;
         // Tiles summed in one go, and the row's place for such sums (worked out where it is needed: the rows are hidden from
@@ -589,9 +590,20 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
             }
             if (masked) {
                 const int hi = lim - k * KT, lo = low - k * KT;
+                if constexpr (TREE) {
+                    const uint32_t* mask = a.masks + tok * a.words;
 #pragma unroll
-                for (int e = 0; e < KT; e++)
-                    if (e > hi || e < lo) x[e] = MASKED;
+                    for (int c = 0; c < KT; c += 32) {
+                        const uint32_t see = tree_sees(mask, a.words, b0 + k * KT + c - first, lo - c, hi + 1 - c);
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            if (!(see >> e & 1u)) x[c + e] = MASKED;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < KT; e++)
+                        if (e > hi || e < lo) x[e] = MASKED;
+                }
             }
             float top = -INFINITY;
 #pragma unroll
@@ -777,12 +789,12 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
     if (warp == T_MMA) tmem_dealloc(tmem, C::kCols);
 }
 
-template <int D, bool PACKED, bool LONG>
+template <int D, bool PACKED, bool LONG, bool TREE>
 cudaError_t launch_tiled(long long slots, long long blocks, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a,
                          const AttnPlan& p, cudaStream_t s) {
     const long long grid = blocks * a.c.heads * p.splits;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    auto kern = tiled_kernel<D, PACKED, LONG>;
+    auto kern = tiled_kernel<D, PACKED, LONG, TREE>;
     static bool configured[64] = {};
     bool& done = device_flag(configured);
     if (!done) {
@@ -806,8 +818,11 @@ cudaError_t launch_tiled_rows(mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, con
     // Parts that no sum has to be put aside in have a kernel without that code: prompts 306 us, 313 with it.
     const bool by_rows = a.sq.cu && all > 2 * packed, longer = p.chunk > kChain;
     const long long slots = by_rows ? packed : each, blocks = by_rows ? packed : all;
-    auto launch = by_rows ? (longer ? launch_tiled<D, true, true> : launch_tiled<D, true, false>)
-                          : (longer ? launch_tiled<D, false, true> : launch_tiled<D, false, false>);
+    auto launch = by_rows ? (longer ? launch_tiled<D, true, true, false> : launch_tiled<D, true, false, false>)
+                          : (longer ? launch_tiled<D, false, true, false> : launch_tiled<D, false, false, false>);
+    if (a.masks)
+        launch = by_rows ? (longer ? launch_tiled<D, true, true, true> : launch_tiled<D, true, false, true>)
+                         : (longer ? launch_tiled<D, false, true, true> : launch_tiled<D, false, false, true>);
     return launch(slots, blocks, qt, ot, a, p, s);
 }
 

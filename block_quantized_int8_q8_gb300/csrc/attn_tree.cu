@@ -3,23 +3,30 @@
 //   t_j = scale log2(e) ks_b (q . k_j) + log2(vs_b),  p_j = 2^(t_j - m),  O = sum_j p_j v_j,  l = sum_b (1/vs_b) sum_{j in b} p_j
 //   out = O / l,  lse = ln(2) (m + log2 l)                (the formulas of attn_few.cu) over the j that a row sees
 //
-// A tree has some ten to a hundred rows (tokens x query heads of a group) for each sequence and key/value head: too many for
-// mma.sync, and too few to fill the 128 lanes of a product whose rows they are.  So the products stand the other way round,
-// cache tokens and head dimensions on the 128 lanes and the query rows along the columns:
+// For 17 to 128 rows (tokens x query heads of a group) of a sequence and key/value head: too many for mma.sync, and too few to
+// fill the 128 lanes of a product whose rows they are, twice.  So the products stand the other way round, cache tokens and head
+// dimensions on the 128 lanes and the query rows along the columns, of which there are R = 64 or 128:
 //   S^T [128 tokens x R] = K Q^T       K: fp16 codes in TMEM (A operand), Q: shared memory, K-major
 //   O^T [128 dims x R]  += V^T P^T     V: shared memory [token][64 dims of 128 bytes], M-major, P the same way, N-major
-// A thread of the softmax then owns a token, with its scales in registers, and half of the rows; what it costs goes with
-// the rows that there are.  K never passes through shared memory, whose bandwidth is the next bound after the cache's.
+// A thread of the softmax then owns a token, with its scales in registers, and 32 of the rows; a group of rows that there are
+// not costs nothing.  K never passes through shared memory, whose bandwidth is the next bound after the cache's.
 //
-// One thread block an SM.  The cache tiles of all (sequence, head, row block) units stand in one line, and each block takes an
+// One thread block an SM.  The cache tiles of all (sequence, key/value head) units stand in one line, and each block takes an
 // equal share of it, wherever that begins and ends (lengths are on the device: the blocks work out the line by themselves);
 // units that are cut leave parts in the workspace, which a second launch joins.  Roles:
-//   * eight softmax warps in two groups, each half of the rows: a tile's S^T, the mask, the exponentials, P as fp16 to
-//     shared memory.  The reference m of a row is raised only when a term passes it by 2^LAZY, which a group votes on; then
-//     O is rescaled.  They also bring the queries in and the results out.
-//   * four warps turn the codes of K into fp16 in TMEM and seven those of V into shared memory, 32 tokens at
-//     a time; the next codes are on their way to the registers that the last ones leave.
-//   * one warp issues the products.
+//   * groups of four softmax warps, each 32 of the rows: a tile's S^T, the mask, the exponentials, P as fp16 to shared memory.
+//     The reference m of a row is raised only when a term passes it by 2^LAZY, which a group votes on; then O is rescaled.
+//     They also list the block's share, bring the queries in and the results out.
+//   * four warps turn the codes of K into fp16 in TMEM and seven (R = 128: three) those of V into shared memory, 32 tokens at
+//     a time; the next codes are on their way to the registers that the last ones leave, those after them to L2.
+//   * one warp issues the products, S up to kBufs tiles ahead.
+// Bound by the latencies between the roles and, next, by instructions: a tile of 128 tokens of heads of 128 takes a block 1170 ns
+// with 64 rows, where its codes take 737 at the rate of a plain copy; the converters alone take 896, the softmax alone 804, the
+// products alone 550.  With 128 rows: 1573; 1318, 1096, 657.  Some 15 us of a call are its start, the first codes and the join.
+// 16 sequences of 8192 tokens, 32 query and 8 key/value heads of 128: 87 us with 32 rows (3.1 TB/s), 93 with 64, 119 with 128
+// (0.55 PFLOP/s); one of 131072, 64 rows, 85; 4 key/value heads of 256, 16 of 4000, 64 rows, 60.
+// Slower: six warps for V (64 rows: 93 -> 102), eleven of fewer registers (96), eight for K (95); S of the next piece's
+// queries from a second buffer was not tried.  A share of tiles without the units' own cost: see EXTRA.
 #include <algorithm>
 #include <type_traits>
 #include "attn_device.cuh"
@@ -33,10 +40,8 @@ namespace {
 constexpr int KT = 128;                      // cache tokens of a tile
 constexpr int N = 32;                        // columns of a softmax group
 constexpr int WINDOW = kChain / KT;          // most tiles that are listed, and summed, in one go
+constexpr int RANGES = 152;                  // shares of the line of tiles: one a multiprocessor
 constexpr float UNSET = 1e30f;               // -m of a row that has seen nothing yet
-
-// The lowest n bits; none for a negative n.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
 
 // Bit c of lane r becomes bit r of lane c: squares off the diagonal change places, ever smaller ones.
 __device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
@@ -89,7 +94,7 @@ template <int D, int R> struct Tree {
 struct Piece {
     int s, head, n0;             // n0: first packed row of the sequence
     int first, lim;              // cached tokens before the new ones; tokens past lim do not exist
-    int row0, rows;
+    int rows;
     int tok0;                    // first token of the run
     int x0, tiles;
     int slot;                    // its place in the workspace
@@ -221,23 +226,20 @@ constexpr int EXTRA = 5;
 struct Line {
     Seq q;
     int n, base;                 // new tokens, first token of the first tile
-    int blocks;                  // row blocks
     int tiles;                   // of a unit
 };
-template <int R>
 __device__ __forceinline__ Line line_of(const TreeArgs& a, int s) {
     Line x;
     x.q = load_seq(a.sq, s, a.c.page);
     x.n = min(x.q.n, a.max_tokens);
     const int first = x.q.len - x.q.n, lim = min(min(x.q.end, a.max_kv), first + x.n);
     x.base = a.window > 0 ? max(first - a.window + 1, 0) / 16 * 16 : 0;
-    x.blocks = (x.n * a.group + R - 1) / R;
     x.tiles = max((lim - x.base + KT - 1) / KT, 1);
     return x;
 }
 
-// The line of tiles: every sequence's units one after the other, heads before row blocks, shared out evenly.  The host keeps
-// it below 2^30.
+// The line of tiles: every sequence's units (its key/value heads) one after the other, shared out evenly.  The host keeps it
+// below 2^30.
 struct LineShare {
     int w[32], u[32];            // of the scan
     int span[2];                 // first and last unit with tiles in the window
@@ -252,7 +254,7 @@ struct LineShare {
 
 // Lists the pieces of window `window` of this block's share; its first THREADS threads take part.  The first call works out
 // the line.
-template <int R, int THREADS>
+template <int THREADS>
 __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& work, LineShare& sh, Piece* pieces, int window) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = THREADS / 32, range = blockIdx.x;
     auto exclusive = [&](int w, int u, int& wx, int& ux, int& wall, int& uall) {
@@ -294,8 +296,8 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
         w = units = 0;
         x = Line{};
         if (s < a.sq.seqs) {
-            x = line_of<R>(a, s);
-            units = x.blocks * a.c.heads;
+            x = line_of(a, s);
+            units = x.n > 0 ? a.c.heads : 0;
             w = (EXTRA + x.tiles) * units;
         }
         exclusive(w, units, wx, ux, wall, uall);
@@ -334,13 +336,12 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
             sh.skip = max(tile0 - g, 0);
             if (window == 0) {
                 // The join of the unit that this range begins within, if the range before is the first with tiles of it.
-                const int head = k / x.blocks, row0 = (k - head * x.blocks) * R;
                 int parts = 0, slot0 = 0;
                 if (tile0 < g && tile0 >= sh.start(range - 1)) {
                     parts = sh.range_of(tile0 + x.tiles - 1) - (range - 1) + 1;
                     slot0 = 2 * (range - 1) + (tile0 > sh.start(range - 1));
                 }
-                work.joins[2 * range] = make_int4(x.q.n0, row0, min(x.n * a.group - row0, R), head);
+                work.joins[2 * range] = make_int4(x.q.n0, x.n * a.group, k, 0);
                 work.joins[2 * range + 1] = make_int4(parts, slot0, 2 * range, 0);
             }
         }
@@ -358,12 +359,11 @@ __device__ __forceinline__ void list_pieces(const TreeArgs& a, const TreeWork& w
                 if (hi <= lo) continue;
                 Piece p;
                 p.s = s;
-                p.head = k / x.blocks;
+                p.head = k;
                 p.n0 = x.q.n0;
                 p.first = first;
                 p.lim = min(min(x.q.end, a.max_kv), first + x.n);
-                p.row0 = (k - p.head * x.blocks) * R;
-                p.rows = min(x.n * a.group - p.row0, R);
+                p.rows = x.n * a.group;
                 p.tok0 = x.base + (lo - tile0) * KT;
                 p.x0 = x0;
                 p.tiles = hi - lo;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
         int y0 = 0, k0 = 0;                                   // tiles and pieces of the windows before
 #pragma unroll 1
         for (int window = 0;; window++) {
-            if constexpr (decltype(lists)::value) list_pieces<R, 32 * C::kSoftmaxWarps>(a, work, s_line, s_piece, window);
+            if constexpr (decltype(lists)::value) list_pieces<32 * C::kSoftmaxWarps>(a, work, s_line, s_piece, window);
             tc_fence_before();
             __syncthreads();
             tc_fence_after();
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 if (p.rows <= c0) return;
 #pragma unroll
                 for (int i = 0; i < N; i += RPP) {
-                    const int c = c0 + i + (w * 32 + lane) / LPR, row = p.row0 + min(c, p.rows - 1), m = lane % LPR;
+                    const int c = c0 + i + (w * 32 + lane) / LPR, row = min(c, p.rows - 1), m = lane % LPR;
                     const uint16_t* from = static_cast<const uint16_t*>(a.q.data) + (long long)(p.n0 + row / a.group) * a.q.ts +
                                            (long long)(p.head * a.group + row % a.group) * a.q.hs + 8 * m;
                     cp_async_16(sb + C::q_off + (m / 8) * (R * 128) + sw128_off(c, m % 8), from, c < p.rows ? 16 : 0);
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 const bool busy = p.rows > c0, more = k + 1 < pieces;
                 named_bar_sync(id, 128);                      // the last piece's values are read
                 if (gt < N) {
-                    const int c = c0 + gt, row = p.row0 + min(c, p.rows - 1), tok = p.n0 + row / a.group;
+                    const int c = c0 + gt, row = min(c, p.rows - 1), tok = p.n0 + row / a.group;
                     const bool real = c < p.rows;
                     s_neg[c] = real ? UNSET : -INFINITY;
                     s_m[c] = -INFINITY;
@@ -773,19 +773,13 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < N / 32; b++) see[b] = 0xFFFFFFFFu;
                     if (__builtin_expect(masked && busy, 0)) {
-                        // lane c: what column c sees of the warp's 32 tokens, which start d0 past the cached ones; then turned
-                        // over, so that a token has its columns
-                        const int j0 = p.tok0 + (y - (y_end - p.tiles)) * KT + 32 * w, d0 = j0 - p.first;
-                        const uint32_t there = low_bits(p.lim - j0), cached = low_bits(-d0);
+                        // lane c: what column c sees of the warp's 32 tokens; turned over, so that a token has its columns
+                        const int j0 = p.tok0 + (y - (y_end - p.tiles)) * KT + 32 * w;
 #pragma unroll
                         for (int b = 0; b < N / 32; b++) {
-                            const int c = c0 + 32 * b + lane;
-                            const uint32_t* mask = a.masks + (long long)s_tok[c] * a.words;
-                            const int at = d0 >> 5;           // of d0's word
-                            const uint32_t lo = at >= 0 && at < a.words ? mask[at] : 0u, hi = at >= -1 && at + 1 < a.words ? mask[at + 1] : 0u;
-                            uint32_t x = __funnelshift_r(lo, hi, d0 & 31) & ~cached;
-                            x |= cached & ~(a.window > 0 ? low_bits(s_low[c] - j0) : 0u);
-                            see[b] = transpose32(x & there, lane);
+                            const int c = c0 + 32 * b + lane, low = a.window > 0 ? s_low[c] - j0 : 0;
+                            see[b] = transpose32(tree_sees(a.masks + (long long)s_tok[c] * a.words, a.words, j0 - p.first, low, p.lim - j0),
+                                                 lane);
                         }
                     }
                     ok = wait_for(bar.sfull(buf), (y / C::kBufs) & 1, abort_flag) && ok;
@@ -920,9 +914,8 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                             const float inv = l == 0.f ? 0.f : 1.f / l;
                             keep *= inv;
                             add *= inv;
-                            const int row = p.row0 + c;
                             if (ok && a.lse)
-                                a.lse[(long long)s_tok[c] * a.heads + p.head * a.group + row % a.group] =
+                                a.lse[(long long)s_tok[c] * a.heads + p.head * a.group + c % a.group] =
                                     l == 0.f ? -INFINITY : LN2 * (m + log2f(l));
                         } else if (ok) {
                             *ml = make_float2(m, l);
@@ -983,8 +976,8 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, const 
     pdl_wait();
     const int4 parts = work.joins[2 * c + 1];
     if (parts.x == 0) return;
-    const int4 unit = work.joins[2 * c];                      // first packed row, row block, rows, head
-    if (row >= unit.z) return;
+    const int4 unit = work.joins[2 * c];                      // first token, rows, head
+    if (row >= unit.y) return;
     auto place = [&](int p) { return (long long)(p == 0 ? parts.y : parts.z + 2 * (p - 1)) * R + row; };
     float mx = -INFINITY;
     for (int p = lane; p < parts.x; p += 32) mx = fmaxf(mx, work.part_ml[place(p)].x);
@@ -1016,8 +1009,8 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, const 
             for (int e = 0; e < PER; e++) acc[e] += s_acc[u][lane + 32 * e];
         }
     }
-    const int r = unit.y + row, h = unit.w * a.group + r % a.group;
-    const long long tok = unit.x + r / a.group, at = tok * a.out.ts + h * a.out.hs + lane;
+    const int h = unit.z * a.group + row % a.group;
+    const long long tok = unit.x + row / a.group, at = tok * a.out.ts + h * a.out.hs + lane;
     const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
     for (int e = 0; e < PER; e++) {
@@ -1042,37 +1035,29 @@ cudaError_t launch_tree(mmq_dtype qt, mmq_dtype ot, const TreeArgs& a, const Tre
         if (e != cudaSuccess) return e;
         done = true;
     }
-    cudaError_t e = launch_pdl_smem(kern, dim3((unsigned)p.ranges), dim3(Tree<D, R>::kThreads), Tree<D, R>::alloc, s, a, work, (int)qt,
+    cudaError_t e = launch_pdl_smem(kern, dim3(RANGES), dim3(Tree<D, R>::kThreads), Tree<D, R>::alloc, s, a, work, (int)qt,
                                     (int)ot);
-    if (e != cudaSuccess || p.ranges == 1) return e;
+    if (e != cudaSuccess) return e;
     if (p.many_parts)
-        return launch_pdl(tree_join_kernel<D, 4>, dim3((unsigned)((p.ranges - 1) * R)), dim3(128), s, a, work, R, (int)ot);
-    return launch_pdl(tree_join_kernel<D, 1>, dim3((unsigned)((p.ranges - 1) * (R / 4))), dim3(128), s, a, work, R, (int)ot);
+        return launch_pdl(tree_join_kernel<D, 4>, dim3((unsigned)((RANGES - 1) * R)), dim3(128), s, a, work, R, (int)ot);
+    return launch_pdl(tree_join_kernel<D, 1>, dim3((unsigned)((RANGES - 1) * (R / 4))), dim3(128), s, a, work, R, (int)ot);
 }
 
 }  // namespace
 
-// Shares of the line of tiles: one a multiprocessor, but none below two tiles of what the bounds allow (a block's start
-// and the join cost more).
-TreePlan tree_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
-    constexpr long long SMS = 152, LEAST = 2;
+TreePlan tree_plan(int heads, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
     TreePlan p{};
-    const long long group = heads / kv_heads, rows = max_tokens * group;
-    p.rows = dim == 256 || rows <= 64 ? 64 : 128;
-    const long long each = seqs * ((rows + p.rows - 1) / p.rows), packed = tokens * group / p.rows + seqs;
-    const long long units = kv_heads * std::min(each, packed), tiles = std::max((max_kv + KT - 1) / KT, 1ll);
-    p.fits = (double)kv_heads * (double)each * (double)(EXTRA + tiles) < 1073741824.0;
-    if (!p.fits) return p;
-    const long long shares = (units * tiles + LEAST - 1) / LEAST;
-    p.ranges = (int)std::min(shares, SMS);
-    p.many_parts = units <= SMS / 8;
+    p.rows = max_tokens * (heads / kv_heads) <= 64 ? 64 : 128;
+    const long long units = (long long)kv_heads * seqs;
+    p.fits = (double)units * (double)(EXTRA + max_kv / KT + 1) < 1073741824.0;
+    p.many_parts = units <= RANGES / 8;
     size_t off = 0;
     p.joins = off;
-    off += ((size_t)p.ranges * 2 * sizeof(int4) + 255) & ~size_t(255);
+    off += ((size_t)RANGES * 2 * sizeof(int4) + 255) & ~size_t(255);
     p.part_ml = off;
-    off += ((size_t)p.ranges * 2 * p.rows * sizeof(float2) + 255) & ~size_t(255);
+    off += ((size_t)RANGES * 2 * p.rows * sizeof(float2) + 255) & ~size_t(255);
     p.part_o = off;
-    off += (size_t)p.ranges * 2 * p.rows * dim * sizeof(float);
+    off += (size_t)RANGES * 2 * p.rows * dim * sizeof(float);
     p.total = off;
     return p;
 }

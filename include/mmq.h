@@ -419,10 +419,10 @@ mmq_status mmq_kv_append_tree(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs
  * mmq_attention_tree -- mmq_attention where token i of a sequence's n new ones sees the cached positions j < kv_len - n and, of
  * the new tokens, those that its mask says.  With window > 0 it sees j > kv_len - n + depths[i] - window only; a window must
  * not hide a new token: one below max_tokens is refused (MMQ_ERR_UNSUPPORTED).  depths are used with a window only and may
- * be null without.  max_tokens is at most MMQ_MAX_DRAFT.  With rows = max_tokens * n_heads / kv_heads above 16,
- * seqs * kv_heads * ceil(rows / R) * (ceil(max_kv_len / 128) + 5) is below 2^30 (else MMQ_ERR_SHAPE and a size of 0); R is 64
- * up to 64 rows and for head_dim 256, else 128.  The other arguments, the arithmetic and its bounds are mmq_attention's; the
- * workspace is mmq_attention_tree_workspace_bytes(...) bytes (0: may be null).
+ * be null without.  max_tokens is at most MMQ_MAX_DRAFT.  With max_tokens * n_heads / kv_heads from 17 to 128,
+ * seqs * kv_heads * (max_kv_len / 128 + 6) is below 2^30 (else MMQ_ERR_SHAPE and a size of 0).  The other arguments, the
+ * arithmetic and its bounds are mmq_attention's; the workspace is mmq_attention_tree_workspace_bytes(...) bytes (0: may be
+ * null).
  */
 size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_heads, int head_dim, int seqs,
                                           int64_t max_tokens, int64_t max_kv_len);

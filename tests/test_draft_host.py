@@ -130,7 +130,7 @@ def test_workspace_sizes(lib):  # noqa: F811
 def test_line_of_tiles_is_bounded(lib):  # noqa: F811
     """What the kernel numbers with 32 bits: the bounds' tiles over all sequences and heads."""
     size = lib.mmq_attention_tree_workspace_bytes
-    big, most = 1 << 20, (1 << 30) // (16 * 8192) * 128 - 5 * 128
+    big, most = 1 << 20, ((1 << 30) // (16 * 8192) - 6) * 128
     for tokens, kv_heads, n, max_kv, fits in ((8192, 16, 8192, most - 128, True), (8192, 16, 8192, most, False),
                                                  (big, 64, big, 100000, False)):
         assert (size(tokens, kv_heads, kv_heads, 128, n, 32, max_kv) > 0) == fits

@@ -211,7 +211,7 @@ def ref_tree_attention(q, cache, table, lens, n, masks, scale, window):
 def bound(request, monkeypatch):
     """Which kernel takes the rows depends on the bounds of the lengths: with a loose one, short sequences take the one that
     long ones take."""
-    monkeypatch.setattr(sys.modules[__name__], "BOUND", 1 << 18 if request.param == "loose" else None)
+    monkeypatch.setattr(sys.modules[__name__], "BOUND", 1 << 20 if request.param == "loose" else None)
 
 
 BOUND = None
