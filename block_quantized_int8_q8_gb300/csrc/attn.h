@@ -100,10 +100,13 @@ struct AttnPlan {
     int window;                // 0 where the asked one hides nothing: what the kernels are given
     size_t part_o, part_ml, total;     // workspace offsets and size
 };
-// Most rows (new tokens x query heads) of a key/value head that the few-row kernel takes at once, and by itself.
+// Most rows (new tokens x query heads) of a key/value head that the few-row kernel takes at once.
 constexpr int kFewRows = 16;
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                        long long max_kv, long long window, long long few_rows = kFewRows);
+                        long long max_kv, long long window);
+// The same for the kernel that is asked for.
+AttnPlan attention_plan_of(bool few, long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
+                           long long max_kv, long long window);
 cudaError_t run_attention_few(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,
                               cudaStream_t s);
 cudaError_t run_attention_tiled(int dim, mmq_dtype qt, mmq_dtype ot, const AttnArgs& a, const AttnPlan& p,

@@ -131,11 +131,17 @@ namespace mmq {
 // so that the workspace does not depend on it.  One that no sequence outgrows hides nothing and is none: the largest
 // values of its type, a common way to ask for none, take no part in any sum.
 AttnPlan attention_plan(long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                        long long max_kv, long long window, long long few_rows) {
+                        long long max_kv, long long window) {
+    return attention_plan_of(max_tokens * (heads / kv_heads) <= kFewRows, tokens, heads, kv_heads, dim, seqs, max_tokens, max_kv,
+                             window);
+}
+
+AttnPlan attention_plan_of(bool few, long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
+                           long long max_kv, long long window) {
     AttnPlan p{};
     constexpr long long SMS = 152;
     const long long rows = max_tokens * (heads / kv_heads);
-    p.few = rows <= few_rows;
+    p.few = few;
     const long long pairs = (long long)seqs * kv_heads * (p.few ? (rows + kFewRows - 1) / kFewRows : 1), granule = p.few ? 64 : 128;
     auto cut = [&](long long range) {                         // tokens of a part
         if (p.few) {
@@ -220,13 +226,6 @@ TreeKernel tree_kernel(int group, int kv_heads, int dim, int seqs, long long max
     if (rows <= (dim == 64 ? 32 : 16) || bytes * ((rows + kFewRows - 1) / kFewRows) <= 10e6) return TreeKernel::FEW;
     if (rows <= 64) return bytes < 25e6 ? TreeKernel::TILED : TreeKernel::TILES;
     return rows > 128 || dim == 256 || bytes < 60e6 ? TreeKernel::TILED : TreeKernel::TILES;
-}
-
-// The other kernels' plan.
-AttnPlan tree_attention_plan(TreeKernel kernel, long long tokens, int heads, int kv_heads, int dim, int seqs, long long max_tokens,
-                             long long max_kv, long long window) {
-    return attention_plan(tokens, heads, kv_heads, dim, seqs, max_tokens, max_kv, window,
-                          kernel == TreeKernel::FEW ? kMaxDim : 0);
 }
 
 }  // namespace
@@ -381,7 +380,8 @@ size_t mmq_attention_tree_workspace_bytes(int64_t tokens, int n_heads, int kv_he
     if (max_tokens > MMQ_MAX_DRAFT) return 0;
     const TreeKernel kernel = tree_kernel(n_heads / kv_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
     if (kernel != TreeKernel::TILES)
-        return tree_attention_plan(kernel, tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len, 0).total;
+        return attention_plan_of(kernel == TreeKernel::FEW, tokens, n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len, 0)
+            .total;
     const TreePlan p = tree_plan(n_heads, kv_heads, head_dim, seqs, max_tokens, max_kv_len);
     return p.fits ? p.total : 0;
 }
@@ -419,8 +419,8 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
     if (!aligned16(workspace)) return MMQ_ERR_ALIGN;
     cudaStream_t s = stream_of(stream);
     if (kernel != TreeKernel::TILES) {
-        const AttnPlan fp = tree_attention_plan(kernel, tokens, n_heads, cache->kv_heads, cache->head_dim, seqs->seqs, max_tokens,
-                                                max_kv_len, windowed ? window : 0);
+        const AttnPlan fp = attention_plan_of(kernel == TreeKernel::FEW, tokens, n_heads, cache->kv_heads, cache->head_dim,
+                                              seqs->seqs, max_tokens, max_kv_len, windowed ? window : 0);
         AttnArgs a = attention_args(q, n_heads, cache, seqs, tokens, max_tokens, max_kv_len, scale, 1, fp, out, lse, workspace);
         a.depths = tree->depths;
         a.masks = tree->masks;

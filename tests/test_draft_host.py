@@ -1,11 +1,15 @@
 """Host-side checks of the boundary of the operators on a tree of drafted tokens (no GPU needed).  Arguments are refused before
 any CUDA call, so the pointers here are fake and never dereferenced."""
+import ctypes
+import random
 import struct
 
 import pytest
 
 from test_attention_host import (ALIGN, BF16, CACHE_AND_SEQS, F16, F32, FAKE, INVALID, SHAPE, UNSUPPORTED, WORKSPACE, cache,
                                  heads, lib, rotary, seqs)  # noqa: F401
+
+from test_attention_plan import Plan, device_parts
 
 from block_quantized_int8_q8_gb300 import api
 
@@ -137,6 +141,30 @@ def test_line_of_tiles_is_bounded(lib):  # noqa: F811
         if not fits:
             assert lib.mmq_attention_tree(heads(), kv_heads, cache(h=kv_heads), seqs(n=n), tree(), tokens, 32, max_kv, 0.1, 0,
                                           heads(), None, FAKE, 1 << 40, None) == SHAPE
+
+
+def test_parts_of_a_tree_fit_the_launch_and_the_workspace(lib):  # noqa: F811
+    """As test_attention_plan.py has it, for a tree's rows: many in the few-row kernel, few in the kernel of prompts."""
+    plan = getattr(lib, "_ZN3mmq17attention_plan_ofEbxiiiixxx")
+    plan.argtypes = [ctypes.c_bool, ctypes.c_int64] + [ctypes.c_int] * 4 + [ctypes.c_int64] * 3
+    plan.restype = Plan
+    rng = random.Random(4)
+    for _ in range(4000):
+        kv, dim, few = rng.choice([1, 2, 8]), rng.choice([64, 128, 256]), rng.random() < 0.5
+        heads, seqs = kv * rng.choice([1, 3, 4, 8, 32]), int(2 ** rng.uniform(0, 9))
+        most, max_kv = int(2 ** rng.uniform(0, 10)), int(2 ** rng.uniform(0, 18))
+        tokens = rng.randint(max(most, seqs), max(seqs * most, most, seqs))
+        window = rng.choice([0, 0, most, most + 16, max_kv // 2, max_kv, (1 << 63) - 1])
+        p, whole = (plan(few, tokens, heads, kv, dim, seqs, most, max_kv, w) for w in (window, 0))
+        assert p.few == few and p.total <= whole.total and p.chunk > 0 and p.chunk % 16 == 0
+        assert p.chunk <= 2048 if few else (p.total > 0) == (p.splits > 1 or p.chunk > 32768)
+        assert p.total > 0 or p.splits == 1
+        if p.total > 0:
+            rows = tokens * heads * p.splits
+            assert p.part_o >= rows * 8 and p.total - p.part_o >= rows * dim * 4
+        for length in {0, 1, max_kv - 1, max_kv, max_kv + 7, rng.randint(0, max_kv)}:
+            for n in {1, most, most + 3, rng.randint(1, most)}:
+                assert device_parts(max(length, 0), n, p.chunk, True, p.window, most, max_kv) <= p.splits
 
 
 def test_binding_refuses_what_it_cannot_pass(lib):  # noqa: F811
