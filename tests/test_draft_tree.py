@@ -269,6 +269,7 @@ def test_attention_kinds_of_trees(kind):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("past,n", [([5000, 150, 2311], [9, 20, 33]), ([9001], [26]), ([20011, 1025, 30], [3, 60, 140]),
                                     ([40000], [2])])
@@ -289,6 +290,74 @@ def test_attention_of_many_sequences():
 
 
 @gpu
+def test_attention_of_more_tiles_than_a_block_lists_at_once(monkeypatch):
+    """Units that lie across two lists of a block among them."""
+    monkeypatch.setattr(sys.modules[__name__], "BOUND", 1 << 20)
+    g = torch.Generator().manual_seed(9)
+    n = torch.randint(0, 4, (3300,), generator=g).tolist()
+    past = torch.randint(0, 500, (3300,), generator=g).tolist()
+    check(past, n, 16, 2, 64, 16, 16)
+
+
+@gpu
+@pytest.mark.usefixtures("bound")
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_of_one_large_tree_among_small_ones(D):
+    check([50] + [20] * 40, [300] + [1, 2] * 20, 8, 1, D, 16, 16)
+
+
+@gpu
+@pytest.mark.usefixtures("bound")
+@pytest.mark.parametrize("n", [3, 12, 40])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_rows_that_are_no_numbers_stay_alone(n, D):
+    """A row of NaN, of an infinity, of zeros, of the largest values: the other rows are what they are without them."""
+    g = torch.Generator().manual_seed(3)
+    cache, table = make_cache(g, [300], 2, D, 64, 16)
+    q = torch.randn(n, 8, D, generator=g).bfloat16()
+    tree = make_tree([draw_parents(n, g)], [n])
+    args = (cache, table.cuda(), i32([300]), top([300]), i32([0, n]), n)
+    want = api.attention(q.cuda(), *args, out_dtype=torch.float32, tree=tree)
+    vmax = float((cache.v.abs().amax((2, 3)) * cache.v_scale.amax(-1)).max())
+    for value in (float("nan"), float("inf"), -float("inf"), 0.0, 3.0e38):
+        x = q.clone()
+        x[1, 3, 5] = value
+        x[2, 6] = value
+        got = api.attention(x.cuda(), *args, out_dtype=torch.float32, tree=tree)
+        same = torch.ones(n, 8, dtype=torch.bool)
+        same[1, 3] = same[2, 6] = False
+        assert (got - want).abs()[same.cuda()].max() <= 2 * vmax * (2.0 ** -11 + 2.0 ** -16), value
+        if value == 0.0:
+            assert torch.isfinite(got).all()
+    assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.usefixtures("bound")
+def test_attention_two_calls_at_once():
+    g = torch.Generator().manual_seed(6)
+    calls = []
+    for lens, n, D in (([3000, 200, 900], 20, 128), ([5000, 77], 11, 64)):
+        cache, table = make_cache(g, lens, 2, D, 64, 16)
+        q = torch.randn(n * len(lens), 8, D, generator=g).bfloat16().cuda()
+        tree = make_tree([draw_parents(n, g) for _ in lens], [n] * len(lens))
+        calls.append((q, cache, table.cuda(), i32(lens), top(lens), offsets([n] * len(lens)).cuda(), n, tree))
+    want = [api.attention(*c[:-1], tree=c[-1]) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(8):
+        for c, st, o in zip(calls, streams, got):
+            with torch.cuda.stream(st):
+                o.append(api.attention(*c[:-1], tree=c[-1]))
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(w, x) for x in o)
+
+
+@gpu
+@pytest.mark.usefixtures("bound")
 def test_attention_of_the_largest_trees():
     check([100, 0], [1024, 1000], 2, 1, 64, 64, 16)
     check([1000], [1024], 3, 1, 128, 64, 64, kind="path")
@@ -390,6 +459,7 @@ def test_attention_ignores_what_lies_past_the_length(n, D):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 @pytest.mark.parametrize("n", [2, 50])
 def test_attention_strided_rows_streams_and_workspace(n):
     """Queries and outputs that are slices of wider rows, another stream, a caller's workspace: the same bits."""
@@ -400,13 +470,13 @@ def test_attention_strided_rows_streams_and_workspace(n):
     q = wide[:, 2:10]
     tree = make_tree([draw_parents(n, g), draw_parents(n, g)], [n, n])
     kv, cu, tb = i32(lens), offsets([n, n]).cuda(), table.cuda()
-    want = api.attention(q.contiguous(), cache, tb, kv, 3000, cu, n, tree=tree)
-    need = api.attention_tree_workspace_bytes(2 * n, 8, 2, 128, 2, n, 3000)
+    want = api.attention(q.contiguous(), cache, tb, kv, top(lens), cu, n, tree=tree)
+    need = api.attention_tree_workspace_bytes(2 * n, 8, 2, 128, 2, n, top(lens))
     ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
     out = torch.full((2 * n, 12, 128), 5.0, dtype=torch.bfloat16, device="cuda")
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
-    api.attention(q, cache, tb, kv, 3000, cu, n, out=out[:, 1:9], workspace=ws, stream=st, tree=tree)
+    api.attention(q, cache, tb, kv, top(lens), cu, n, out=out[:, 1:9], workspace=ws, stream=st, tree=tree)
     torch.cuda.current_stream().wait_stream(st)
     assert torch.equal(out[:, 1:9], want)
     assert (out[:, 0] == 5).all() and (out[:, 9:] == 5).all() and (ws[need:] == 0xFF).all()
@@ -604,6 +674,7 @@ def test_verification_steps(D, page, block):
 
 
 @gpu
+@pytest.mark.usefixtures("bound")
 def test_steps_in_a_graph():
     """A captured step replays while lengths, trees and paths change on the device."""
     g = torch.Generator().manual_seed(4)
@@ -616,13 +687,13 @@ def test_steps_in_a_graph():
     lens = i32([0] * S)
     q = torch.empty(S * n, Hq, D, dtype=torch.bfloat16, device="cuda")
     out = torch.empty(S * n, Hq, D, device="cuda")
-    ws = torch.empty(api.attention_tree_workspace_bytes(S * n, Hq, H, D, S, n, 700) + 16, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(api.attention_tree_workspace_bytes(S * n, Hq, H, D, S, n, top([700])) + 16, dtype=torch.uint8, device="cuda")
 
     def step():
         lens.add_(n)
         tree = api.draft_tree(parents, cu, n)
         api.kv_append(cache, rows[:, Hq:Hq + H], rows[:, Hq + H:], tb, lens, cu, cos, sin, q=rows[:, :Hq], q_out=q, tree=tree)
-        api.attention(q, cache, tb, lens, 700, cu, n, out=out, workspace=ws, tree=tree)
+        api.attention(q, cache, tb, lens, top([700]), cu, n, out=out, workspace=ws, tree=tree)
 
     def accept():
         api.kv_keep(cache, tb, lens, S * n, kept, counts, cu)
