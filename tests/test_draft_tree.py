@@ -317,18 +317,20 @@ def test_attention_rows_that_are_no_numbers_stay_alone(n, D):
     q = torch.randn(n, 8, D, generator=g).bfloat16()
     tree = make_tree([draw_parents(n, g)], [n])
     args = (cache, table.cuda(), i32([300]), top([300]), i32([0, n]), n)
-    want = api.attention(q.cuda(), *args, out_dtype=torch.float32, tree=tree)
     vmax = float((cache.v.abs().amax((2, 3)) * cache.v_scale.amax(-1)).max())
-    for value in (float("nan"), float("inf"), -float("inf"), 0.0, 3.0e38):
-        x = q.clone()
-        x[1, 3, 5] = value
-        x[2, 6] = value
-        got = api.attention(x.cuda(), *args, out_dtype=torch.float32, tree=tree)
-        same = torch.ones(n, 8, dtype=torch.bool)
-        same[1, 3] = same[2, 6] = False
-        assert (got - want).abs()[same.cuda()].max() <= 2 * vmax * (2.0 ** -11 + 2.0 ** -16), value
-        if value == 0.0:
-            assert torch.isfinite(got).all()
+    for small in (1.0, 2.0 ** -20):                           # small rows under a large scale: only the whole has to be in bounds
+        more = dict(scale=D ** -0.5 / small, out_dtype=torch.float32, tree=tree)
+        want = api.attention((q * small).cuda(), *args, **more)
+        for value in (float("nan"), float("inf"), -float("inf"), 0.0) + ((3.0e38,) if small == 1.0 else ()):
+            x = q * small
+            x[1, 3, 5] = value
+            x[2, 6] = value
+            got = api.attention(x.cuda(), *args, **more)
+            same = torch.ones(n, 8, dtype=torch.bool)
+            same[1, 3] = same[2, 6] = False
+            assert (got - want).abs()[same.cuda()].max() <= 2 * vmax * (2.0 ** -11 + 2.0 ** -16), (value, small)
+            if value == 0.0:
+                assert torch.isfinite(got).all()
     assert api.read_device_errors() == 0
 
 
