@@ -1,5 +1,6 @@
 // attn_few.cu -- attention of few query rows over the 8-bit paged cache: single new tokens (decode) and the few of a
-// verification step, up to 16 rows (new tokens x query heads) for each sequence and key/value head.
+// verification step, up to 16 rows (new tokens x query heads) for each sequence and key/value head.  Small problems of a tree
+// of drafted tokens come here with more rows, 16 to a block.
 //
 //   t_j = scale log2(e) ks_b (q . k_j) + log2(vs_b)      k_j, v_j: int8 codes, b the block of token j
 //   p_j = 2^(t_j - m),  O = sum_j p_j v_j,  l = sum_b (1/vs_b) sum_{j in b} p_j,  out = O / l,

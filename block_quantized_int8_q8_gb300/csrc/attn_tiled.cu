@@ -1,4 +1,5 @@
-// attn_tiled.cu -- attention of many query rows (prompts, chunks of prompts) over the 8-bit paged cache, on tcgen05.
+// attn_tiled.cu -- attention of many query rows (prompts, chunks of prompts, large trees of drafted tokens) over the 8-bit
+// paged cache, on tcgen05.
 //
 //   S = Q K^T (codes),  t_j = scale log2(e) ks_b S_j + log2(vs_b),  p_j = 2^(t_j - m),  O = sum_j p_j v_j (codes),
 //   l = sum_b (1/vs_b) sum_{j in b} p_j,  out = O / l      (the same formulas as attn_few.cu)
