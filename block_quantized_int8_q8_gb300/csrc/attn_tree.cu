@@ -23,10 +23,10 @@
 // Bound by the latencies between the roles and, next, by instructions: a tile of 128 tokens of heads of 128 takes a block 1170 ns
 // with 64 rows, where its codes take 737 at the rate of a plain copy; the converters alone take 896, the softmax alone 804, the
 // products alone 550.  With 128 rows: 1573; 1318, 1096, 657.  Some 15 us of a call are its start, the first codes and the join.
-// 16 sequences of 8192 tokens, 32 query and 8 key/value heads of 128: 87 us with 32 rows (3.1 TB/s), 93 with 64, 119 with 128
-// (0.55 PFLOP/s); one of 131072, 64 rows, 85; 4 key/value heads of 256, 16 of 4000, 64 rows, 60.
-// Slower: six warps for V (64 rows: 93 -> 102), eleven of fewer registers (96), eight for K (95); S of the next piece's
-// queries from a second buffer was not tried.  A share of tiles without the units' own cost: see EXTRA.
+// 16 sequences of 8192 tokens, 32 query and 8 key/value heads of 128: 85 us with 32 rows (3.2 TB/s), 91 with 64, 120 with 128
+// (0.55 PFLOP/s); one of 131072, 64 rows, 89; 4 key/value heads of 256, 16 of 4000, 64 rows, 58.
+// Slower: six warps for V (64 rows: 93 -> 102), eleven of fewer registers (96), eight for K (95).  Without any load of codes it
+// would take 89 instead of 91: what is left is between the conversion, the softmax and the products, not memory.
 #include <algorithm>
 #include <type_traits>
 #include "attn_device.cuh"
@@ -70,9 +70,10 @@ template <int D, int R> struct Tree {
     static constexpr int kVBytes = KT * D * 2, kQBytes = R * D * 2, kPBytes = KT * R * 2;
     static constexpr int kScaleSlots = 16;
     static constexpr int kKCols = D / 2;
-    // Tiles of K and V that the converters may be ahead: with two of each every wait of one role stops the others.
+    // Tiles of K and V that the converters may be ahead (16 sequences of 8192, 64 rows: four of V 94 us, three 91, two 91, two of
+    // each 93; 32 heads of 64, 16 of 2000, 64 rows: four 97, three 101; 64 sequences of 2000, 32 rows: 113, 115, 115, 118).
     static constexpr int kKStages = D == 64 ? 4 : (R == 64 && D == 128 ? 4 : 2);
-    static constexpr int kVStages = D == 64 ? 4 : (D == 128 ? (R == 64 ? 4 : 3) : 2);
+    static constexpr int kVStages = D == 64 ? 4 : (D == 128 ? 3 : 2);
     // Buffers of S and of P.  With two, S of a tile waits for the softmax two tiles before, and then for the products in
     // between (19 sequences of 8192, 64 rows: 104 us with two, 101 with three).
     static constexpr int kBufs = R == 64 && D <= 128 ? 3 : 2;
