@@ -508,6 +508,44 @@ def test_attention_flags_lengths_pages_and_offsets(n, Hq, H, D):
 
 
 @gpu
+@pytest.mark.parametrize("n", [5, 16])
+def test_attention_of_a_batch_flags_lengths_pages_and_offsets(n):
+    """As above, where the tiles of many sequences are shared out."""
+    g = torch.Generator().manual_seed(2)
+    S = 128
+    cache, table = make_cache(g, [300] * S, 8, 128, 64, 16)
+    q = torch.randn(S * n, 32, 128, generator=g).bfloat16().cuda()
+    tree = make_tree([draw_parents(n, g) for _ in range(S)], [n] * S)
+    tb, kv, cu = table.cuda(), i32([300] * S), offsets([n] * S).cuda()
+    api.read_device_errors()
+    want = api.attention(q, cache, tb, kv, 300, cu, n, tree=tree)
+    assert api.read_device_errors() == 0
+    api.attention(q, cache, tb, kv, 250, cu, n, tree=tree)
+    assert api.read_device_errors() == api.DEVERR_LENGTH
+    out = torch.full((S, n, 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    api.attention(q, cache, tb, kv, 300, cu, n - 1, out=out.view(S * n, 32, 128), tree=tree)     # one token more than stated
+    assert api.read_device_errors() == api.DEVERR_LENGTH
+    assert (out[:, n - 1] == 7).all() and (out[:, :n - 1] != 7).any(-1).all()
+    for last in (S * n - 1, S * n + 5):
+        wrong = cu.clone()
+        wrong[-1] = last
+        api.attention(q, cache, tb, kv, 300, wrong, n + 5, tree=tree)
+        assert api.read_device_errors() & api.DEVERR_LENGTH, last
+    fallen = cu.clone()
+    fallen[40] = 0
+    api.attention(q, cache, tb, kv, 300, fallen, n, tree=tree)
+    assert api.read_device_errors() & api.DEVERR_LENGTH
+    table[3, 1], table[77, 4] = -5, 2 ** 30
+    got = api.attention(q, cache, table.cuda(), kv, 300, cu, n, tree=tree)
+    assert api.read_device_errors() == api.DEVERR_PAGE and torch.isfinite(got.float()).all()
+    others = torch.ones(S, dtype=torch.bool)
+    others[3] = others[77] = False
+    vmax = float((cache.v.abs().amax((2, 3)) * cache.v_scale.amax(-1)).max())
+    diff = (got.float() - want.float()).view(S, -1).abs().amax(-1).cpu()
+    assert diff[others].max() <= vmax * (2 * (2.0 ** -11 + 2.0 ** -16) + 2.0 ** -7) and (diff[~others] > 0).all()
+
+
+@gpu
 @pytest.mark.usefixtures("bound")
 def test_attention_of_a_path_is_causal_attention():
     g = torch.Generator().manual_seed(8)
