@@ -134,6 +134,10 @@ struct KeepArgs {
 };
 cudaError_t run_kv_keep(int dim, const KeepArgs& a, cudaStream_t s);
 
+// Which kernel a tree's rows take (attn_api.cu): the few-row kernel, attn_tree.cu's, the kernel of prompts.
+enum class TreeKernel { FEW, TILES, TILED };
+TreeKernel tree_kernel(int group, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv);
+
 // Attention of 17 to 128 rows of a tree (head_dim 256: 64) over long texts (attn_tree.cu).
 struct TreeArgs {
     HeadRows q, out;

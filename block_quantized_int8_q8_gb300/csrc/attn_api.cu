@@ -206,6 +206,8 @@ AttnArgs attention_args(const mmq_heads* q, int n_heads, const mmq_kv_cache* cac
     return a;
 }
 
+}  // namespace
+
 // Which kernel a tree's rows take (microseconds below: 8 key/value heads of 128 unless stated, bounds that hold).
 // FEW, the few-row kernel: for 16 rows (32 of head_dim 64), of which tiles of 64 would leave most empty, and for small problems,
 //   whose blocks start and end sooner, 16 rows at a time, each reading the cache again.
@@ -218,8 +220,6 @@ AttnArgs attention_args(const mmq_heads* q, int n_heads, const mmq_kv_cache* cac
 //   bytes of K, up to 64 rows: 17 MB (16 of 1000) 36 / 29, 34 MB (64 of 500) 69 / 72, 50 MB (16 of 3000) 52 / 57, 135 MB (16 of
 //   8192) 95 / 126; up to 128: 34 MB (64 of 500) 81 / 73, 50 MB (16 of 3000) 65 / 59, 70 MB (32 heads of 64, 16 of 2000) 121 / 132,
 //   135 MB (64 of 2000) 142 / 149.  With two blocks of 128 (16 of 8192, 192 rows) 201 / 134.
-enum class TreeKernel { FEW, TILES, TILED };
-
 TreeKernel tree_kernel(int group, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
     const long long rows = max_tokens * group;
     const double bytes = (double)seqs * kv_heads * (max_kv + max_tokens) * dim;
@@ -227,8 +227,6 @@ TreeKernel tree_kernel(int group, int kv_heads, int dim, int seqs, long long max
     if (rows <= 64) return bytes < 25e6 ? TreeKernel::TILED : TreeKernel::TILES;
     return rows > 128 || dim == 256 || bytes < 60e6 ? TreeKernel::TILED : TreeKernel::TILES;
 }
-
-}  // namespace
 
 }  // namespace mmq
 

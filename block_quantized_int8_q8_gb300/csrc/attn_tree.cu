@@ -86,7 +86,7 @@ template <int D, int R> struct Tree {
     static constexpr int p_off = q_off + kQBytes;
     static constexpr int sc_off = p_off + kBufs * kPBytes;                           // float4 [slots][8]
     static constexpr int bar_off = sc_off + kScaleSlots * 8 * 16;
-    static constexpr int n_bars = 5 + 2 * (kBufs + kKStages + kVStages);
+    static constexpr int n_bars = 3 + 3 * kBufs + 2 * (kKStages + kVStages);
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int total = misc_off + 16, alloc = total + 1024;
     static_assert(alloc <= 232448 - (R == 64 ? 16 : 20) * 1024, "shared memory budget (the rest is static)");
@@ -205,18 +205,19 @@ template <int D, int R> struct TreeBars {
     using C = Tree<D, R>;
     uint32_t b;
     __device__ uint32_t rest(int i) const { return b + 8u * i; }
-    __device__ uint32_t pvdone(int i) const { return rest(i); }                  // of tiles i mod 2
-    __device__ uint32_t qfull() const { return rest(2); }                        // a piece's queries
-    __device__ uint32_t ofree() const { return rest(3); }                        // a piece's O is read
-    __device__ uint32_t done() const { return rest(4); }
-    // of tiles i mod kBufs; as products complete in their order, S of a tile shows that the product with V kBufs tiles before is
-    // complete
-    __device__ uint32_t sfull(int i) const { return rest(5 + i); }
-    __device__ uint32_t pready(int i) const { return rest(5 + C::kBufs + i); }
-    __device__ uint32_t kfull(int i) const { return rest(5 + 2 * C::kBufs + i); }
-    __device__ uint32_t kempty(int i) const { return rest(5 + 2 * C::kBufs + C::kKStages + i); }
-    __device__ uint32_t vfull(int i) const { return rest(5 + 2 * (C::kBufs + C::kKStages) + i); }
-    __device__ uint32_t vempty(int i) const { return rest(5 + 2 * (C::kBufs + C::kKStages) + C::kVStages + i); }
+    __device__ uint32_t qfull() const { return rest(0); }                        // a piece's queries
+    __device__ uint32_t ofree() const { return rest(1); }                        // a piece's O is read
+    __device__ uint32_t done() const { return rest(2); }
+    // Of tiles i mod kBufs.  As products complete in their order, S of a tile shows that the product with V kBufs tiles before is
+    // complete; pvdone has as many barriers, so that who has seen S of tile y may wait for the product of y or y - 1 without
+    // having waited for those before: of that barrier, the phase before is over.
+    __device__ uint32_t sfull(int i) const { return rest(3 + i); }
+    __device__ uint32_t pready(int i) const { return rest(3 + C::kBufs + i); }
+    __device__ uint32_t pvdone(int i) const { return rest(3 + 2 * C::kBufs + i); }
+    __device__ uint32_t kfull(int i) const { return rest(3 + 3 * C::kBufs + i); }
+    __device__ uint32_t kempty(int i) const { return rest(3 + 3 * C::kBufs + C::kKStages + i); }
+    __device__ uint32_t vfull(int i) const { return rest(3 + 3 * C::kBufs + 2 * C::kKStages + i); }
+    __device__ uint32_t vempty(int i) const { return rest(3 + 3 * C::kBufs + 2 * C::kKStages + C::kVStages + i); }
 };
 
 // What a unit costs besides its tiles, in tiles: its queries, its result, and the pipeline in between.  In the line it stands
@@ -414,8 +415,8 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
             for (int i = 0; i < C::kBufs; i++) {
                 mbar_init(bar.sfull(i), 2);                   // the product, and the thread that saw K and its scales
                 mbar_init(bar.pready(i), C::kSoftmaxWarps);
+                mbar_init(bar.pvdone(i), 1);
             }
-            for (int i = 0; i < 2; i++) mbar_init(bar.pvdone(i), 1);
             mbar_init(bar.qfull(), C::kSoftmaxWarps);
             mbar_init(bar.ofree(), C::kSoftmaxWarps);
             mbar_init(bar.done(), 1);
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                         for (int k = 0; k < KT / 16; k++)
                             umma_ss(tmem + C::kOCol + h * R, v + h * (2 * KT * 128 >> 4) + k * (2048 >> 4), p + k * (2048 >> 4),
                                     idesc_o, !fresh || k > 0);
-                    umma_commit(bar.pvdone(y & 1));
+                    umma_commit(bar.pvdone(buf));
                     umma_commit(bar.vempty(st));
                 }
                 __syncwarp();
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 16; i++) l2[16 * b + i] = f2_mul(l2[16 * b + i], fac(i));
                                 if (y > y_end - p.tiles) {
-                                    ok = wait_for(bar.pvdone((y - 1) & 1), ((y - 1) >> 1) & 1, abort_flag) && ok;
+                                    ok = wait_for(bar.pvdone((y - 1) % C::kBufs), ((y - 1) / C::kBufs) & 1, abort_flag) && ok;
                                     tc_fence_after();
 #pragma unroll 1
                                     for (int o = 0; o < 2 * C::kHalves; o++) {        // halves of the columns, dimensions
@@ -889,7 +890,7 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 if (more) convert_q(s_piece[k + 1]);
                 // ---- the piece's result
                 const int yz = y_end - 1;
-                ok = wait_for(bar.pvdone(yz & 1), (yz >> 1) & 1, abort_flag) && ok;
+                ok = wait_for(bar.pvdone(yz % C::kBufs), (yz / C::kBufs) & 1, abort_flag) && ok;
                 tc_fence_after();
                 if (busy) {
 #pragma unroll
