@@ -87,6 +87,8 @@ mmq_status append(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, const mmq_
     MMQ_TRY(check_rotary(rotary, cache->head_dim));
     if (!q != !q_out || (q && q_heads <= 0)) return MMQ_ERR_INVALID_ARG;
     if (!work) return MMQ_OK;
+    if (tree && !tree->depths) return MMQ_ERR_INVALID_ARG;
+    if (tree && !aligned16(tree->depths)) return MMQ_ERR_ALIGN;
     MMQ_TRY(check_rows(k));
     MMQ_TRY(check_rows(v));
     if (q) MMQ_TRY(check_rows(q));
@@ -277,8 +279,7 @@ mmq_status mmq_kv_append_tree(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs
                               int64_t tokens, const mmq_heads* k, const mmq_heads* v, const float* k_weight,
                               const mmq_heads* q, int q_heads, const float* q_weight, const mmq_heads* q_out,
                               const mmq_rotary* rotary, float eps, mmq_stream_t stream) {
-    if (!tree || !tree->depths) return MMQ_ERR_INVALID_ARG;
-    if (!aligned16(tree->depths)) return MMQ_ERR_ALIGN;
+    if (!tree) return MMQ_ERR_INVALID_ARG;
     return append(cache, seqs, tree, tokens, k, v, k_weight, q, q_heads, q_weight, q_out, rotary, eps, stream_of(stream),
                   "mmq_kv_append_tree");
 }
