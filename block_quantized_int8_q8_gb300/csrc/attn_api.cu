@@ -364,7 +364,7 @@ mmq_status mmq_kv_keep(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64
     if (kept_stride < 0) return MMQ_ERR_INVALID_ARG;
     if (kept_stride > MMQ_MAX_DRAFT) return MMQ_ERR_SHAPE;
     if (!work) return MMQ_OK;
-    if (!kept || !counts) return MMQ_ERR_INVALID_ARG;
+    if ((!kept && kept_stride > 0) || !counts) return MMQ_ERR_INVALID_ARG;
     if (!aligned16(kept) || !aligned16(counts)) return MMQ_ERR_ALIGN;
     const KeepArgs a{cache_of(cache), seqs_of(seqs, tokens), kept, counts, kept_stride};
     return done(run_kv_keep(cache->head_dim, a, stream_of(stream)), "mmq_kv_keep");

@@ -439,7 +439,7 @@ mmq_status mmq_attention_tree(const mmq_heads* q, int n_heads, const mmq_kv_cach
  * A block into which a token moves gets the largest scale s' that one of its tokens had (those that stay in it among
  * them); a code of a token whose block had the scale s becomes round-half-even(code * (s/s')), quotient and product in f32
  * (0 where s' is 0).  A block whose tokens all stay is not touched.  Tokens on an invalid page become zeros.
- * kept_stride is at most MMQ_MAX_DRAFT.
+ * kept_stride is at most MMQ_MAX_DRAFT; with 0, where no sequence keeps a token, kept may be null.
  */
 mmq_status mmq_kv_keep(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, int64_t tokens, const int32_t* kept,
                        int64_t kept_stride, const int32_t* counts, mmq_stream_t stream);

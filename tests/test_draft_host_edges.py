@@ -2,7 +2,7 @@
 (no GPU needed).  The pointers are fake and never dereferenced."""
 import pytest
 
-from test_attention_host import FAKE, INVALID, cache, heads, lib, seqs  # noqa: F401
+from test_attention_host import ALIGN, FAKE, INVALID, cache, heads, lib, seqs  # noqa: F401
 from test_draft_host import tree
 
 
@@ -15,3 +15,19 @@ from test_draft_host import tree
 def test_append_of_no_tokens_needs_no_depths(lib, t, tokens, status):  # noqa: F811
     assert lib.mmq_kv_append_tree(cache(), seqs(), t, tokens, heads(), heads(), None, None, 0, None, None, None, 1e-6,
                                   None) == status
+
+
+@pytest.mark.parametrize("kept,stride,counts,tokens,status", [
+    (None, 0, None, 5, INVALID),
+    (None, 4, FAKE, 5, INVALID),
+    (None, 0, FAKE, 0, 0),
+    (FAKE + 4, 0, FAKE, 5, ALIGN),
+])
+def test_keep_refuses_rows_that_are_not_there(lib, kept, stride, counts, tokens, status):  # noqa: F811
+    assert lib.mmq_kv_keep(cache(), seqs(), tokens, kept, stride, counts, None) == status
+
+
+def test_keep_of_no_rows_needs_none(lib):  # noqa: F811
+    """A null array of no rows gets past the checks: the next one, of the counts' alignment, is what refuses the call."""
+    assert lib.mmq_kv_keep(cache(), seqs(), 5, None, 0, FAKE + 4, None) == ALIGN
+    assert lib.mmq_kv_keep(cache(), seqs(), 5, None, 1, FAKE + 4, None) == INVALID
