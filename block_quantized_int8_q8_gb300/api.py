@@ -401,6 +401,8 @@ def _of_tree(tree):
         return None, None
     if not isinstance(tree, DraftTree):
         raise MMQError("tree: expected a DraftTree")
+    if tree.depths is None or tree.masks is None:             # (both None would pass for no tree)
+        raise MMQError("tree: expected depths and masks")
     return tree.depths, tree.masks
 
 

@@ -2,6 +2,7 @@
 (no GPU needed).  The pointers are fake and never dereferenced."""
 import pytest
 
+from block_quantized_int8_q8_gb300 import api
 from test_attention_host import ALIGN, FAKE, INVALID, cache, heads, lib, seqs  # noqa: F401
 from test_draft_host import tree
 
@@ -31,3 +32,14 @@ def test_keep_of_no_rows_needs_none(lib):  # noqa: F811
     """A null array of no rows gets past the checks: the next one, of the counts' alignment, is what refuses the call."""
     assert lib.mmq_kv_keep(cache(), seqs(), 5, None, 0, FAKE + 4, None) == ALIGN
     assert lib.mmq_kv_keep(cache(), seqs(), 5, None, 1, FAKE + 4, None) == INVALID
+
+
+def test_a_tree_without_its_tensors_is_not_no_tree(lib):  # noqa: F811
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(2, dtype=torch.int32)
+    for t in (api.DraftTree(None, None), api.DraftTree(x, None), api.DraftTree(None, x[:, None])):
+        with pytest.raises(api.MMQError):
+            api._of_tree(t)
+    assert api._of_tree(None) == (None, None)
+    t = api.DraftTree(x, x[:, None])
+    assert api._of_tree(t)[0] is t.depths and api._of_tree(t)[1] is t.masks
