@@ -133,6 +133,9 @@ __device__ __forceinline__ float largest(const Quad& x, float m) {
     return fmaxf(m, fmaxf(fabsf(f2_lo(x[1])), fabsf(f2_hi(x[1]))));
 }
 
+// Position that a tree's token turns at.  A sum past int32 wraps to one that no table has.
+__device__ __forceinline__ int turn_position(int first, int depth) { return (int)((unsigned)first + (unsigned)depth); }
+
 template <int D, int B, typename T>
 __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int head, bool isv, bool by_token) {
     using S = AppendShape<D, B>;
@@ -177,7 +180,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
         fill[i] = j < B && pos >= p0 && pos < q.end;
         turn_at[i] = pos;
         if (fill[i]) {
-            if (rotate && a.depths) turn_at[i] = p0 + a.depths[q.n0 + pos - p0];
+            if (rotate && a.depths) turn_at[i] = turn_position(p0, a.depths[q.n0 + pos - p0]);
             const T* p = static_cast<const T*>(in.data) + (long long)(q.n0 + pos - p0) * in.ts + head * in.hs;
             in0[i] = load_raw(p + ch.o0);
             in1[i] = load_raw(p + ch.o1);
@@ -264,10 +267,13 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
                 while (s + 1 < a.sq.seqs && a.sq.cu[s + 1] <= t) s++;
                 q = load_seq(a.sq, s, a.c.page);
             }
-            if (t >= q.n0 && t < q.n0 + q.n) pos = q.len - q.n + (a.depths ? a.depths[t] : t - q.n0);
-            if (a.rot.cos && pos >= a.rot.positions) {
-                pos = -1;
-                flag_error(DEVERR_POSITION);
+            if (t >= q.n0 && t < q.n0 + q.n) pos = q.len - q.n + (t - q.n0);
+            if (a.rot.cos && pos >= 0) {                      // a row that has a place turns, at its depth's position
+                if (a.depths) pos = turn_position(q.len - q.n, a.depths[t]);
+                if (pos < 0 || pos >= a.rot.positions) {
+                    pos = -1;
+                    flag_error(DEVERR_POSITION);
+                }
             }
         }
         s_pos[threadIdx.x] = pos;

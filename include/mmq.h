@@ -408,7 +408,7 @@ mmq_status mmq_draft_masks(const int32_t* parents, const int32_t* cu_tokens, int
 /*
  * mmq_kv_append_tree -- mmq_kv_append with the rotation at the tokens' depths: key and query of token i turn at position
  * kv_len - n + depths[i] (one outside the rotation table is skipped, MMQ_DEVERR_POSITION), and are stored at
- * kv_len - n + i.  tree's masks are not used and may be null.
+ * kv_len - n + i.  Without a rotation depths change nothing.  tree's masks are not used and may be null.
  */
 mmq_status mmq_kv_append_tree(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs, const mmq_draft_tree* tree,
                               int64_t tokens, const mmq_heads* k, const mmq_heads* v, const float* k_weight,
