@@ -109,6 +109,11 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
         if (odd || (rows > 0 && (q.n > n || min(q.end, a.max_kv) < q.len))) flag_error(DEVERR_LENGTH);
     }
     if (rows <= 0) return;
+    if (TREE && a.window > 0 && split == 0 && head == 0) {    // depths of the block's tokens
+        const int at = r0 / a.group + (int)threadIdx.x;
+        if (at <= (r0 + rows - 1) / a.group && tree_depth(a.depths[q.n0 + at], a.max_tokens) != a.depths[q.n0 + at])
+            flag_error(DEVERR_DRAFT);
+    }
     const Range rg = visible_range(a, q, chunk);
     if (split >= rg.parts) return;
     const int first = q.len - q.n, end = min(q.end, a.max_kv);
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(FEW_THREADS, few_blocks(D, NT)) few_kernel(con
                         const int j = tok + 16 * u + g;
                         if constexpr (TREE) {
                             const uint32_t* mask = a.masks + (long long)(q.n0 + at) * a.words;
-                            const int low = a.window > 0 ? first + a.depths[q.n0 + at] - a.window + 1 : 0;
+                            const int low = a.window > 0 ? first + tree_depth(a.depths[q.n0 + at], a.max_tokens) - a.window + 1 : 0;
                             auto hidden = [&](int j) {
                                 return j >= lim_new || (j < first ? j < low : !(mask[(j - first) / 32] >> ((j - first) % 32) & 1u));
                             };

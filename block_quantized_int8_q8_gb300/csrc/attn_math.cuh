@@ -74,6 +74,10 @@ __device__ __forceinline__ Range visible_range(const AttnArgs& a, const Seq& q, 
 
 // The lowest n bits; none for a negative n.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
+// A token's depth, which a window goes by.  The caller's array may hold any number: one that no token of a tree of max_tokens
+// has counts as the nearest that one has, since the range of tokens that is gone over, and the stretch of it that needs no mask,
+// follow from the bounds.
+__device__ __forceinline__ int tree_depth(int depth, int max_tokens) { return min(max(depth, 0), max_tokens - 1); }
 // What a row of a tree sees of 32 tokens, the first of which comes d0 after the cached text: of the new tokens what its mask
 // says, of the cached ones those from the low-th of the 32 on; nothing from the there-th on.
 __device__ __forceinline__ uint32_t tree_sees(const uint32_t* mask, int words, int d0, int low, int there) {

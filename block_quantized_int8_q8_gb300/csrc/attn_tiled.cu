@@ -511,7 +511,12 @@ __global__ void __launch_bounds__(T_THREADS, 1) tiled_kernel(const AttnArgs a, i
         // row of this warp sees whole and that need no mask
         const int b0 = base + j0 * KT, k_s = span[i].s - j0, k_e = span[i].e - j0;
         const int lim = (!real ? -1 : (a.causal ? min(first + (TREE ? n - 1 : tokrow), end - 1) : end - 1)) - b0;
-        const int low = (a.window > 0 ? first + (TREE ? a.depths[tok] : tokrow) - a.window + 1 : 0) - b0;
+        int past = tokrow;                                    // the row's token counts this many from the first
+        if (TREE && a.window > 0) {
+            past = tree_depth(a.depths[tok], a.max_tokens);
+            if (past != a.depths[tok]) flag_error(DEVERR_DRAFT);
+        }
+        const int low = (a.window > 0 ? first + past - a.window + 1 : 0) - b0;
         const int ra = min(row0 + (r & ~31), row0 + rows - 1), rz = min(row0 + (r | 31), row0 + rows - 1);
         const int k_hi = max((a.causal ? min(first + (TREE ? -1 : ra / a.group), end - 1) : end - 1) - b0 + 1, 0) / KT;
         const int k_lo = a.window > 0 ? (max(first + (TREE ? a.max_tokens - 1 : rz / a.group) - a.window + 1 - b0, 0) + KT - 1) / KT : 0;

@@ -758,7 +758,11 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     s_neg[c] = real ? UNSET : -INFINITY;
                     s_m[c] = -INFINITY;
                     s_tok[c] = tok;
-                    if (a.window > 0) s_low[c] = p.first + a.depths[tok] - a.window + 1;
+                    if (a.window > 0) {
+                        const int depth = a.depths[tok], held = tree_depth(depth, a.max_tokens);
+                        if (held != depth) flag_error(DEVERR_DRAFT);
+                        s_low[c] = p.first + held - a.window + 1;
+                    }
                     s_out[c] = (long long)tok * a.out.ts + (p.head * a.group + row % a.group) * a.out.hs;
                 }
                 named_bar_sync(id, 128);

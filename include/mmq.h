@@ -109,8 +109,9 @@ typedef enum {
 #define MMQ_DEVERR_LENGTH     32u  /* a sequence was longer than its page table or the stated maximum, or (append, read)
                                       shorter than its new tokens, or the token offsets fell or did not run from 0
                                       to the number of tokens; what does not fit was skipped */
-#define MMQ_DEVERR_DRAFT      64u  /* a drafted token's parent was not a row before it (taken as -1), or the rows to keep of
-                                      a sequence were too many, not ascending or not its own (it was left as it was) */
+#define MMQ_DEVERR_DRAFT      64u  /* a drafted token's parent was not a row before it (taken as -1), its depth, in attention
+                                      with a window, not one of a tree (taken as the nearest), or the rows to keep of a
+                                      sequence were too many, not ascending or not its own (it was left as it was) */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* mmq_status_string(mmq_status s);
@@ -419,7 +420,7 @@ mmq_status mmq_kv_append_tree(const mmq_kv_cache* cache, const mmq_kv_seqs* seqs
  * mmq_attention_tree -- mmq_attention where token i of a sequence's n new ones sees the cached positions j < kv_len - n and, of
  * the new tokens, those that its mask says.  With window > 0 it sees j > kv_len - n + depths[i] - window only; a window must
  * not hide a new token: one below max_tokens is refused (MMQ_ERR_UNSUPPORTED).  depths are used with a window only and may
- * be null without.  max_tokens is at most MMQ_MAX_DRAFT.  With max_tokens * n_heads / kv_heads from 17 to 128,
+ * be null without; one outside 0 .. max_tokens - 1 sets MMQ_DEVERR_DRAFT and counts as the nearest of these.  max_tokens is at most MMQ_MAX_DRAFT.  With max_tokens * n_heads / kv_heads from 17 to 128,
  * seqs * kv_heads * (max_kv_len / 128 + 6) is below 2^30 (else MMQ_ERR_SHAPE and a size of 0).  The other arguments, the
  * arithmetic and its bounds are mmq_attention's; the workspace is mmq_attention_tree_workspace_bytes(...) bytes (0: may be
  * null).

@@ -1,14 +1,18 @@
 """The operators on a tree of drafted tokens at the edges of what their documentation allows.  Tolerances as in
 test_draft_tree.py."""
+import math
+
 import pytest
 import torch
 
 import test_draft_tree as T
-from test_attention_ops import assert_close, make_cache, offsets, ref_norm_rope, rotary_tables
+from test_attention_ops import ULP, assert_close, make_cache, offsets, ref_norm_rope, rotary_tables
+from test_draft_tiles import FEW, TILED, TILES, kernel
 
 from block_quantized_int8_q8_gb300 import api
 
 gpu = pytest.mark.gpu
+LOOSE = 1 << 20                                               # a loose bound of the lengths
 
 
 # ------------------------------------------------------------------------------------------------ nothing to do
@@ -84,3 +88,42 @@ def test_append_writes_every_query_that_has_a_place(D, dt, rot):
         key = ref_norm_rope(rows[t, 4:6], None, 1e-6, *((cos[at], sin[at]) if rot else (None, None)), False)
         step = cache.k_scale[int(table[seq[t], p // 16]), :, 0].double().cpu()[:, None]
         assert ((got.double() - key).abs() <= step * (0.5 + 2.0 ** -7) + 2.0 ** -20).all(), t
+
+
+# ------------------------------------------------------------------------------------------------ depths that are no depths
+@gpu
+@pytest.mark.parametrize("depth", [0, 11, 12, 100, 100000, 2 ** 31 - 1, -1, -100, -(2 ** 31)])
+@pytest.mark.parametrize("D,n,takes", [(64, 3, FEW), (64, 12, TILES), (64, 40, TILED), (128, 3, FEW), (128, 12, TILES),
+                                       (128, 40, TILED), (256, 3, FEW), (256, 12, TILES), (256, 40, TILED)])
+def test_window_takes_a_depth_past_the_bounds_as_the_nearest(D, n, takes, depth):
+    """A depth that no tree of so many tokens has is flagged, and counts as the nearest that one has; every kernel agrees."""
+    assert kernel(4, 2, D, 2, n, LOOSE) == takes
+    g = torch.Generator().manual_seed(depth % 1000 + D)
+    past, m, window = [900, 400], [n, 2], 200
+    lens = [a + b for a, b in zip(past, m)]
+    cache, table = make_cache(g, lens, 2, D, 64, 16)
+    q = torch.randn(sum(m), 8, D, generator=g).bfloat16()
+    parents = [T.draw_parents(k, g, "star") for k in m]
+    tree = T.make_tree(parents, m)
+    depths = tree.depths.clone()
+    depths[1] = depth
+    near = min(max(depth, 0), n - 1)
+    api.read_device_errors()
+    args = (q.cuda(), cache, table.cuda(), T.i32(lens), LOOSE, offsets(m).cuda(), n)
+    out, lse = api.attention(*args, window=window, out_dtype=torch.float32, return_lse=True,
+                             tree=api.DraftTree(depths, tree.masks))
+    assert api.read_device_errors() == (api.DEVERR_DRAFT if near != depth else 0)
+    want, wlse, vmax = T.ref_tree_attention(q, cache, table, lens, m, [T.sees(p) for p in parents], D ** -0.5, window)
+    # the one row with another depth than its mask has
+    first, ref = past[0], T.RefCache(cache)
+    j = torch.arange(lens[0])
+    see = torch.where(j < first, j > first + near - window, torch.cat([torch.zeros(first, dtype=torch.bool), T.sees(parents[0])[1]]))
+    for h in range(8):
+        k, v = (ref.values(side, table[0], 0, lens[0])[:, h // 4] for side in (0, 1))
+        s = (k @ q[1, h].double() * D ** -0.5).masked_fill(~see, -math.inf)
+        wlse[1, h], want[1, h] = torch.logsumexp(s, 0), torch.softmax(s, 0) @ v
+    assert_close(out, want, torch.full_like(want, vmax * (2.0 ** -11 + 2.0 ** -16 + ULP[torch.float32])))
+    assert ((lse.double().cpu() - wlse).abs() <= 2.0 ** -18 + 2.0 ** -20 * wlse.abs()).all()
+    again = api.attention(*args, out_dtype=torch.float32, tree=api.DraftTree(depths, tree.masks))     # not looked at without a window
+    assert torch.equal(again, api.attention(*args, out_dtype=torch.float32, tree=tree))
+    assert api.read_device_errors() == 0
