@@ -688,7 +688,9 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
             // 4w + t, 0 2 1 3 within.  All rows of the group by one power of two, which brings the largest magnitude to
             // [2^14, 2^15), so that one factor turns S into scores: a row is then exact where it was exact on its own, down
             // to 2^-14 of its largest value and rounded to 2^-25 of it below, as long as that is within 2^13 of the group's.
-            // A smaller row is brought that near, and its S is multiplied by the rest (s_even) first.
+            // A smaller row is brought that near, and its S is multiplied by the rest (s_even) first.  So is a row so large
+            // that the common factor would reach 1 (|scale q| from some 10^4 on): the factor times a key's scale is then finite
+            // whatever the row, and a row out of bounds leaves its neighbours alone.
             float factor = 0.f;                               // of the next piece's scores
             bool uneven = false;
             auto convert_q = [&](const Piece& p) {
@@ -712,23 +714,26 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                     float most = own < INFINITY ? own : 0.f;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    // exponents count from 127; a zero row's does not matter
-                    const int high = max((int)(__float_as_uint(most) >> 23), 1);
+                    // exponents count from 127; a zero row's does not matter; up to cap the factor is below 1
+                    const int cap = 267 - (int)(__float_as_uint(fabsf(a.scale * LOG2E)) >> 23);
+                    const int high = min(max((int)(__float_as_uint(most) >> 23), 1), cap);
                     factor = a.scale * LOG2E * pow2((high - 141) / 2) * pow2(high - 141 - (high - 141) / 2);
                     uneven = false;
 #pragma unroll 1
                     for (int i = 0; i < N; i += RPP) {
                         const int c = c0 + i + (w * 32 + lane) / LPR;
                         const float top = s_next[c];
-                        const int rest = top == 0.f ? 0 : max(high - 13 - max((int)(__float_as_uint(top) >> 23), 1), 0);
+                        const int e2 = max((int)(__float_as_uint(top) >> 23), 1);
+                        const int rest = top == 0.f ? 0 : max(high - 13 - e2, 0) + min(high - e2, 0);
                         const int up = 141 - high + rest;
                         const float up0 = pow2(up / 2), up1 = pow2(up - up / 2);
                         float x[8];
                         unpack8(ld_shared_u4(panel + sw128_off(c, m % 8)), qt == MMQ_BF16, x);
 #pragma unroll
                         for (int e = 0; e < 8; e++) x[e] = x[e] * up0 * up1;
-                        if (m == 0) s_even[c] = pow2(-min(rest, 126)) * pow2(min(126 - rest, 0));
-                        uneven |= rest > 0;
+                        const int half = min(max(-rest, -126), 127);
+                        if (m == 0) s_even[c] = pow2(half) * pow2(-rest - half);
+                        uneven |= rest != 0;
                         __syncwarp();                         // the rows are read
 #pragma unroll
                         for (int e = 0; e < 2; e++) {

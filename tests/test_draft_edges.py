@@ -127,3 +127,50 @@ def test_window_takes_a_depth_past_the_bounds_as_the_nearest(D, n, takes, depth)
     again = api.attention(*args, out_dtype=torch.float32, tree=api.DraftTree(depths, tree.masks))     # not looked at without a window
     assert torch.equal(again, api.attention(*args, out_dtype=torch.float32, tree=tree))
     assert api.read_device_errors() == 0
+
+
+# ------------------------------------------------------------------------------------------------ rows of any magnitude
+#: new tokens whose rows each kernel takes at four query heads for a key/value head under a loose bound, by head_dim
+KERNELS = [(64, 3, FEW), (64, 12, TILES), (64, 30, TILES), (64, 40, TILED), (128, 3, FEW), (128, 12, TILES), (128, 30, TILES),
+           (128, 40, TILED), (256, 3, FEW), (256, 12, TILES), (256, 40, TILED)]
+
+
+@gpu
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -20])
+@pytest.mark.parametrize("value", [3.0e38, -3.0e38, 1.0e30])
+@pytest.mark.parametrize("D,n,takes", KERNELS)
+def test_a_huge_finite_row_stays_alone(D, n, takes, value, small):
+    """A finite row out of bounds, which no common factor with its neighbours may follow: they are what they are without it."""
+    assert kernel(4, 2, D, 1, n, LOOSE) == takes
+    g = torch.Generator().manual_seed(3)
+    cache, table = make_cache(g, [300], 2, D, 64, 16)
+    q = torch.randn(n, 8, D, generator=g).bfloat16() * small
+    more = dict(scale=D ** -0.5 / small, out_dtype=torch.float32, return_lse=True, tree=T.make_tree([T.draw_parents(n, g)], [n]))
+    args = (cache, table.cuda(), T.i32([300]), LOOSE, T.i32([0, n]), n)
+    vmax = float((cache.v.abs().amax((2, 3)) * cache.v_scale.amax(-1)).max())
+    want, wlse = api.attention(q.cuda(), *args, **more)
+    x = q.clone()
+    x[1, 3, 5] = value
+    x[2, 6] = value
+    got, lse = api.attention(x.cuda(), *args, **more)
+    same = torch.ones(n, 8, dtype=torch.bool)
+    same[1, 3] = same[2, 6] = False
+    assert (got - want).abs()[same.cuda()].max() <= 2 * vmax * (2.0 ** -11 + 2.0 ** -16)
+    assert ((lse - wlse).abs() <= 2.0 ** -17 + 2.0 ** -19 * wlse.abs())[same.cuda()].all()
+    assert api.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("D,n,takes", KERNELS)
+def test_rows_of_many_magnitudes_over_tiny_scales(D, n, takes, monkeypatch):
+    """Key scales of 2^-60: rows of 2^56 to 2^60 have ordinary scores, the others next to none, all within bounds."""
+    assert kernel(4, 2, D, 2, n, LOOSE) == takes
+
+    def tamper(cache, table, q):
+        cache.k_scale.mul_(2.0 ** -60)
+        q[0::3] *= 2.0 ** 60
+        q[1::3] *= 2.0 ** 56
+        q[2::3] *= 2.0 ** 30
+
+    monkeypatch.setattr(T, "BOUND", LOOSE)
+    T.check([300, 190], [n, 3], 8, 2, D, 64, 16, tamper=tamper)
