@@ -774,9 +774,10 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
                 uint64_t l2[N / 2];
 #pragma unroll
                 for (int i = 0; i < N / 2; i++) l2[i] = 0ull;
-                // every row sees every token of the tiles from x_low to before x_high, between the window's edge and the new tokens
+                // every row sees every token of the tiles from y_low to before y_high, between the window's edge and the new tokens
+                // (or what the bounds leave of the cached ones)
                 const int y_end = y0 + p.x0 + p.tiles;
-                const int y_high = y0 + p.x0 + (p.first - p.tok0 >= 0 ? (p.first - p.tok0) / KT : 0);
+                const int y_high = y0 + p.x0 + max(min(p.first, p.lim) - p.tok0, 0) / KT;
                 const int y_low = a.window > 0 ? y0 + p.x0 + (max(p.first + a.max_tokens - a.window - p.tok0, -1) + KT) / KT : 0;
 #pragma unroll 1
                 for (int y = y0 + p.x0; y < y_end; y++) {

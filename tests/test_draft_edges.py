@@ -174,3 +174,35 @@ def test_rows_of_many_magnitudes_over_tiny_scales(D, n, takes, monkeypatch):
 
     monkeypatch.setattr(T, "BOUND", LOOSE)
     T.check([300, 190], [n, 3], 8, 2, D, 64, 16, tamper=tamper)
+
+
+# ------------------------------------------------------------------------------------------------ bounds that do not hold
+@gpu
+@pytest.mark.parametrize("bound", [200, 201, 128, 137])
+@pytest.mark.parametrize("S,n,H,D,takes", [(1, 2, 2, 128, FEW), (256, 5, 8, 128, TILES), (256, 16, 16, 128, TILES),
+                                           (128, 10, 32, 64, TILES), (60, 8, 16, 256, TILES), (2, 300, 8, 128, TILED)])
+def test_tokens_past_the_stated_length_are_skipped(S, n, H, D, takes, bound):
+    """Texts longer than the stated maximum are flagged, and no row sees a token past it."""
+    assert kernel(4, H, D, S, n, bound) == takes
+    g = torch.Generator().manual_seed(bound)
+    length, few = 290 + n, min(S, 3)
+    cache, table = make_cache(g, [length] * few, H, D, 64, 16)
+    cache.v_scale[:, :, 0::4] *= 8.0                          # what comes after a boundary weighs
+    q = torch.randn(few * n, 4 * H, D, generator=g).bfloat16()
+    copies = [i % few for i in range(S)]
+    rows = torch.cat([torch.arange(i * n, i * n + n) for i in copies])
+    tree = T.make_tree([T.draw_parents(n, g)] * S, [n] * S)
+    api.read_device_errors()
+    out, lse = api.attention(q[rows].cuda(), cache, table[copies].cuda(), T.i32([length] * S), bound,
+                             offsets([n] * S).cuda(), n, out_dtype=torch.float32, return_lse=True, tree=tree)
+    assert api.read_device_errors() == api.DEVERR_LENGTH
+    ref = T.RefCache(cache)
+    want, wlse, vmax = torch.empty(few * n, 4 * H, D, dtype=torch.float64), torch.empty(few * n, 4 * H, dtype=torch.float64), 0.0
+    for i in range(few):
+        k, v = (ref.values(side, table[i], 0, bound) for side in (0, 1))
+        vmax = max(vmax, float(v.abs().max()))
+        for h in range(4 * H):
+            s = q[i * n:i * n + n, h].double() @ k[:, h // 4].T * D ** -0.5
+            wlse[i * n:i * n + n, h], want[i * n:i * n + n, h] = torch.logsumexp(s, -1), torch.softmax(s, -1) @ v[:, h // 4]
+    assert_close(out, want[rows], torch.full_like(want[rows], vmax * (2.0 ** -11 + 2.0 ** -16 + ULP[torch.float32])))
+    assert ((lse.double().cpu() - wlse[rows]).abs() <= 2.0 ** -18 + 2.0 ** -20 * wlse[rows].abs()).all()
