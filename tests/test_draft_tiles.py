@@ -1,6 +1,6 @@
-"""Attention of a tree's rows in the kernel that shares out tiles (csrc/attn_tree.cu), at sizes that the rule of csrc/attn_api.cu
-sends there, which is asserted: batches of which a block has more tiles than it lists at once, and calls that repeat.
-References and tolerances as in test_draft_tree.py."""
+"""Attention of a tree's rows in the kernel that shares out tiles (csrc/attn_tree.cu): every behaviour of the operator at sizes
+that the rule of csrc/attn_api.cu sends there, which is asserted for each, and batches of which a block has more tiles than
+it lists at once.  References and tolerances as in test_draft_tree.py."""
 import ctypes
 import math
 
@@ -8,13 +8,18 @@ import pytest
 import torch
 
 import test_draft_tree as T
-from test_attention_ops import ULP, assert_close, offsets
+from test_attention_ops import ULP, assert_close, make_cache, offsets
 
 from block_quantized_int8_q8_gb300 import _build, api
 
 gpu = pytest.mark.gpu
 FEW, TILES, TILED = range(3)                                  # TreeKernel of csrc/attn.h
 TILE, SHARES, LISTED = 128, 152, 256                          # tokens of a tile, blocks, tiles that a block lists at once
+LOOSE = 1 << 20
+
+#: rows (tokens x query heads of a group of 4) of the largest tree, for each head_dim
+ROWS = [(64, 36), (64, 64), (64, 100), (64, 128), (128, 20), (128, 40), (128, 64), (128, 68), (128, 128), (256, 20), (256, 36),
+        (256, 64)]
 
 
 def kernel(group, kv_heads, dim, seqs, most, max_kv):
@@ -23,6 +28,142 @@ def kernel(group, kv_heads, dim, seqs, most, max_kv):
     f.argtypes = [ctypes.c_int] * 4 + [ctypes.c_int64] * 2
     f.restype = ctypes.c_int
     return f(group, kv_heads, dim, seqs, most, max_kv)
+
+
+@pytest.fixture(autouse=True)
+def loose(monkeypatch):
+    """A loose bound of the lengths, with which short sequences take the kernel that long ones take."""
+    monkeypatch.setattr(T, "BOUND", LOOSE)
+
+
+def check(past, n, Hq, H, D, *args, **more):
+    assert kernel(Hq // H, H, D, len(n), max(n), LOOSE) == TILES
+    T.check(past, n, Hq, H, D, *args, **more)
+
+
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_sizes_are_the_kernels(D, rows):
+    for seqs in (1, 4, 700):
+        assert kernel(4, 2, D, seqs, rows // 4, LOOSE) == TILES
+    assert kernel(4, 2, D, 3, 1, LOOSE) == FEW and kernel(4, 2, D, 3, 33, LOOSE) == TILED
+
+
+@gpu
+@pytest.mark.parametrize("window", [1, 100, 128, 300, 5000])
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_window(D, rows, window):
+    n = rows // 4
+    check([400, 150, 33, 2000, 129], [n, 3, n // 2, n, 1], 8, 2, D, 32, 16, window=max(window, n))
+
+
+@gpu
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_rows_without_a_place(D, rows):
+    n = rows // 4
+    check([-3, 5, -(n // 2), -n, -n - 9], [4, 3, n, n, n], 8, 2, D, 32, 16)
+    check([-3, -1, -n // 2], [4, 1, n], 8, 2, D, 32, 16, kind="apart")
+    check([-3, 200, -n // 2], [4, 1, n], 8, 2, D, 32, 16, window=n)
+
+
+@gpu
+@pytest.mark.parametrize("qt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("ot", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,rows", [(64, 36), (64, 128), (128, 20), (128, 100), (256, 60)])
+def test_types(qt, ot, D, rows):
+    check([200, 77, 2500], [2, rows // 4, 3], 8, 2, D, 64, 32, qt, ot)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["forest", "path", "star", "apart"])
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_kinds_of_trees(D, rows, kind):
+    check([130, 0, 61, 1000], [rows // 8, 1, rows // 4, 3], 8, 2, D, kind=kind)
+
+
+@gpu
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_sharp_rows_and_scales(D, rows):
+    def tamper(cache, table, q):
+        q[0] *= 8.0
+        cache.v_scale[int(table[0, 0]), :, 0] = 0
+        cache.v[int(table[0, 0]), :, :16] = 0
+        cache.v_scale[int(table[0, 2])] = 1e-7
+        cache.k_scale[int(table[1, 0]), :, 0] = 0
+
+    def tiny(cache, table, q):
+        q *= 2.0 ** -100
+        cache.v_scale.mul_(2.0 ** -30)
+
+    n = [rows // 4, 3]
+    check([300, 200], n, 8, 2, D, 64, 16, tamper=tamper)
+    check([300, 200], n, 8, 2, D, 64, 16, tamper=tiny, scale=2.0 ** 97)
+    check([300, 200], n, 8, 2, D, 64, 16, scale=-0.1)
+    check([300, 200], n, 8, 2, D, 64, 16, scale=0.0)
+
+
+@gpu
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_reference_that_grows_late(D, rows):
+    def tamper(cache, table, q):
+        q.abs_()
+        cache.k.copy_(torch.randint(60, 70, cache.k.shape, generator=torch.Generator().manual_seed(1)))
+        for j, pg in enumerate(table[0].tolist()):
+            if pg >= 0:
+                cache.k_scale[pg] = 0.002 * (j + 1)
+    check([1000], [rows // 4], 8, 2, D, 64, 16, tamper=tamper)
+    check([1000], [rows // 4], 8, 2, D, 64, 16, tamper=tamper, scale=-D ** -0.5)
+
+
+@gpu
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_ignores_what_lies_past_the_length(D, rows):
+    n = [rows // 8, rows // 4]
+    assert kernel(4, 2, D, 2, max(n), LOOSE) == TILES
+    T.test_attention_ignores_what_lies_past_the_length(n, D)
+
+
+@gpu
+@pytest.mark.parametrize("qt,ot", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32)])
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_strided_rows_streams_and_workspace(D, rows, qt, ot):
+    """Queries and outputs that are slices of wider rows, another stream, a caller's workspace between two canaries; two runs: the
+    same bits."""
+    g = torch.Generator().manual_seed(11)
+    n, lens = rows // 4, [3000, 2900]
+    assert kernel(4, 2, D, 2, n, LOOSE) == TILES
+    cache, table = make_cache(g, lens, 2, D, 64, 32)
+    wide = torch.randn(2 * n, 13, D, generator=g).to(qt).cuda()
+    q = wide[:, 2:10]
+    tree = T.make_tree([T.draw_parents(n, g), T.draw_parents(n, g)], [n, n])
+    kv, cu, tb = T.i32(lens), offsets([n, n]).cuda(), table.cuda()
+    want, lse = api.attention(q.contiguous(), cache, tb, kv, LOOSE, cu, n, tree=tree, out_dtype=ot, return_lse=True)
+    need = api.attention_tree_workspace_bytes(2 * n, 8, 2, D, 2, n, LOOSE)
+    ws = torch.full((64 + need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((2 * n + 2, 12, D), 5.0, dtype=ot, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    _, again = api.attention(q, cache, tb, kv, LOOSE, cu, n, out=out[1:-1, 1:9], workspace=ws[64:64 + need], stream=st, tree=tree,
+                             return_lse=True)
+    torch.cuda.current_stream().wait_stream(st)
+    assert torch.equal(out[1:-1, 1:9], want) and torch.equal(lse, again)
+    assert (out[:, 0] == 5).all() and (out[:, 9:] == 5).all() and (out[0] == 5).all() and (out[-1] == 5).all()
+    assert (ws[:64] == 0xFF).all() and (ws[64 + need:] == 0xFF).all()
+
+
+@gpu
+@pytest.mark.parametrize("D,rows", ROWS)
+def test_a_path_is_causal_attention(D, rows):
+    g = torch.Generator().manual_seed(8)
+    n, lens = [rows // 8, rows // 4, 1], [800, rows // 4, 400]
+    assert kernel(4, 2, D, 3, max(n), LOOSE) == TILES
+    cache, table = make_cache(g, lens, 2, D, 64, 16)
+    q = torch.randn(sum(n), 8, D, generator=g).bfloat16().cuda()
+    args = (q, cache, table.cuda(), T.i32(lens), LOOSE, offsets(n).cuda(), max(n))
+    more = dict(out_dtype=torch.float32, return_lse=True)
+    a, la = api.attention(*args, **more)
+    b, lb = api.attention(*args, **more, tree=T.make_tree([T.draw_parents(k, g, "path") for k in n], n))
+    vmax = float((cache.v.abs().amax((2, 3)) * cache.v_scale.amax(-1)).max())
+    assert (a - b).abs().max() <= vmax * 2 * (2.0 ** -11 + 2.0 ** -16) and (la - lb).abs().max() <= 2.0 ** -17 + 2.0 ** -19 * 12
 
 
 # ------------------------------------------------------------------------------------------------ more than one list of tiles
