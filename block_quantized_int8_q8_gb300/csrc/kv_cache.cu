@@ -136,7 +136,9 @@ __device__ __forceinline__ float largest(const Quad& x, float m) {
 // Position that a tree's token turns at.  A sum past int32 wraps to one that no table has.
 __device__ __forceinline__ int turn_position(int first, int depth) { return (int)((unsigned)first + (unsigned)depth); }
 
-template <int D, int B, typename T>
+// TREE: a token turns at its depth's position.  A variant of its own: the positions held over the loads take two to six registers
+// more, and batches of chains 0.5 to 0.8 % (64 sequences of 64 tokens, heads of 128 and 256: 22.7 -> 22.8 and 47.5 -> 47.8 us).
+template <int D, int B, bool TREE, typename T>
 __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int head, bool isv, bool by_token) {
     using S = AppendShape<D, B>;
     constexpr int NR = (B + S::kRows - 1) / S::kRows;
@@ -178,9 +180,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     for (int i = 0; i < NR; i++) {
         const int j = r0 + i * S::kRows, pos = b0 + j;
         fill[i] = j < B && pos >= p0 && pos < q.end;
-        turn_at[i] = pos;
+        if (TREE) turn_at[i] = pos;
         if (fill[i]) {
-            if (rotate && a.depths) turn_at[i] = turn_position(p0, a.depths[q.n0 + pos - p0]);
+            if (TREE && rotate) turn_at[i] = turn_position(p0, a.depths[q.n0 + pos - p0]);
             const T* p = static_cast<const T*>(in.data) + (long long)(q.n0 + pos - p0) * in.ts + head * in.hs;
             in0[i] = load_raw(p + ch.o0);
             in1[i] = load_raw(p + ch.o1);
@@ -202,9 +204,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < NR; i++) {
-        const int pos = turn_at[i];
+        const int pos = TREE ? turn_at[i] : b0 + r0 + i * S::kRows;
         if (rotate && fill[i]) {
-            if (pos < 0 || pos >= a.rot.positions) {
+            if ((TREE && pos < 0) || pos >= a.rot.positions) {
                 fill[i] = false;
                 if (l == 0) flag_error(DEVERR_POSITION);
                 x0[i][0] = x0[i][1] = x1[i][0] = x1[i][1] = 0ull;
@@ -249,7 +251,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int slot, int 
 
 // Queries of QTOKENS packed rows (one for a decode step, whose latency counts): positions first, then units of kQHeads
 // heads of one token.
-template <int D, int B, typename T>
+template <int D, int B, bool TREE, typename T>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int count, int qot) {
     using S = AppendShape<D, B>;
     constexpr int H = S::kQHeads;
@@ -268,12 +270,14 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
                 q = load_seq(a.sq, s, a.c.page);
             }
             if (t >= q.n0 && t < q.n0 + q.n) pos = q.len - q.n + (t - q.n0);
-            if (a.rot.cos && pos >= 0) {                      // a row that has a place turns, at its depth's position
-                if (a.depths) pos = turn_position(q.len - q.n, a.depths[t]);
-                if (pos < 0 || pos >= a.rot.positions) {
-                    pos = -1;
-                    flag_error(DEVERR_POSITION);
-                }
+            bool off = a.rot.cos && pos >= a.rot.positions;   // a row that has a place turns, at a position of the table
+            if (TREE && a.rot.cos && pos >= 0) {
+                pos = turn_position(q.len - q.n, a.depths[t]);
+                off = pos < 0 || pos >= a.rot.positions;
+            }
+            if (off) {
+                pos = -1;
+                flag_error(DEVERR_POSITION);
             }
         }
         s_pos[threadIdx.x] = pos;
@@ -331,7 +335,7 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int t0, int 
     }
 }
 
-template <int D, int B, typename T>
+template <int D, int B, bool TREE, typename T>
 __global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(const AppendArgs a, unsigned query_share,
                                                                           bool by_token, int qtokens, int qot) {
     pdl_wait();
@@ -340,9 +344,9 @@ __global__ void __launch_bounds__(AppendShape<D, B>::kThreads) append_kernel(con
     if (__umulhi(blockIdx.x + 1, query_share) == q) {
         const int slot = b / (2u * a.c.heads), w = b - slot * 2u * a.c.heads;
         const bool isv = w >= a.c.heads;
-        append_block<D, B, T>(a, slot, isv ? w - a.c.heads : w, isv, by_token);
+        append_block<D, B, TREE, T>(a, slot, isv ? w - a.c.heads : w, isv, by_token);
     } else {
-        append_queries<D, B, T>(a, (int)q * qtokens, qtokens, qot);
+        append_queries<D, B, TREE, T>(a, (int)q * qtokens, qtokens, qot);
     }
 }
 
@@ -500,8 +504,9 @@ cudaError_t launch_append(mmq_dtype t, mmq_dtype qot, const AppendArgs& a, cudaS
     // the queries' blocks for every 2^32 of the grid, rounded up: the last block's number comes out exactly
     const unsigned share = (unsigned)((((grid - kv) << 32) + grid - 1) / grid);
     return with_type(t, [&](auto ti) {
-        return launch_pdl(append_kernel<D, B, decltype(ti)>, dim3((unsigned)grid), dim3(S::kThreads), s, a, share,
-                          by_token, qtokens, (int)qot);
+        using T = decltype(ti);
+        return launch_pdl(a.depths ? append_kernel<D, B, true, T> : append_kernel<D, B, false, T>, dim3((unsigned)grid),
+                          dim3(S::kThreads), s, a, share, by_token, qtokens, (int)qot);
     });
 }
 
