@@ -210,18 +210,23 @@ AttnArgs attention_args(const mmq_heads* q, int n_heads, const mmq_kv_cache* cac
 
 }  // namespace
 
-// Which kernel a tree's rows take (microseconds below: 8 key/value heads of 128 unless stated, bounds that hold).
+// Which kernel a tree's rows take.  Microseconds below: a captured call from a cold L2, 32 query and 8 key/value heads of 128
+// unless stated, bounds that hold; "one of 2000" is one sequence of 2000 cached tokens.
 // FEW, the few-row kernel: for 16 rows (32 of head_dim 64), of which tiles of 64 would leave most empty, and for small problems,
 //   whose blocks start and end sooner, 16 rows at a time, each reading the cache again.
-//   16 rows, few / tiles: 64 sequences of 2000: 89 / 108; 16 of 8192: 85 / 86; 32 heads of 64, 16 of 2000: 55 / 85
-//   (32 rows: 79 / 91); 4 heads of 256, 16 of 4000: 60 / 58.  More rows, few / tiled, by the bytes of K that are read: 8 MB (one
-//   of 2000, 64 rows) 20 / 24, 8 MB (4 of 1000, 32 rows) 26 / 28, 17 MB (16 of 500, 32 rows) 30 / 22, 17 MB (one of 2000, 128
-//   rows) 28 / 24.
+//   16 rows, few / tiles: one of 2000, 8000, 32000, 131072: 17 / 26, 22 / 30, 31 / 41, 90 / 83; 64 of 500: 36 / 54; 64 of
+//   2000: 87 / 110; 16 of 3000: 48 / 48; 16 of 8192: 85 / 84; 32 heads of 64, 16 of 2000: 56 / 87 (32 rows: 79 / 91); 4 heads
+//   of 256, 16 of 4000: 61 / 56.  Where it loses most, few / tiled: 16 of 500: 30 / 22; 16 of 1000: 34 / 30.
+//   More rows, few / tiled, by the bytes of K that are read: 4 MB (one of 2000, 32 rows) 18 / 24; 8 MB (one of 2000, 64 rows)
+//   20 / 24, (4 of 1000, 32 rows) 26 / 28; 16 MB (one of 8000, 32 rows) 24 / 26, (one of 4000, 64 rows) 22 / 25, (one of 2000,
+//   128 rows) 28 / 26, (4 of 1000, 64 rows) 30 / 28, (16 of 500, 32 rows) 30 / 22.
 // TILED, the kernel of prompts: 256 rows (head_dim 256: 128) that share the converted codes.
 // TILES, the tree kernel: tiles of 64 or 128 rows in equal shares, which wins where they fill the card.  Tiles / tiled, by the
-//   bytes of K, up to 64 rows: 17 MB (16 of 1000) 36 / 29, 34 MB (64 of 500) 69 / 72, 50 MB (16 of 3000) 52 / 57, 135 MB (16 of
-//   8192) 95 / 126; up to 128: 34 MB (64 of 500) 81 / 73, 50 MB (16 of 3000) 65 / 59, 70 MB (32 heads of 64, 16 of 2000) 121 / 132,
-//   135 MB (64 of 2000) 142 / 149.  With two blocks of 128 (16 of 8192, 192 rows) 201 / 134.
+//   bytes of K, up to 64 rows: 17 MB (16 of 1000) 34 / 30, (one of 16000) 36 / 32; 33 MB (64 of 500) 67 / 71, (one of 32000)
+//   44 / 44, (4 of 8192) 40 / 48; 50 MB (16 of 3000) 54 / 56; 134 MB (16 of 8192) 93 / 127, (one of 131072) 91 / 114.  Up to
+//   128: 33 MB (64 of 500) 83 / 73, (4 of 8192) 48 / 46; 50 MB (16 of 3000) 68 / 58; 74 MB (32 heads of 64, 16 of 2000)
+//   122 / 132; 135 MB (64 of 2000) 147 / 149, (16 of 8192) 123 / 128, (one of 131072) 120 / 115.
+// The bounds decide, which the workspace's size follows from; a window, which that size is not asked with, has no say.
 TreeKernel tree_kernel(int group, int kv_heads, int dim, int seqs, long long max_tokens, long long max_kv) {
     const long long rows = max_tokens * group;
     const double bytes = (double)seqs * kv_heads * (max_kv + max_tokens) * dim;

@@ -23,8 +23,8 @@
 // Bound by the latencies between the roles and, next, by instructions: a tile of 128 tokens of heads of 128 takes a block 1170 ns
 // with 64 rows, where its codes take 737 at the rate of a plain copy; the converters alone take 896, the softmax alone 804, the
 // products alone 550.  With 128 rows: 1573; 1318, 1096, 657.  Some 15 us of a call are its start, the first codes and the join.
-// 16 sequences of 8192 tokens, 32 query and 8 key/value heads of 128: 85 us with 32 rows (3.2 TB/s), 91 with 64, 120 with 128
-// (0.55 PFLOP/s); one of 131072, 64 rows, 89; 4 key/value heads of 256, 16 of 4000, 64 rows, 58.
+// 16 sequences of 8192 tokens, 32 query and 8 key/value heads of 128: 85 us with 32 rows (3.2 TB/s), 92 with 64, 123 with 128
+// (0.56 PFLOP/s); one of 131072, 64 rows, 90; 4 key/value heads of 256, 16 of 4000, 64 rows, 58.
 // Slower: six warps for V (64 rows: 93 -> 102), eleven of fewer registers (96), eight for K (95).  Without any load of codes it
 // would take 89 instead of 91: what is left is between the conversion, the softmax and the products, not memory.
 #include <algorithm>
@@ -59,8 +59,9 @@ template <int D, int R> struct Tree {
     static constexpr int kGroups = R / N, kSoftmaxWarps = 4 * kGroups, kWarpsV = R == 128 ? 3 : 7;
     static constexpr int kWarpK = kSoftmaxWarps, kWarpV = kWarpK + 4, kWarpMma = kWarpV + kWarpsV, kWarps = kWarpMma + 1;
     static constexpr int kThreads = kWarps * 32;
-    // Units that a converter warp has on their way to L2 besides those in its registers: 16 sequences of 8192, 32 rows, take 89 us
-    // with one, 87 with two, 91 with three; with 128 rows, where fewer registers are left, 122, 130 and 142.
+    // Units that a converter warp has on their way to L2 besides those in its registers, one, two, three: 16 sequences of 8192, 32
+    // rows, 83, 85, 88 us, 64 rows 91, 91, 95; 32 heads of 64, 16 of 2000, 64 rows, 99, 97, 97; heads of 256 61, 58, 60; with
+    // 128 rows, where fewer registers are left, 123, 134 and 142.
     static constexpr int kAhead = R == 64 ? 2 : 1;
     // registers a thread: 20 warps have 96; of 24 each gets 80 at launch, some of which move to the softmax warps
     static constexpr int kRegsSoftmax = 88, kRegsRest = 64;
@@ -70,12 +71,14 @@ template <int D, int R> struct Tree {
     static constexpr int kVBytes = KT * D * 2, kQBytes = R * D * 2, kPBytes = KT * R * 2;
     static constexpr int kScaleSlots = 16;
     static constexpr int kKCols = D / 2;
-    // Tiles of K and V that the converters may be ahead (16 sequences of 8192, 64 rows: four of V 94 us, three 91, two 91, two of
-    // each 93; 32 heads of 64, 16 of 2000, 64 rows: four 97, three 101; 64 sequences of 2000, 32 rows: 113, 115, 115, 118).
+    // Tiles of K and V that the converters may be ahead, three of V, two, two of each: 16 sequences of 8192, 32 rows, 85, 87, 86 us,
+    // 64 rows 92, 93, 93, 128 rows 123, 120, 120; 64 sequences of 2000, 32 rows: 116, 120, 118.  32 heads of 64, 16 of 2000, 64
+    // rows, four of V 97, three 101.
     static constexpr int kKStages = D == 64 ? 4 : (R == 64 && D == 128 ? 4 : 2);
     static constexpr int kVStages = D == 64 ? 4 : (D == 128 ? 3 : 2);
     // Buffers of S and of P.  With two, S of a tile waits for the softmax two tiles before, and then for the products in
-    // between (19 sequences of 8192, 64 rows: 104 us with two, 101 with three).
+    // between (two, three: 64 sequences of 2000, 32 rows, 120 and 116 us; 32 heads of 64, 16 of 2000, 64 rows, 101 and 97; 16
+    // sequences of 8192, 64 rows, 93 and 92).
     static constexpr int kBufs = R == 64 && D <= 128 ? 3 : 2;
     // TMEM columns: S, O, K
     static constexpr int kOCol = kBufs * R, kKCol = kOCol + kHalves * R;
@@ -222,7 +225,7 @@ template <int D, int R> struct TreeBars {
 
 // What a unit costs besides its tiles, in tiles: its queries, its result, and the pipeline in between.  In the line it stands
 // before them, or a block whose share lies among short sequences would be the last by far: 24 sequences of up to 8192 tokens,
-// 64 rows, take 147 us with 0, 97 with 4, 91 with 5, 89 with 8; 16 of 8192 each, 32 rows, 91, 89, 87 and 91.
+// 64 rows, take 138 us with 0, 91 with 4, 87 with 5, 87 with 8; 16 of 8192 each, 32 rows, 86, 86, 85 and 88.
 constexpr int EXTRA = 5;
 
 // A sequence's place in the line of tiles.
@@ -523,6 +526,10 @@ __global__ void __launch_bounds__(Tree<D, R>::kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < 2; g++) from[g] = codes + (long long)place[0][g] * (16 * D) + 128 * strip;
                 };
+                // A barrier shows a phase's parity only, so a warp must not be two phases off.  It is not lapped, since its own
+                // unit completes the tile; and as stages are released in the order of the tiles, the wait for its unit before,
+                // at most a lap of stages back, shows that the phase before this one is complete.
+                static_assert((TURN + 4 * STRIPS - 1) / (4 * STRIPS) <= (isv ? C::kVStages : C::kKStages), "units too far apart");
                 uint4 r[2][2][CU];
 #pragma unroll 1
                 for (int u = 0; u < AHEAD; u++) step(u);
