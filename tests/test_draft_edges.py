@@ -206,3 +206,39 @@ def test_tokens_past_the_stated_length_are_skipped(S, n, H, D, takes, bound):
             wlse[i * n:i * n + n, h], want[i * n:i * n + n, h] = torch.logsumexp(s, -1), torch.softmax(s, -1) @ v[:, h // 4]
     assert_close(out, want[rows], torch.full_like(want[rows], vmax * (2.0 ** -11 + 2.0 ** -16 + ULP[torch.float32])))
     assert ((lse.double().cpu() - wlse[rows]).abs() <= 2.0 ** -18 + 2.0 ** -20 * wlse[rows].abs()).all()
+
+
+# ------------------------------------------------------------------------------------------------ large caches
+@gpu
+@pytest.mark.parametrize("D,page,block", [(64, 16, 16), (128, 64, 16), (256, 64, 32)])
+def test_caches_past_32_bits_of_bytes(D, page, block):
+    """The same pages at the end of a cache of 4.3 GB of codes a side: every operator does what it does with them in a small one."""
+    g = torch.Generator().manual_seed(D)
+    H, n, lens = 2, [40, 3, 12], [700, 300, 1500]
+    small, table = make_cache(g, lens, H, D, page, block)
+    pages = (1 << 32) // (H * page * D) + 2 * small.pages
+    big = api.KVCache(*(torch.empty((pages,) + x.shape[1:], dtype=x.dtype, device="cuda")
+                        for x in (small.k, small.v, small.k_scale, small.v_scale)))
+    shift = pages - small.pages
+    for name in ("k", "v", "k_scale", "v_scale"):
+        getattr(big, name)[shift:] = getattr(small, name)
+    cu, kv, tree = offsets(n).cuda(), T.i32(lens), T.make_tree([T.draw_parents(k, g) for k in n], n)
+    rows = torch.randn(sum(n), 8 + 2 * H, D, generator=g).bfloat16().cuda()
+    cos, sin = (t.cuda() for t in rotary_tables(max(lens), D))
+    got = []
+    api.read_device_errors()
+    for cache, tb in ((small, table), (big, torch.where(table >= 0, table + shift, table))):
+        tb, out = tb.cuda(), []
+        q = api.kv_append(cache, rows[:, 8:8 + H], rows[:, 8 + H:], tb, kv, cu, cos, sin, q=rows[:, :8], tree=tree)
+        out.append(q)
+        for some, takes in ((slice(0, 3), TILED), (slice(1, 3), TILES), (slice(1, 2), FEW)):
+            at, m = slice(int(cu[some.start]), int(cu[some.stop])), max(n[some])
+            assert kernel(4, H, D, len(n[some]), m, LOOSE) == takes
+            out += api.attention(q[at], cache, tb[some].clone(), kv[some].clone(), LOOSE, cu[some.start:some.stop + 1] - cu[some.start],
+                                 m, return_lse=True, tree=api.DraftTree(tree.depths[at].clone(), tree.masks[at].clone()))
+        api.kv_keep(cache, tb, kv, sum(n), T.i32([[0, 5, 9, 31], [1, 2, 0, 0], [0, 1, 7, 11]]), T.i32([4, 2, 4]), cu)
+        left = [a - b + c for a, b, c in zip(lens, n, (4, 2, 4))]
+        out += api.kv_read(cache, tb, T.i32(left), sum(left), offsets(left).cuda(), torch.float32)
+        got.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert api.read_device_errors() == 0
